@@ -360,6 +360,126 @@ muon_status muon_probe_copy_lds(const void* src, void* dst, size_t bytes, void* 
 typedef enum { MUON_COEFF_QUINTIC = 0, MUON_COEFF_HYBRID = 1 } muon_coeff_kind;
 muon_status muon_ns_coefficients(int32_t kind, int32_t steps, float* out, size_t cap);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the step: what makes the gradients muon_step reads.
+ *
+ * Norms give the gradients of a table's AdamW vectors (layer norm weights and
+ * biases, RMS norm weights); the linear layer on 8-bit rows gives those of
+ * its Muon matrices from activations that were kept in 8 bits.  They follow
+ * the conventions above; in addition
+ *   - matrices take a leading dimension (elements between rows) of at least
+ *     their column count; only the rows x cols values are read or written
+ *     unless a comment says otherwise;
+ *   - dtype codes are muon_dtype; sums, statistics and products are held in
+ *     32 bits and rounded once on output;
+ *   - an output must not overlap an input, except where said;
+ *   - results do not depend on the stream, on other calls or on timing: sums
+ *     are joined in a fixed order.
+ * ------------------------------------------------------------------------- */
+
+/* 8-bit rows: a rows x cols matrix held as int8 q (leading dimension ldq) and
+ * one fp32 scale per row, standing for q[i][j] * scale[i].
+ *   scale[i] = 2^e, e the smallest integer with max_j |x[i][j]| <= 127 * 2^e,
+ *              not below -126 (an all-zero row has 2^-126);
+ *   q[i][j]  = x[i][j] / scale[i] rounded to nearest even, in [-127, 127]
+ *              (in [-63, 63] where e is 122, its largest value, so that every
+ *              q * scale is finite).
+ * A row that holds a NaN or an infinity gets scale NaN and q = 0, so whatever
+ * is computed from it is NaN.  A power of two costs up to one of the 8 bits
+ * against max / 127 and makes q * scale exact in bf16, so restoring a row and
+ * feeding it to bf16 matrix instructions rounds nothing.
+ * Storage: q is 16-byte aligned, ldq is a multiple of 16, every row's ldq
+ * bytes belong to the buffer, and the bytes from cols up to the next
+ * multiple of 16 are zero.  muon_rows8_quantize and muon_norm_forward write
+ * those zeros; the bytes behind them are left as they are. */
+muon_status muon_rows8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t dtype,
+                                int8_t* q, int64_t ldq, float* scale, void* stream);
+/* y[i][j] = q[i][j] * scale[i] (y may be bf16 or fp32; exact for the scales
+ * muon_rows8_quantize writes, apart from bf16's range at its far ends).
+ * Errors of both: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30,
+ * a leading dimension below cols or above 2^40, ldq not a multiple of 16);
+ * MUON_E_ARG (a pointer null or not aligned: x and y to their element, q to
+ * 16 bytes, scale to 4); MUON_E_HIP. */
+muon_status muon_rows8_dequantize(const int8_t* q, int64_t ldq, const float* scale, int64_t rows, int64_t cols,
+                                  void* y, int64_t ldy, int32_t dtype, void* stream);
+
+/* Row norms.  Per row x of cols values (all rows independent):
+ *   mu = mean(x) (MUON_NORM_LAYER) or 0 (MUON_NORM_RMS)
+ *   r  = 1 / sqrt(mean((x - mu)^2) + eps),  h = (x - mu) r
+ *   y  = h gamma + beta */
+typedef enum { MUON_NORM_LAYER = 0, MUON_NORM_RMS = 1 } muon_norm_kind;
+
+/* x: rows x cols, dtype.  gamma, beta: cols values of vec_dtype; beta may be
+ * NULL.  Outputs, each optional, at least one given:
+ *   y (dtype, ldy); may be x itself (with ldy == ldx)
+ *   q, ldq, scale: y, before any rounding to dtype, as 8-bit rows (both or neither)
+ *   mean, rstd: rows fp32 values of mu and r, for the backward pass (mean must
+ *     be NULL for MUON_NORM_RMS).
+ * Errors: MUON_E_METHOD (unknown kind), MUON_E_DTYPE, MUON_E_SHAPE (as for
+ * muon_rows8_quantize), MUON_E_ARG (a required pointer null, any pointer
+ * misaligned, eps negative or not finite, no output), MUON_E_HIP. */
+muon_status muon_norm_forward(int32_t kind, const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t dtype,
+                              const void* gamma, const void* beta, int32_t vec_dtype, float eps, void* y,
+                              int64_t ldy, int8_t* q, int64_t ldq, float* scale, float* mean, float* rstd,
+                              void* stream);
+
+/* Gradients of muon_norm_forward, with g = dy gamma and the saved mean, rstd:
+ *   dx     = r (g - mean(g) - h mean(g h))   (MUON_NORM_RMS: without mean(g))
+ *   dgamma = sum over rows of dy h,  dbeta = sum over rows of dy
+ * dy, x, dx: rows x cols, dtype; dx may be dy itself (with lddx == lddy).
+ * dgamma, dbeta (cols values of vec_dtype, each may be NULL) are overwritten,
+ * or added to when accumulate is nonzero; with rows == 0 the sums are zero.
+ * mean: NULL for MUON_NORM_RMS.  workspace: muon_norm_backward_workspace_bytes
+ * bytes (needed only if dgamma or dbeta is given).  Errors as for
+ * muon_norm_forward, and MUON_E_WORKSPACE. */
+muon_status muon_norm_backward(int32_t kind, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                               int64_t rows, int64_t cols, int32_t dtype, const void* gamma, int32_t vec_dtype,
+                               const float* mean, const float* rstd, void* dx, int64_t lddx, void* dgamma,
+                               void* dbeta, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                               void* stream);
+muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes);
+
+/* A linear layer y = x W^T + bias on 8-bit rows: x as tokens x in rows (q,
+ * scale per token), W as out x in rows (wq, wscale per output channel).
+ * The products of 8-bit values are summed exactly in 32-bit integers, hence
+ * in <= 131071.  y: tokens x out of dtype; bias: out values of bias_dtype, or
+ * NULL.  The gradients are those of this layer with the rounding to 8 bits
+ * taken as the identity:
+ *   dW[n][k] = sum_t dy[t][n] scale[t] q[t][k]     out x in, dw_dtype; written,
+ *              or added to dw when accumulate is nonzero
+ *   dX[t][k] = sum_n dy[t][n] wscale[n] wq[n][k]   tokens x in, dx_dtype
+ * dy: tokens x out, bf16 or fp32.  q * scale enters the gradient products in
+ * bf16: exact for powers of two, rounded once for other scales.  fp32 dy is
+ * taken as three bf16 pieces that add up to it, so it loses nothing.
+ * With tokens == 0 the weight gradient is zero; with out == 0 the input
+ * gradient is; with in == 0 y is the bias.
+ * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, in above
+ * 131071 for the forward product, a leading dimension below its column count
+ * or above 2^21, ldq or ldw not a multiple of 16); MUON_E_ARG (a pointer null
+ * or misaligned: 8-bit rows to 16 bytes, others to their element);
+ * MUON_E_WORKSPACE (workspace smaller than muon_linear8_workspace_bytes);
+ * MUON_E_HIP. */
+typedef enum {
+  MUON_LINEAR8_FORWARD = 0,
+  MUON_LINEAR8_WEIGHT_GRAD = 1,
+  MUON_LINEAR8_INPUT_GRAD = 2
+} muon_linear8_pass;
+muon_status muon_linear8_forward(const int8_t* q, int64_t ldq, const float* scale, const int8_t* wq, int64_t ldw,
+                                 const float* wscale, const void* bias, int32_t bias_dtype, int64_t tokens,
+                                 int64_t out, int64_t in, void* y, int64_t ldy, int32_t dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+muon_status muon_linear8_weight_grad(const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* q, int64_t ldq,
+                                     const float* scale, int64_t tokens, int64_t out, int64_t in, void* dw,
+                                     int64_t lddw, int32_t dw_dtype, int32_t accumulate, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+muon_status muon_linear8_input_grad(const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* wq, int64_t ldw,
+                                    const float* wscale, int64_t tokens, int64_t out, int64_t in, void* dx,
+                                    int64_t lddx, int32_t dx_dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+/* Bytes of workspace of one pass (muon_linear8_pass), host only; 0 for many
+ * sizes.  Errors: MUON_E_METHOD (unknown pass), MUON_E_SHAPE, MUON_E_ARG. */
+muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t out, int64_t in, size_t* bytes);
+
 /* Static text for a status code. */
 const char* muon_status_string(int32_t status);
 

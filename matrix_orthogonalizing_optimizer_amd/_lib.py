@@ -23,12 +23,17 @@ MUON_F32, MUON_BF16 = 0, 1
 MUON_KIND_MUON, MUON_KIND_ADAMW = 0, 1
 MUON_SCALE_MOONLIGHT, MUON_SCALE_SPECTRAL, MUON_SCALE_UNIT_RMS = 0, 1, 2
 MUON_COEFF_QUINTIC, MUON_COEFF_HYBRID = 0, 1
+MUON_NORM_LAYER, MUON_NORM_RMS = 0, 1
+MUON_LINEAR8_FORWARD, MUON_LINEAR8_WEIGHT_GRAD, MUON_LINEAR8_INPUT_GRAD = 0, 1, 2
 
 EXPORTED = ["muon_plan_create", "muon_plan_destroy", "muon_plan_workspace_bytes",
             "muon_plan_buckets", "muon_plan_units", "muon_step", "ns_orthogonalize",
             "ns_orthogonalize_workspace_bytes", "muon_timing_enable", "muon_timing_collect",
             "muon_ns_coefficients", "muon_status_string", "muon_version", "muon_probe_mfma",
-            "muon_probe_copy", "ns_orthogonalize_noalloc", "muon_probe_copy_lds"]
+            "muon_probe_copy", "ns_orthogonalize_noalloc", "muon_probe_copy_lds",
+            "muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
+            "muon_norm_backward_workspace_bytes", "muon_linear8_forward", "muon_linear8_weight_grad",
+            "muon_linear8_input_grad", "muon_linear8_workspace_bytes"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -113,6 +118,21 @@ def lib():
     L.muon_probe_copy.restype = i32
     L.muon_probe_copy_lds.argtypes = [vp, vp, ctypes.c_size_t, vp]
     L.muon_probe_copy_lds.restype = i32
+    f32 = ctypes.c_float
+    L.muon_rows8_quantize.argtypes = [vp, i64, i64, i64, i32, vp, i64, vp, vp]
+    L.muon_rows8_dequantize.argtypes = [vp, i64, vp, i64, i64, vp, i64, i32, vp]
+    L.muon_norm_forward.argtypes = [i32, vp, i64, i64, i64, i32, vp, vp, i32, f32, vp, i64, vp, i64, vp, vp, vp, vp]
+    L.muon_norm_backward.argtypes = [i32, vp, i64, vp, i64, i64, i64, i32, vp, i32, vp, vp, vp, i64, vp, vp, i32,
+                                     vp, sz, vp]
+    L.muon_norm_backward_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.muon_linear8_forward.argtypes = [vp, i64, vp, vp, i64, vp, vp, i32, i64, i64, i64, vp, i64, i32, vp, sz, vp]
+    L.muon_linear8_weight_grad.argtypes = [vp, i64, i32, vp, i64, vp, i64, i64, i64, vp, i64, i32, i32, vp, sz, vp]
+    L.muon_linear8_input_grad.argtypes = [vp, i64, i32, vp, i64, vp, i64, i64, i64, vp, i64, i32, vp, sz, vp]
+    L.muon_linear8_workspace_bytes.argtypes = [i32, i64, i64, i64, ctypes.POINTER(sz)]
+    for n in ("muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
+              "muon_norm_backward_workspace_bytes", "muon_linear8_forward", "muon_linear8_weight_grad",
+              "muon_linear8_input_grad", "muon_linear8_workspace_bytes"):
+        getattr(L, n).restype = i32
     L.muon_ns_coefficients.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_float), sz]
     L.muon_ns_coefficients.restype = i32
     L.muon_status_string.argtypes = [i32]
@@ -438,3 +458,294 @@ def muon_ns_coefficients(kind: int, steps: int):
 
 def muon_version() -> int:
     return lib().muon_version()
+
+
+# ---------------------------------------------------------------------------
+# Operators around the step: norms, 8-bit rows, the linear layer on 8-bit rows
+
+def _matrix(name, t):
+    """(rows, cols, ld, dtype code) of a 2-D tensor with unit column stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+    ld = t.stride(0) if rows > 1 else cols
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld} for {cols} columns)")
+    return rows, cols, ld, _dtype_code(name, t)
+
+
+def _dtype_code(name, t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return MUON_BF16
+    if t.dtype == torch.float32:
+        return MUON_F32
+    raise ValueError(f"{name}: must be float32 or bfloat16, got {t.dtype}")
+
+
+def _rows8(name, q, scale, shape=None):
+    """(rows, cols, ldq) of 8-bit rows and their scales: int8, rows a multiple
+    of 16 bytes apart, every row's bytes up to the next one in the storage."""
+    import torch
+    if q.dtype != torch.int8 or q.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D int8 tensor, got {q.dtype} {tuple(q.shape)}")
+    rows, cols = q.shape
+    if shape is not None and (rows, cols) != tuple(shape):
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {(rows, cols)}")
+    if cols > 1 and rows > 0 and q.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+    ld = q.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    if rows > 0 and cols > 0:
+        if ld % 16 or ld < cols or q.data_ptr() % 16:
+            raise ValueError(f"{name}: rows must start 16-byte aligned and lie a multiple of 16 bytes apart")
+        if q.untyped_storage().nbytes() - q.storage_offset() < rows * ld:
+            raise ValueError(f"{name}: the storage ends before the last row's {ld} bytes")
+    else:
+        ld = (cols + 15) // 16 * 16
+    _vector(f"scale of {name}", scale, rows, torch.float32)
+    return rows, cols, ld
+
+
+def _vector(name, t, n, dtype=None):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
+
+
+def _call_device(stream, **tensors):
+    """Every tensor of a call lives on the GPU its kernels run on; returns
+    that GPU's index."""
+    di = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a {t.device} tensor; the library needs device memory")
+        if di is None:
+            di = _device_index(stream)
+        if t.device.index != di:
+            raise ValueError(f"{name}: on {t.device}, the kernels run on cuda:{di}")
+    return di
+
+
+class _On:
+    """Allocates and launches on the call's GPU and stream: a buffer made
+    here belongs to the stream that uses it, so the allocator does not hand
+    it on while the call's kernels still run."""
+
+    def __init__(self, di, stream):
+        self.di, self.stream = di, stream
+
+    def empty(self, *shape, dtype):
+        import torch
+        dev = torch.device("cuda", self.di)
+        if self.stream is None:
+            return torch.empty(*shape, dtype=dtype, device=dev)
+        s = self.stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, device=dev) if s else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(s):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+    def rows8(self, rows, cols):
+        import torch
+        return (self.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8)[:, :cols],
+                self.empty(rows, dtype=torch.float32))
+
+    def call(self, fn, *args):
+        import torch
+        f = getattr(lib(), fn)
+        if self.di == torch.cuda.current_device():
+            st = f(*args, _stream(self.stream))
+        else:
+            with torch.cuda.device(self.di):
+                st = f(*args, _stream(self.stream))
+        _check(fn, st)
+
+
+def _scratch(on, workspace, nbytes):
+    """(tensor kept alive, pointer, bytes) of a call's workspace."""
+    import torch
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = on.empty(nbytes, dtype=torch.uint8)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def muon_rows8_quantize(x, q=None, scale=None, stream=None):
+    """(q, scale): the 8-bit rows of x (2-D, fp32 or bf16, rows may be
+    strided).  q: int8, x's shape, rows a multiple of 16 bytes apart (None:
+    allocated so); scale: fp32, one per row, a power of two."""
+    rows, cols, ldx, dt = _matrix("x", x)
+    if (q is None) != (scale is None):
+        raise ValueError("q and scale: give both or neither")
+    on = _On(_call_device(stream, x=x, q=q, scale=scale), stream)
+    if q is None:
+        q, scale = on.rows8(rows, cols)
+    _, _, ldq = _rows8("q", q, scale, (rows, cols))
+    on.call("muon_rows8_quantize", x.data_ptr(), rows, cols, ldx, dt, q.data_ptr(), ldq, scale.data_ptr())
+    return q, scale
+
+
+def muon_rows8_dequantize(q, scale, out=None, dtype=None, stream=None):
+    """The matrix that 8-bit rows stand for, q * scale per row, as ``out``
+    (2-D, fp32 or bf16) or a new tensor of ``dtype`` (default bfloat16)."""
+    import torch
+    rows, cols, ldq = _rows8("q", q, scale)
+    on = _On(_call_device(stream, q=q, scale=scale, out=out), stream)
+    if out is None:
+        out = on.empty(rows, cols, dtype=dtype or torch.bfloat16)
+    r, c, ldy, dt = _matrix("out", out)
+    if (r, c) != (rows, cols):
+        raise ValueError(f"out: expected {(rows, cols)}, got {(r, c)}")
+    on.call("muon_rows8_dequantize", q.data_ptr(), ldq, scale.data_ptr(), rows, cols, out.data_ptr(), ldy, dt)
+    return out
+
+
+def muon_norm_forward(x, gamma, beta=None, eps=1e-5, kind=MUON_NORM_LAYER, y=None, q=None, scale=None, mean=None,
+                      rstd=None, stream=None) -> None:
+    """Layer norm (or RMS norm) of the rows of x into the buffers given, any
+    of: y (x's dtype; may be x), q and scale (8-bit rows, see
+    muon_rows8_quantize), mean and rstd (fp32, one per row, what
+    muon_norm_backward takes; no mean for MUON_NORM_RMS)."""
+    import torch
+    rows, cols, ldx, dt = _matrix("x", x)
+    _vector("gamma", gamma, cols)
+    vdt = _dtype_code("gamma", gamma)
+    if beta is not None:
+        _vector("beta", beta, cols, gamma.dtype)
+    ldy = ldq = 0
+    if y is not None:
+        r, c, ldy, ydt = _matrix("y", y)
+        if (r, c) != (rows, cols) or ydt != dt:
+            raise ValueError(f"y: expected {(rows, cols)} of {x.dtype}, got {(r, c)} of {y.dtype}")
+    if (q is None) != (scale is None):
+        raise ValueError("q and scale: give both or neither")
+    if q is not None:
+        _, _, ldq = _rows8("q", q, scale, (rows, cols))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _vector(name, t, rows, torch.float32)
+    on = _On(_call_device(stream, x=x, gamma=gamma, beta=beta, y=y, q=q, scale=scale, mean=mean, rstd=rstd), stream)
+    on.call("muon_norm_forward", kind, x.data_ptr(), rows, cols, ldx, dt, gamma.data_ptr(), _ptr(beta), vdt, eps,
+            _ptr(y), ldy, _ptr(q), ldq, _ptr(scale), _ptr(mean), _ptr(rstd))
+
+
+def muon_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    b = ctypes.c_size_t()
+    _check("muon_norm_backward_workspace_bytes",
+           lib().muon_norm_backward_workspace_bytes(rows, cols, ctypes.byref(b)))
+    return b.value
+
+
+def muon_norm_backward(dy, x, gamma, mean, rstd, kind=MUON_NORM_LAYER, dx=None, dgamma=None, dbeta=None,
+                       accumulate=False, workspace=None, stream=None):
+    """Gradients of muon_norm_forward: writes dx (allocated if None, may be
+    dy) and returns it; dgamma and dbeta (gamma's dtype) are written where
+    given, or added to with accumulate.  mean: None for MUON_NORM_RMS."""
+    import torch
+    rows, cols, lddy, dt = _matrix("dy", dy)
+    r, c, ldx, xdt = _matrix("x", x)
+    if (r, c) != (rows, cols) or xdt != dt:
+        raise ValueError(f"x: expected {(rows, cols)} of {dy.dtype}, got {(r, c)} of {x.dtype}")
+    _vector("gamma", gamma, cols)
+    vdt = _dtype_code("gamma", gamma)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _vector(name, t, rows, torch.float32)
+    for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
+        if t is not None:
+            _vector(name, t, cols, gamma.dtype)
+    on = _On(_call_device(stream, dy=dy, x=x, gamma=gamma, mean=mean, rstd=rstd, dx=dx, dgamma=dgamma, dbeta=dbeta,
+                          workspace=workspace), stream)
+    if dx is None:
+        dx = on.empty(rows, cols, dtype=dy.dtype)
+    r, c, lddx, ddt = _matrix("dx", dx)
+    if (r, c) != (rows, cols) or ddt != dt:
+        raise ValueError(f"dx: expected {(rows, cols)} of {dy.dtype}, got {(r, c)} of {dx.dtype}")
+    nb = muon_norm_backward_workspace_bytes(rows, cols) if dgamma is not None or dbeta is not None else 0
+    workspace, wp, wsz = _scratch(on, workspace, nb)
+    on.call("muon_norm_backward", kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, dt, gamma.data_ptr(), vdt,
+            _ptr(mean), _ptr(rstd), dx.data_ptr(), lddx, _ptr(dgamma), _ptr(dbeta), 1 if accumulate else 0, wp, wsz)
+    return dx
+
+
+def muon_linear8_workspace_bytes(kind: int, tokens: int, out: int, in_: int) -> int:
+    """Workspace of one pass (MUON_LINEAR8_FORWARD, _WEIGHT_GRAD, _INPUT_GRAD)."""
+    b = ctypes.c_size_t()
+    _check("muon_linear8_workspace_bytes",
+           lib().muon_linear8_workspace_bytes(kind, tokens, out, in_, ctypes.byref(b)))
+    return b.value
+
+
+def muon_linear8_forward(q, scale, wq, wscale, bias=None, y=None, dtype=None, workspace=None, stream=None):
+    """y = x W^T + bias on 8-bit rows: x as (q, scale) per token, W (out x in)
+    as (wq, wscale) per output channel.  y: tokens x out, fp32 or bf16 (None:
+    allocated, of ``dtype``, default bfloat16); returned."""
+    import torch
+    tokens, in_, ldq = _rows8("q", q, scale)
+    out, win, ldw = _rows8("wq", wq, wscale)
+    if win != in_:
+        raise ValueError(f"wq: expected {in_} columns, got {win}")
+    bdt = 0
+    if bias is not None:
+        _vector("bias", bias, out)
+        bdt = _dtype_code("bias", bias)
+    on = _On(_call_device(stream, q=q, scale=scale, wq=wq, wscale=wscale, bias=bias, y=y, workspace=workspace), stream)
+    if y is None:
+        y = on.empty(tokens, out, dtype=dtype or torch.bfloat16)
+    r, c, ldy, dt = _matrix("y", y)
+    if (r, c) != (tokens, out):
+        raise ValueError(f"y: expected {(tokens, out)}, got {(r, c)}")
+    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_FORWARD, tokens, out, in_)
+    workspace, wp, wsz = _scratch(on, workspace, nb)
+    on.call("muon_linear8_forward", q.data_ptr(), ldq, scale.data_ptr(), wq.data_ptr(), ldw, wscale.data_ptr(),
+            _ptr(bias), bdt, tokens, out, in_, y.data_ptr(), ldy, dt, wp, wsz)
+    return y
+
+
+def muon_linear8_weight_grad(dy, q, scale, dw=None, dtype=None, accumulate=False, workspace=None, stream=None):
+    """dW = dy^T x (out x in) from the kept 8-bit rows (q, scale) of x: the
+    gradient muon_step reads.  dw: written, or added to with accumulate
+    (None: allocated, of ``dtype``, default dy's); returned."""
+    tokens, out, lddy, dydt = _matrix("dy", dy)
+    rows, in_, ldq = _rows8("q", q, scale)
+    if rows != tokens:
+        raise ValueError(f"q: {rows} rows for {tokens} tokens")
+    on = _On(_call_device(stream, dy=dy, q=q, scale=scale, dw=dw, workspace=workspace), stream)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw")
+        dw = on.empty(out, in_, dtype=dtype or dy.dtype)
+    r, c, lddw, dt = _matrix("dw", dw)
+    if (r, c) != (out, in_):
+        raise ValueError(f"dw: expected {(out, in_)}, got {(r, c)}")
+    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_WEIGHT_GRAD, tokens, out, in_)
+    workspace, wp, wsz = _scratch(on, workspace, nb)
+    on.call("muon_linear8_weight_grad", dy.data_ptr(), lddy, dydt, q.data_ptr(), ldq, scale.data_ptr(), tokens, out,
+            in_, dw.data_ptr(), lddw, dt, 1 if accumulate else 0, wp, wsz)
+    return dw
+
+
+def muon_linear8_input_grad(dy, wq, wscale, dx=None, dtype=None, workspace=None, stream=None):
+    """dX = dy W (tokens x in) with W as 8-bit rows (wq, wscale).  dx: None:
+    allocated, of ``dtype``, default dy's; returned."""
+    tokens, out, lddy, dydt = _matrix("dy", dy)
+    rows, in_, ldw = _rows8("wq", wq, wscale)
+    if rows != out:
+        raise ValueError(f"wq: {rows} rows for {out} columns of dy")
+    on = _On(_call_device(stream, dy=dy, wq=wq, wscale=wscale, dx=dx, workspace=workspace), stream)
+    if dx is None:
+        dx = on.empty(tokens, in_, dtype=dtype or dy.dtype)
+    r, c, lddx, dt = _matrix("dx", dx)
+    if (r, c) != (tokens, in_):
+        raise ValueError(f"dx: expected {(tokens, in_)}, got {(r, c)}")
+    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_INPUT_GRAD, tokens, out, in_)
+    workspace, wp, wsz = _scratch(on, workspace, nb)
+    on.call("muon_linear8_input_grad", dy.data_ptr(), lddy, dydt, wq.data_ptr(), ldw, wscale.data_ptr(), tokens, out,
+            in_, dx.data_ptr(), lddx, dt, wp, wsz)
+    return dx

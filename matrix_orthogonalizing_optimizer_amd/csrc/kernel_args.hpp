@@ -53,6 +53,66 @@ struct AdamArgs {
   float one_minus_b1, one_minus_b2, eps, keep, step;
 };
 
+// Row operators (see row_ops.hpp).
+struct RowArgs {
+  const void* x;
+  const void* gamma;  // vec_dtype; null when only quantizing
+  const void* beta;   // or null
+  void* y;            // or null
+  int8_t* q;          // or null
+  float* scale;
+  float* mean;        // or null
+  float* rstd;        // or null
+  int64_t ldx, ldy, ldq, rows;
+  int32_t cols;
+  int32_t vec_dtype;
+  float eps;
+};
+struct RestoreArgs {
+  const int8_t* q;
+  const float* scale;
+  void* y;
+  int64_t ldq, ldy, rows;
+  int64_t per_row;  // pieces of 16 columns per row
+  int32_t cols;
+};
+struct NormBwdArgs {
+  const void* dy;
+  const void* x;
+  const void* gamma;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  float* partials;  // [2][workgroups][cols], or null: no vector gradients
+  int64_t lddy, ldx, lddx, rows;
+  int32_t cols;
+  int32_t vec_dtype;
+};
+struct JoinArgs {
+  const float* partials;
+  void* dgamma;
+  void* dbeta;
+  int32_t parts;
+  int32_t accumulate;
+  int64_t cols;
+};
+
+// Linear layer on 8-bit rows (see linear8.hpp).
+struct Linear8Args {
+  const int8_t* q;       // tokens x in (forward, weight gradient)
+  const float* scale;
+  const int8_t* w;       // out x in (forward, input gradient)
+  const float* wscale;
+  const void* bias;
+  const void* dy;
+  void* o;               // y, dW or dX
+  void* ws;              // partial results
+  int64_t ldq, ldw, lddy, ldo;
+  int32_t tokens, out, in;
+  int32_t bias_dtype;
+  int32_t accumulate;
+};
+
 // Host table -> device memory through kernel arguments: one launch carries
 // up to BLOB_WORDS 32-bit words of a descriptor table, so no host staging
 // buffer, no host-to-device copy and no wait on the host are involved.

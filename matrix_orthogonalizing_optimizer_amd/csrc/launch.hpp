@@ -26,4 +26,16 @@ hipError_t launch_adamw(const AdamArgs& a, int64_t total_blocks, hipStream_t s);
 // launches on s; src may be reused as soon as the call returns.
 hipError_t launch_upload(void* dst, const void* src, size_t bytes, hipStream_t s);
 
+// Row operators.  kind: 0 layer norm, 1 RMS norm, 2 (forward only) no norm.
+// dt: dtype of x / dy / y / dx.  parts: workgroups of the backward kernel,
+// and rows of a.partials.
+hipError_t launch_row_forward(int kind, int dt, const RowArgs& a, hipStream_t s);
+hipError_t launch_row_restore(int dt, const RestoreArgs& a, hipStream_t s);
+hipError_t launch_norm_backward(int kind, int dt, const NormBwdArgs& a, int parts, hipStream_t s);
+hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s);
+
+// Linear layer on 8-bit rows.
+hipError_t launch_linear8_forward(int dt, const Linear8Args& a, hipStream_t s);
+hipError_t launch_linear8_grad(bool weight, int dy_dt, int out_dt, const Linear8Args& a, hipStream_t s);
+
 }  // namespace muon

@@ -1,0 +1,262 @@
+// C entry points of the operators around the step (norms, 8-bit rows, the
+// linear layer on 8-bit rows): validation, then one or two launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "consts.hpp"
+#include "launch.hpp"
+#include "libmuon.h"
+#include "plan.hpp"
+#include "timing.hpp"
+
+using namespace muon;
+
+namespace {
+
+constexpr int64_t MAX_SIDE = (int64_t)1 << 30;
+constexpr int64_t MAX_LD = (int64_t)1 << 40;    // row operators: 64-bit offsets
+constexpr int64_t MAX_LD8 = (int64_t)1 << 21;   // linear layer: a tile's rows within 32-bit offsets
+constexpr int64_t MAX_IN = 131071;              // 128 * 128 * in stays below 2^31
+
+bool dtype_ok(int32_t d) { return d == MUON_F32 || d == MUON_BF16; }
+size_t esize(int32_t d) { return d == MUON_F32 ? 4 : 2; }
+bool side_ok(int64_t v) { return v >= 0 && v <= MAX_SIDE; }
+bool ld_ok(int64_t ld, int64_t cols, int64_t most) { return ld >= cols && ld <= most; }
+bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool at_or_null(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int dev_dt(int32_t d) { return d == MUON_F32 ? DT_F32 : DT_BF16; }
+char* ws_base(void* p) {
+  const uintptr_t u = reinterpret_cast<uintptr_t>(p);
+  return reinterpret_cast<char*>((u + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN);
+}
+muon_status done(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_E_HIP; }
+
+// Workgroups of the norm's backward kernel = partial rows of its column sums.
+int norm_parts(int64_t rows, int64_t cols) {
+  const int64_t per = cols <= 1024 ? 4 : 1;  // rows a workgroup takes at a time
+  return (int)std::min<int64_t>(512, std::max<int64_t>(1, (rows + per - 1) / per));
+}
+size_t norm_ws(int64_t rows, int64_t cols) {
+  if (rows == 0 || cols == 0) return 0;
+  return (size_t)norm_parts(rows, cols) * (size_t)cols * 2 * sizeof(float) + WS_ALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_rows8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t dtype, int8_t* q,
+                                int64_t ldq, float* scale, void* stream) {
+  if (!dtype_ok(dtype)) return MUON_E_DTYPE;
+  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(ldx, cols, MAX_LD) || !ld_ok(ldq, cols, MAX_LD) || ldq % 16)
+    return MUON_E_SHAPE;
+  if (rows == 0) return MUON_OK;
+  if (!at(scale, 4) || (cols > 0 && (!at(x, esize(dtype)) || !at(q, 16)))) return MUON_E_ARG;
+  RowArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x; a.ldx = ldx;
+  a.q = q; a.ldq = ldq; a.scale = scale;
+  a.rows = rows; a.cols = (int32_t)cols;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const double n = (double)rows * (double)cols;
+  return done(timed(F_ROWS8, 0.0, n * (double)(esize(dtype) + 1), s,
+                    [&] { return launch_row_forward(2, dev_dt(dtype), a, s); }));
+}
+
+muon_status muon_rows8_dequantize(const int8_t* q, int64_t ldq, const float* scale, int64_t rows, int64_t cols,
+                                  void* y, int64_t ldy, int32_t dtype, void* stream) {
+  if (!dtype_ok(dtype)) return MUON_E_DTYPE;
+  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(ldy, cols, MAX_LD) || !ld_ok(ldq, cols, MAX_LD) || ldq % 16)
+    return MUON_E_SHAPE;
+  if (rows == 0 || cols == 0) return MUON_OK;
+  if (!at(scale, 4) || !at(q, 16) || !at(y, esize(dtype))) return MUON_E_ARG;
+  RestoreArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q; a.ldq = ldq; a.scale = scale;
+  a.y = y; a.ldy = ldy;
+  a.rows = rows; a.cols = (int32_t)cols; a.per_row = (cols + 15) / 16;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const double n = (double)rows * (double)cols;
+  return done(timed(F_ROWS8, 0.0, n * (double)(esize(dtype) + 1), s,
+                    [&] { return launch_row_restore(dev_dt(dtype), a, s); }));
+}
+
+muon_status muon_norm_forward(int32_t kind, const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t dtype,
+                              const void* gamma, const void* beta, int32_t vec_dtype, float eps, void* y, int64_t ldy,
+                              int8_t* q, int64_t ldq, float* scale, float* mean, float* rstd, void* stream) {
+  if (kind != MUON_NORM_LAYER && kind != MUON_NORM_RMS) return MUON_E_METHOD;
+  if (!dtype_ok(dtype) || !dtype_ok(vec_dtype)) return MUON_E_DTYPE;
+  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(ldx, cols, MAX_LD) || (y && !ld_ok(ldy, cols, MAX_LD)) ||
+      (q && (!ld_ok(ldq, cols, MAX_LD) || ldq % 16)))
+    return MUON_E_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.f) return MUON_E_ARG;
+  if ((q != nullptr) != (scale != nullptr) || (kind == MUON_NORM_RMS && mean)) return MUON_E_ARG;
+  if (rows == 0 || cols == 0) return MUON_OK;
+  if (!y && !q && !mean && !rstd) return MUON_E_ARG;
+  if (!at(x, esize(dtype)) || !at(gamma, esize(vec_dtype)) || !at_or_null(beta, esize(vec_dtype)) ||
+      !at_or_null(y, esize(dtype)) || !at_or_null(q, 16) || !at_or_null(scale, 4) || !at_or_null(mean, 4) ||
+      !at_or_null(rstd, 4))
+    return MUON_E_ARG;
+  if (y == x && y && ldy != ldx) return MUON_E_ARG;
+  RowArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x; a.ldx = ldx;
+  a.gamma = gamma; a.beta = beta; a.vec_dtype = dev_dt(vec_dtype);
+  a.eps = eps;
+  a.y = y; a.ldy = ldy;
+  a.q = q; a.ldq = ldq; a.scale = scale;
+  a.mean = mean; a.rstd = rstd;
+  a.rows = rows; a.cols = (int32_t)cols;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const double n = (double)rows * (double)cols, es = (double)esize(dtype);
+  return done(timed(F_NORM_FWD, 0.0, n * (es + (y ? es : 0.0) + (q ? 1.0 : 0.0)), s,
+                    [&] { return launch_row_forward(kind, dev_dt(dtype), a, s); }));
+}
+
+muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return MUON_E_ARG;
+  if (!side_ok(rows) || !side_ok(cols)) return MUON_E_SHAPE;
+  *bytes = norm_ws(rows, cols);
+  return MUON_OK;
+}
+
+muon_status muon_norm_backward(int32_t kind, const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows,
+                               int64_t cols, int32_t dtype, const void* gamma, int32_t vec_dtype, const float* mean,
+                               const float* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                               int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  if (kind != MUON_NORM_LAYER && kind != MUON_NORM_RMS) return MUON_E_METHOD;
+  if (!dtype_ok(dtype) || !dtype_ok(vec_dtype)) return MUON_E_DTYPE;
+  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(lddy, cols, MAX_LD) || !ld_ok(ldx, cols, MAX_LD) ||
+      !ld_ok(lddx, cols, MAX_LD))
+    return MUON_E_SHAPE;
+  const size_t es = esize(dtype), ve = esize(vec_dtype);
+  if (kind == MUON_NORM_RMS && (mean || dbeta)) return MUON_E_ARG;
+  if (!at_or_null(dgamma, ve) || !at_or_null(dbeta, ve)) return MUON_E_ARG;
+  if (cols == 0) return MUON_OK;
+  if (rows > 0) {
+    if (!at(dy, es) || !at(x, es) || !at(dx, es) || !at(gamma, ve) || !at(rstd, 4) || !at_or_null(mean, 4) ||
+        (kind == MUON_NORM_LAYER && !mean))
+      return MUON_E_ARG;
+    if (dx == dy && lddx != lddy) return MUON_E_ARG;
+  }
+  const bool vecs = dgamma || dbeta;
+  if (vecs && rows > 0 && (!workspace || workspace_bytes < norm_ws(rows, cols))) return MUON_E_WORKSPACE;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int parts = rows > 0 ? norm_parts(rows, cols) : 0;
+  float* part = vecs && rows > 0 ? reinterpret_cast<float*>(ws_base(workspace)) : nullptr;
+  if (rows > 0) {
+    NormBwdArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.dy = dy; a.lddy = lddy;
+    a.x = x; a.ldx = ldx;
+    a.gamma = gamma; a.vec_dtype = dev_dt(vec_dtype);
+    a.mean = mean; a.rstd = rstd;
+    a.dx = dx; a.lddx = lddx;
+    a.partials = part;
+    a.rows = rows; a.cols = (int32_t)cols;
+    const double n = (double)rows * (double)cols;
+    const hipError_t e = timed(F_NORM_BWD, 0.0, 3.0 * n * (double)es, s,
+                               [&] { return launch_norm_backward(kind, dev_dt(dtype), a, parts, s); });
+    if (e != hipSuccess) return MUON_E_HIP;
+  }
+  if (vecs) {
+    JoinArgs j;
+    std::memset(&j, 0, sizeof(j));
+    j.partials = part;
+    j.parts = parts;
+    j.dgamma = dgamma; j.dbeta = dbeta;
+    j.accumulate = accumulate;
+    j.cols = cols;
+    const hipError_t e =
+        timed(F_NORM_BWD, 0.0, 0.0, s, [&] { return launch_norm_join(dev_dt(vec_dtype), j, s); });
+    if (e != hipSuccess) return MUON_E_HIP;
+  }
+  return MUON_OK;
+}
+
+muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t out, int64_t in, size_t* bytes) {
+  if (!bytes) return MUON_E_ARG;
+  if (pass < MUON_LINEAR8_FORWARD || pass > MUON_LINEAR8_INPUT_GRAD) return MUON_E_METHOD;
+  if (!side_ok(tokens) || !side_ok(out) || !side_ok(in) || (pass == MUON_LINEAR8_FORWARD && in > MAX_IN))
+    return MUON_E_SHAPE;
+  *bytes = 0;
+  return MUON_OK;
+}
+
+muon_status muon_linear8_forward(const int8_t* q, int64_t ldq, const float* scale, const int8_t* wq, int64_t ldw,
+                                 const float* wscale, const void* bias, int32_t bias_dtype, int64_t tokens,
+                                 int64_t out, int64_t in, void* y, int64_t ldy, int32_t dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype) || (bias && !dtype_ok(bias_dtype))) return MUON_E_DTYPE;
+  if (!side_ok(tokens) || !side_ok(out) || !side_ok(in) || in > MAX_IN || !ld_ok(ldq, in, MAX_LD8) ||
+      !ld_ok(ldw, in, MAX_LD8) || !ld_ok(ldy, out, MAX_LD8) || ldq % 16 || ldw % 16)
+    return MUON_E_SHAPE;
+  if (tokens == 0 || out == 0) return MUON_OK;
+  if (!at(scale, 4) || !at(wscale, 4) || !at(y, esize(dtype)) || (bias && !at(bias, esize(bias_dtype))) ||
+      (in > 0 && (!at(q, 16) || !at(wq, 16))))
+    return MUON_E_ARG;
+  (void)workspace;
+  (void)workspace_bytes;
+  Linear8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q; a.ldq = ldq; a.scale = scale;
+  a.w = wq; a.ldw = ldw; a.wscale = wscale;
+  a.bias = bias; a.bias_dtype = dev_dt(bias_dtype);
+  a.o = y; a.ldo = ldy;
+  a.tokens = (int32_t)tokens; a.out = (int32_t)out; a.in = (int32_t)in;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const double f = 2.0 * (double)tokens * (double)out * (double)in;
+  return done(timed(F_LINEAR8_Y, f, 0.0, s, [&] { return launch_linear8_forward(dev_dt(dtype), a, s); }));
+}
+
+static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* q,
+                                int64_t ldq, const float* scale, int64_t tokens, int64_t out, int64_t in, void* o,
+                                int64_t ldo, int32_t o_dtype, int32_t accumulate, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dy_dtype) || !dtype_ok(o_dtype)) return MUON_E_DTYPE;
+  if (!side_ok(tokens) || !side_ok(out) || !side_ok(in) || !ld_ok(lddy, out, MAX_LD8) || !ld_ok(ldq, in, MAX_LD8) ||
+      !ld_ok(ldo, in, MAX_LD8) || ldq % 16)
+    return MUON_E_SHAPE;
+  const int64_t rows = weight ? out : tokens, sum = weight ? tokens : out;
+  if (rows == 0 || in == 0) return MUON_OK;
+  if (!at(o, esize(o_dtype)) || (sum > 0 && (!at(dy, esize(dy_dtype)) || !at(q, 16) || !at(scale, 4))))
+    return MUON_E_ARG;
+  (void)workspace;
+  (void)workspace_bytes;
+  Linear8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.dy = dy; a.lddy = lddy;
+  if (weight) {
+    a.q = q; a.ldq = ldq; a.scale = scale;
+  } else {
+    a.w = q; a.ldw = ldq; a.wscale = scale;
+  }
+  a.o = o; a.ldo = ldo;
+  a.accumulate = accumulate;
+  a.tokens = (int32_t)tokens; a.out = (int32_t)out; a.in = (int32_t)in;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const double f = 2.0 * (double)tokens * (double)out * (double)in;
+  return done(timed(weight ? F_LINEAR8_DW : F_LINEAR8_DX, f, 0.0, s,
+                    [&] { return launch_linear8_grad(weight, dev_dt(dy_dtype), dev_dt(o_dtype), a, s); }));
+}
+
+muon_status muon_linear8_weight_grad(const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* q, int64_t ldq,
+                                     const float* scale, int64_t tokens, int64_t out, int64_t in, void* dw,
+                                     int64_t lddw, int32_t dw_dtype, int32_t accumulate, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  return linear8_grad(true, dy, lddy, dy_dtype, q, ldq, scale, tokens, out, in, dw, lddw, dw_dtype, accumulate,
+                      workspace, workspace_bytes, stream);
+}
+
+muon_status muon_linear8_input_grad(const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* wq, int64_t ldw,
+                                    const float* wscale, int64_t tokens, int64_t out, int64_t in, void* dx,
+                                    int64_t lddx, int32_t dx_dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  return linear8_grad(false, dy, lddy, dy_dtype, wq, ldw, wscale, tokens, out, in, dx, lddx, dx_dtype, 0, workspace,
+                      workspace_bytes, stream);
+}
+
+}  // extern "C"

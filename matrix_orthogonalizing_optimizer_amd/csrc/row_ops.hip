@@ -1,0 +1,84 @@
+// Launchers of the row operators.
+#include <type_traits>
+
+#include "consts.hpp"
+#include "launch.hpp"
+#include "row_ops.hpp"
+
+namespace muon {
+
+namespace {
+
+// (threads per row, pieces per thread) for a row of `cols` values
+template <typename F> hipError_t by_width(int cols, F&& f) {
+  if (cols <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  if (cols <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (cols <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  if (cols <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  if (cols <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+}
+
+template <typename T, int KIND> hipError_t forward(const RowArgs& a, hipStream_t s) {
+  if (a.cols > ROW_MAX_COLS) {
+    hipLaunchKernelGGL((row_forward_long_kernel<T, KIND>), dim3((unsigned)a.rows), dim3(1024), 0, s, a);
+    return hipGetLastError();
+  }
+  return by_width(a.cols, [&](auto g, auto nv) {
+    constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
+    constexpr int RPW = G < 256 ? 256 / G : 1;
+    hipLaunchKernelGGL((row_forward_kernel<T, KIND, G, NV>), dim3((unsigned)((a.rows + RPW - 1) / RPW)),
+                       dim3(G < 256 ? 256 : G), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+template <typename T, int KIND> hipError_t backward(const NormBwdArgs& a, int parts, hipStream_t s) {
+  if (a.cols > ROW_MAX_COLS) {
+    // the column sums first: dx may overwrite dy
+    if (a.partials) {
+      hipLaunchKernelGGL((norm_columns_long_kernel<T, KIND>), dim3((unsigned)((a.cols + 255) / 256), (unsigned)parts),
+                         dim3(256), 0, s, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((norm_backward_long_kernel<T, KIND>), dim3((unsigned)a.rows), dim3(1024), 0, s, a);
+    return hipGetLastError();
+  }
+  return by_width(a.cols, [&](auto g, auto nv) {
+    constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
+    hipLaunchKernelGGL((norm_backward_kernel<T, KIND, G, NV>), dim3((unsigned)parts), dim3(G < 256 ? 256 : G), 0, s,
+                       a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+hipError_t launch_row_forward(int kind, int dt, const RowArgs& a, hipStream_t s) {
+  if (dt == DT_BF16)
+    return kind == 0 ? forward<bf16, 0>(a, s) : kind == 1 ? forward<bf16, 1>(a, s) : forward<bf16, ROW_COPY>(a, s);
+  return kind == 0 ? forward<float, 0>(a, s) : kind == 1 ? forward<float, 1>(a, s) : forward<float, ROW_COPY>(a, s);
+}
+
+hipError_t launch_row_restore(int dt, const RestoreArgs& a, hipStream_t s) {
+  const int64_t blocks = (a.rows * a.per_row + DEQ_PIECES - 1) / DEQ_PIECES;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (dt == DT_BF16) hipLaunchKernelGGL((row_restore_kernel<bf16>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((row_restore_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_backward(int kind, int dt, const NormBwdArgs& a, int parts, hipStream_t s) {
+  if (dt == DT_BF16) return kind == 0 ? backward<bf16, 0>(a, parts, s) : backward<bf16, 1>(a, parts, s);
+  return kind == 0 ? backward<float, 0>(a, parts, s) : backward<float, 1>(a, parts, s);
+}
+
+hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s) {
+  const dim3 g((unsigned)((a.cols + 63) / 64), a.dbeta ? 2 : 1);
+  if (vec_dtype == DT_BF16) hipLaunchKernelGGL((norm_columns_join_kernel<bf16>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((norm_columns_join_kernel<float>), g, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -1,0 +1,530 @@
+// Row operators on gfx950: norms, their gradients, and 8-bit rows.
+//
+// Per row x of `cols` values,
+//   mu = mean(x) or 0,  r = 1 / sqrt(mean((x - mu)^2) + eps),  h = (x - mu) r,
+//   y = h gamma + beta;
+//   g = dy gamma,  dx = r (g - mean(g) - h mean(g h)),
+//   dgamma = sum_rows dy h,  dbeta = sum_rows dy;
+//   8-bit rows: s = 2^e with max|y| <= 127 s, q = rne(y / s).
+// All of it is bound by HBM: a row is read once and kept in registers (fp32)
+// by a group of G threads, G = 64 (one wave, no barrier) up to 1024 columns
+// and wider groups above, so that a thread holds at most two pieces of 8
+// columns.  Rows longer than 16384 columns are read again for each pass.
+#pragma once
+
+#include "device_common.hpp"
+#include "kernel_args.hpp"
+
+namespace muon {
+
+constexpr int ROW_VE = 8;  // columns per piece
+
+// Vectors at the alignment of their elements only: global accesses may be
+// unaligned on gfx950, so rows of odd widths and odd starts take the same
+// path as aligned ones.
+typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename T> __device__ __forceinline__ void row_load8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x4_e2 w = *as_global(reinterpret_cast<const u32x4_e2*>(p));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = __builtin_bit_cast(float, (e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+  } else {
+    const f32x4_e4 a = *as_global(reinterpret_cast<const f32x4_e4*>(p));
+    const f32x4_e4 b = *as_global(reinterpret_cast<const f32x4_e4*>(p + 4));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[e + 4] = b[e]; }
+  }
+}
+
+template <typename T> __device__ __forceinline__ void row_store8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    u32x4_e2 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
+    *as_global(reinterpret_cast<u32x4_e2*>(p)) = w;
+  } else {
+    *as_global(reinterpret_cast<f32x4_e4*>(p)) = f32x4_e4{v[0], v[1], v[2], v[3]};
+    *as_global(reinterpret_cast<f32x4_e4*>(p + 4)) = f32x4_e4{v[4], v[5], v[6], v[7]};
+  }
+}
+
+// Piece at column c of a row of `cols`: columns past the end read as zero
+// and are not written.
+template <typename T> __device__ __forceinline__ void piece_load(const T* row, int c, int cols, float (&v)[8]) {
+  if (c + 8 <= cols) {
+    row_load8(row + c, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? to_f32(as_global(row)[c + e]) : 0.f;
+  }
+}
+template <typename T> __device__ __forceinline__ void piece_store(T* row, int c, int cols, const float (&v)[8]) {
+  if (c + 8 <= cols) {
+    row_store8(row + c, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < cols) as_global(row)[c + e] = from_f32<T>(v[e]);
+  }
+}
+// The same for a vector whose dtype is known at run time only.
+__device__ __forceinline__ void vec_load(const void* p, int dt, int c, int cols, float (&v)[8]) {
+  if (dt == DT_F32) piece_load(static_cast<const float*>(p), c, cols, v);
+  else piece_load(static_cast<const bf16*>(p), c, cols, v);
+}
+
+// Deterministic sums over a group of G threads (a whole number of waves):
+// butterfly inside a wave, waves in order.  G > 64: all threads of the
+// workgroup take part and `red` is one of two alternating buffers, so one
+// barrier per sum is enough (a wave writes a buffer again only after the
+// barrier of the sum in between, which every reader of it has passed).
+template <int G, int N> struct GroupRed {
+  float slot[2][G / 64][N];
+};
+template <int G, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], GroupRed<G, N>& red, int buf) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+  if constexpr (G > 64) {
+    const int w = (threadIdx.x % G) >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) red.slot[buf][w][k] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float s = red.slot[buf][0][k];
+#pragma unroll
+      for (int i = 1; i < G / 64; ++i) s += red.slot[buf][i][k];
+      v[k] = s;
+    }
+  }
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_umax(uint32_t v, GroupRed<G, 1>& red, int buf) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, off, 64);
+    v = v > o ? v : o;
+  }
+  if constexpr (G > 64) {
+    const int w = (threadIdx.x % G) >> 6;
+    if ((threadIdx.x & 63) == 0) red.slot[buf][w][0] = __builtin_bit_cast(float, v);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < G / 64; ++i) {
+      const uint32_t o = __builtin_bit_cast(uint32_t, red.slot[buf][i][0]);
+      v = v > o ? v : o;
+    }
+  }
+  return v;
+}
+
+// Magnitude bits of a float: as unsigned integers they order like the
+// magnitudes, infinities above every finite value and NaNs above those, so
+// one integer maximum finds both the scale and a non-finite row.
+__device__ __forceinline__ uint32_t mag_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
+
+// Scale of a row whose largest magnitude has the bits m: the smallest power
+// of two with max <= 127 s.  max = f 2^k, 1 <= f < 2: s = 2^(k - 6) if
+// f <= 127/64, else 2^(k - 5); 127/64 has the fraction bits 0x7e0000, and
+// adding 0x1ffff carries into the exponent exactly above it.  inv = 1 / s is
+// a normal number (s is at least 2^-126 and below 2^123).
+// lim: 127, or 63 for the largest scale, 2^122, where 64 s is out of range.
+__device__ __forceinline__ void row_scale(uint32_t m, float& s, float& inv, float& lim) {
+  int e = (int)((m + 0x1ffffu) >> 23) - 6;
+  e = e < 1 ? 1 : e;
+  s = __builtin_bit_cast(float, (uint32_t)e << 23);
+  inv = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
+  lim = e == 122 + 127 ? 63.f : 127.f;
+  if (m >= 0x7f800000u) {
+    s = __builtin_bit_cast(float, 0x7fc00000u);
+    inv = 0.f;
+  }
+}
+// 8 values -> 8 bytes; x * inv is exact (a power of two) wherever it matters:
+// what falls below the normal range rounds to 0 either way.
+__device__ __forceinline__ u32x2 quant8(const float (&v)[8], float inv, float lim, bool fine) {
+  u32x2 w = {0u, 0u};
+  if (fine) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float r = __builtin_amdgcn_fmed3f(__builtin_rintf(v[e] * inv), -lim, lim);
+      w[e >> 2] |= ((uint32_t)(int)r & 0xffu) << (8 * (e & 3));
+    }
+  }
+  return w;
+}
+
+enum : int { ROW_COPY = 2 };  // next to MUON_NORM_LAYER = 0 and MUON_NORM_RMS = 1: no norm, quantize only
+
+// Norm forward / quantize, a row per group of G threads, NV pieces each.
+// Two reductions for the layer norm (the variance is taken around the mean
+// from registers, not as a difference of sums), one more for the 8-bit scale.
+template <typename T, int KIND, int G, int NV>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void row_forward_kernel(const RowArgs a) {
+  constexpr int RPW = G < 256 ? 256 / G : 1;  // rows per workgroup
+  __shared__ GroupRed<G, 1> red;
+  const int t = threadIdx.x % G;
+  const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / G;
+  if (G < 256 && row >= a.rows) return;  // whole waves, and no barrier below when G == 64
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  float v[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) piece_load(x, (i * G + t) * ROW_VE, a.cols, v[i]);
+  if constexpr (KIND != ROW_COPY) {
+    float mean = 0.f;
+    if constexpr (KIND == 0) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[0] += v[i][e];
+      group_sum<G, 1>(s, red, 0);
+      mean = s[0] / (float)a.cols;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = (i * G + t) * ROW_VE + e < a.cols ? v[i][e] - mean : 0.f;
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] = fmaf(v[i][e], v[i][e], s[0]);
+    group_sum<G, 1>(s, red, 1);
+    const float r = 1.f / sqrtf(s[0] / (float)a.cols + a.eps);
+    if (t == 0) {
+      if (a.mean) as_global(a.mean)[row] = mean;
+      if (a.rstd) as_global(a.rstd)[row] = r;
+    }
+    if (!a.y && !a.scale) return;  // uniform
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * G + t) * ROW_VE;
+      float w[8];
+      vec_load(a.gamma, a.vec_dtype, c, a.cols, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * w[e];
+      if (a.beta) {
+        vec_load(a.beta, a.vec_dtype, c, a.cols, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] += w[e];
+      }
+    }
+    if (a.y) {
+      T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) piece_store(y, (i * G + t) * ROW_VE, a.cols, v[i]);
+    }
+  }
+  if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // a NaN's padding products (0 * NaN) sit in columns past the end
+        const uint32_t b = (i * G + t) * ROW_VE + e < a.cols ? mag_bits(v[i][e]) : 0u;
+        m = m > b ? m : b;
+      }
+    m = group_umax<G>(m, red, 0);
+    float s, inv, lim;
+    row_scale(m, s, inv, lim);
+    const bool fine = m < 0x7f800000u;
+    if (t == 0) as_global(a.scale)[row] = s;
+    int8_t* q = a.q + row * a.ldq;
+    const int cpad = (a.cols + 15) & ~15;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * G + t) * ROW_VE;
+      if (c < cpad) *as_global(reinterpret_cast<u32x2*>(q + c)) = quant8(v[i], inv, lim, fine);
+    }
+  }
+}
+
+// The same for rows of any length, which are read again for every pass.  A
+// thread rereads only pieces that it alone writes, so y may be x.
+template <typename T, int KIND>
+__global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a) {
+  constexpr int G = 1024;
+  __shared__ GroupRed<G, 1> red;
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  float mean = 0.f, r = 1.f;
+  if constexpr (KIND != ROW_COPY) {
+    if constexpr (KIND == 0) {
+      float s[1] = {0.f};
+      for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+        float v[8];
+        piece_load(x, (int)c, a.cols, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[0] += v[e];
+      }
+      group_sum<G, 1>(s, red, 0);
+      mean = s[0] / (float)a.cols;
+    }
+    float s[1] = {0.f};
+    for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+      float v[8];
+      piece_load(x, (int)c, a.cols, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = c + e < a.cols ? v[e] - mean : 0.f;
+        s[0] = fmaf(d, d, s[0]);
+      }
+    }
+    group_sum<G, 1>(s, red, 1);
+    r = 1.f / sqrtf(s[0] / (float)a.cols + a.eps);
+    if (t == 0) {
+      if (a.mean) as_global(a.mean)[row] = mean;
+      if (a.rstd) as_global(a.rstd)[row] = r;
+    }
+    if (!a.y && !a.scale) return;
+  }
+  auto value = [&](int64_t c, float (&v)[8]) {
+    piece_load(x, (int)c, a.cols, v);
+    if constexpr (KIND != ROW_COPY) {
+      float w[8];
+      vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * r * w[e];
+      if (a.beta) {
+        vec_load(a.beta, a.vec_dtype, (int)c, a.cols, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += w[e];
+      }
+    }
+  };
+  float s = 0.f, inv = 0.f, lim = 0.f;
+  bool fine = false;
+  if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
+    uint32_t m = 0;
+    for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+      float v[8];
+      value(c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = c + e < a.cols ? mag_bits(v[e]) : 0u;
+        m = m > b ? m : b;
+      }
+    }
+    m = group_umax<G>(m, red, 0);
+    row_scale(m, s, inv, lim);
+    fine = m < 0x7f800000u;
+    if (t == 0) as_global(a.scale)[row] = s;
+  }
+  const int64_t cpad = ((int64_t)a.cols + 15) & ~(int64_t)15;
+  for (int64_t c = (int64_t)t * ROW_VE; c < cpad; c += G * ROW_VE) {
+    float v[8];
+    value(c, v);
+    if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = c + e < a.cols ? v[e] : 0.f;
+      *as_global(reinterpret_cast<u32x2*>(a.q + row * a.ldq + c)) = quant8(z, inv, lim, fine);
+    }
+    if (KIND != ROW_COPY && a.y) piece_store(static_cast<T*>(a.y) + row * a.ldy, (int)c, a.cols, v);
+  }
+}
+
+// Restore: y = q * scale.  16 columns per thread; a workgroup takes 1024
+// consecutive pieces of the rows x ceil(cols / 16) grid of pieces.
+constexpr int DEQ_PIECES = 1024;
+template <typename T>
+__global__ __launch_bounds__(256) void row_restore_kernel(const RestoreArgs a) {
+  const int64_t total = a.rows * a.per_row;
+  const int64_t base = (int64_t)blockIdx.x * DEQ_PIECES;
+  const int64_t row0 = base / a.per_row;
+  const uint32_t first = (uint32_t)(base - row0 * a.per_row);
+#pragma unroll
+  for (int i = 0; i < DEQ_PIECES / 256; ++i) {
+    const uint32_t p = i * 256 + threadIdx.x;
+    if (base + p >= total) return;
+    const uint32_t dr = (first + p) / (uint32_t)a.per_row;
+    const int c = (int)((first + p) - dr * (uint32_t)a.per_row) * 16;
+    const int64_t row = row0 + dr;
+    const u32x4 w = *as_global(reinterpret_cast<const u32x4*>(a.q + row * a.ldq + c));
+    const float s = as_global(a.scale)[row];
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(w[2 * h + (e >> 2)] >> (8 * (e & 3))) * s;
+      if (c + 8 * h < a.cols) piece_store(y, c + 8 * h, a.cols, v);
+    }
+  }
+}
+
+// Norm backward: workgroups loop over rows; a thread keeps its columns' gamma
+// and its sums of dy h and dy in registers over all of them, and the sums go
+// to workspace once per workgroup (partials[2][workgroups][cols]).
+template <typename T, int KIND, int G, int NV>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const NormBwdArgs a) {
+  constexpr int RPW = G < 256 ? 256 / G : 1;
+  __shared__ GroupRed<G, 2> red;
+  __shared__ float comb[RPW > 1 ? RPW * G * NV * 8 : 1];
+  const int t = threadIdx.x % G;
+  const int sub = threadIdx.x / G;
+  float gam[NV][8], sg[NV][8], sb[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    vec_load(a.gamma, a.vec_dtype, (i * G + t) * ROW_VE, a.cols, gam[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.f;
+  }
+  int buf = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < a.rows; row += (int64_t)gridDim.x * RPW) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+    float h[NV][8], g[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      piece_load(x, (i * G + t) * ROW_VE, a.cols, h[i]);
+      piece_load(dy, (i * G + t) * ROW_VE, a.cols, g[i]);
+    }
+    const float r = as_global(a.rstd)[row];
+    const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[i][e] = (h[i][e] - mean) * r;
+        sg[i][e] = fmaf(g[i][e], h[i][e], sg[i][e]);
+        if (KIND == 0) sb[i][e] += g[i][e];
+        g[i][e] *= gam[i][e];
+        s[0] = fmaf(g[i][e], h[i][e], s[0]);
+        if (KIND == 0) s[1] += g[i][e];
+      }
+    group_sum<G, 2>(s, red, buf);
+    buf ^= 1;
+    const float c2 = s[0] / (float)a.cols, c1 = KIND == 0 ? s[1] / (float)a.cols : 0.f;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - c1 - h[i][e] * c2);
+      if ((i * G + t) * ROW_VE < a.cols) piece_store(dx, (i * G + t) * ROW_VE, a.cols, g[i]);
+    }
+  }
+  if (!a.partials) return;
+  auto put = [&](float (&v)[NV][8], int which) {
+    float* p = a.partials + ((int64_t)which * gridDim.x + blockIdx.x) * a.cols;
+    if constexpr (RPW > 1) {  // the workgroup's rows join in order
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) comb[((sub * NV + i) * 8 + e) * G + t] = v[i][e];
+      __syncthreads();
+      if (sub == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float s = comb[(i * 8 + e) * G + t];
+#pragma unroll
+            for (int w = 1; w < RPW; ++w) s += comb[((w * NV + i) * 8 + e) * G + t];
+            v[i][e] = s;
+          }
+      }
+      __syncthreads();
+      if (sub != 0) return;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * G + t) * ROW_VE < a.cols) piece_store(p, (i * G + t) * ROW_VE, a.cols, v[i]);
+  };
+  put(sg, 0);
+  if constexpr (KIND == 0) put(sb, 1);
+}
+
+// Long rows: dx with the row read twice, and the column sums on their own.
+template <typename T, int KIND>
+__global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdArgs a) {
+  constexpr int G = 1024;
+  __shared__ GroupRed<G, 2> red;
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+  T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+  const float r = as_global(a.rstd)[row];
+  const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f;
+  float s[2] = {0.f, 0.f};
+  for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+    float h[8], g[8], w[8];
+    piece_load(x, (int)c, a.cols, h);
+    piece_load(dy, (int)c, a.cols, g);
+    vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float ge = g[e] * w[e];
+      s[0] = fmaf(ge, (h[e] - mean) * r, s[0]);
+      s[1] += ge;
+    }
+  }
+  group_sum<G, 2>(s, red, 0);
+  const float c2 = s[0] / (float)a.cols, c1 = KIND == 0 ? s[1] / (float)a.cols : 0.f;
+  for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+    float h[8], g[8], w[8];
+    piece_load(x, (int)c, a.cols, h);
+    piece_load(dy, (int)c, a.cols, g);
+    vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = r * (g[e] * w[e] - c1 - (h[e] - mean) * r * c2);
+    piece_store(dx, (int)c, a.cols, g);
+  }
+}
+
+// partials[2][gridDim.y][cols] of the columns of 256 threads x 1 column.
+template <typename T, int KIND>
+__global__ __launch_bounds__(256) void norm_columns_long_kernel(const NormBwdArgs a) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.cols) return;
+  float sg = 0.f, sb = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float g = to_f32(as_global(static_cast<const T*>(a.dy))[row * a.lddy + c]);
+    const float x = to_f32(as_global(static_cast<const T*>(a.x))[row * a.ldx + c]);
+    const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f;
+    sg = fmaf(g, (x - mean) * as_global(a.rstd)[row], sg);
+    sb += g;
+  }
+  as_global(a.partials)[(int64_t)blockIdx.y * a.cols + c] = sg;
+  if (KIND == 0) as_global(a.partials)[((int64_t)gridDim.y + blockIdx.y) * a.cols + c] = sb;
+}
+
+// Joins the workgroups' column sums in order: 64 columns per workgroup, 4
+// waves each a quarter of the partials, in fixed order.
+template <typename TV>
+__global__ __launch_bounds__(256) void norm_columns_join_kernel(const JoinArgs a) {
+  __shared__ float part[4][64];
+  const int which = blockIdx.y;
+  TV* out = static_cast<TV*>(which == 0 ? a.dgamma : a.dbeta);
+  if (!out) return;  // uniform
+  const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + l;
+  const float* p = a.partials + (int64_t)which * a.parts * a.cols;
+  const int per = (a.parts + 3) / 4;
+  const int hi = min(a.parts, (w + 1) * per);
+  float s = 0.f;
+  if (c < a.cols) {
+#pragma unroll 8
+    for (int i = w * per; i < hi; ++i) s += as_global(p)[(int64_t)i * a.cols + c];
+  }
+  part[w][l] = s;
+  __syncthreads();
+  if (w == 0 && c < a.cols) {
+    s = (part[0][l] + part[1][l]) + (part[2][l] + part[3][l]);
+    if (a.accumulate) s += to_f32(as_global(out)[c]);
+    as_global(out)[c] = from_f32<TV>(s);
+  }
+}
+
+}  // namespace muon
