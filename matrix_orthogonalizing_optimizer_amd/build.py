@@ -15,7 +15,8 @@ BUILD = os.path.join(ROOT, "_build", "libmuon")
 LIB = os.path.join(PKG, "libmuon.so")
 
 HIP_SOURCES = ["api.cpp", "timing.cpp", "kernels_elem.hip", "gemm_bf16.hip", "gemm_f16.hip",
-               "gemm_f32.hip", "probes.hip", "noalloc.hip", "ops.cpp", "row_ops.hip", "linear8.hip"]
+               "gemm_f32.hip", "probes.hip", "noalloc.hip", "ops.cpp", "row_ops.hip",
+               "linear8_y.hip", "linear8_dw.hip", "linear8_dx.hip"]
 HOST_SOURCES = ["plan.cpp"]
 ARCH = "gfx950"
 

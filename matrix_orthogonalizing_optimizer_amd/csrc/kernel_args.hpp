@@ -97,18 +97,23 @@ struct JoinArgs {
   int64_t cols;
 };
 
-// Linear layer on 8-bit rows (see linear8.hpp).
+// Products of the linear layer on 8-bit rows (see linear8.hpp): C (M x N) as
+// a sum over K of A B.
+//   forward          A = q (tokens x in), B = w (out x in), both K-contiguous
+//   weight gradient  A = dy (tokens x out, K-major), B = q (tokens x in, K-major)
+//   input gradient   A = dy (tokens x out, K-contiguous), B = w (out x in, K-major)
 struct Linear8Args {
-  const int8_t* q;       // tokens x in (forward, weight gradient)
-  const float* scale;
-  const int8_t* w;       // out x in (forward, input gradient)
-  const float* wscale;
-  const void* bias;
-  const void* dy;
-  void* o;               // y, dW or dX
-  void* ws;              // partial results
-  int64_t ldq, ldw, lddy, ldo;
-  int32_t tokens, out, in;
+  const void* A;
+  const int8_t* B;
+  const float* sa;    // forward: one per row of C
+  const float* sb;    // forward: one per column of C; gradients: one per summation index
+  const void* bias;   // forward: one per column of C, or null
+  void* o;            // C
+  float* ws;          // [splits][M][ldws] partial results
+  int64_t lda, ldb, ldo, ldws;
+  int32_t M, N, K;
+  int32_t tilesM, tilesN, splits;
+  int32_t per_split;  // K-stages (128 bytes of a row) per split
   int32_t bias_dtype;
   int32_t accumulate;
 };

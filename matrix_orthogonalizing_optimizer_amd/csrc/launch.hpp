@@ -34,8 +34,10 @@ hipError_t launch_row_restore(int dt, const RestoreArgs& a, hipStream_t s);
 hipError_t launch_norm_backward(int kind, int dt, const NormBwdArgs& a, int parts, hipStream_t s);
 hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s);
 
-// Linear layer on 8-bit rows.
-hipError_t launch_linear8_forward(int dt, const Linear8Args& a, hipStream_t s);
-hipError_t launch_linear8_grad(bool weight, int dy_dt, int out_dt, const Linear8Args& a, hipStream_t s);
+// Linear layer on 8-bit rows.  tile: 128 or 256; odt: dtype of the result;
+// asrc: how dy is read (A_DIRECT, A_REG16, A_REG32 in linear8.hpp).
+hipError_t launch_linear8_forward(int tile, int odt, const Linear8Args& a, hipStream_t s);
+hipError_t launch_linear8_dw(int tile, int asrc, int odt, const Linear8Args& a, hipStream_t s);
+hipError_t launch_linear8_dx(int tile, int asrc, int odt, const Linear8Args& a, hipStream_t s);
 
 }  // namespace muon

@@ -1,100 +1,578 @@
-// Linear layer on 8-bit rows, gfx950.
+// Linear layer on 8-bit rows, gfx950: three tiled matrix products
+//   L8_Y   y[t][n]  = scale[t] wscale[n] sum_k q[t][k] w[n][k] + bias[n]
+//   L8_DW  dW[n][k] = sum_t dy[t][n] (scale[t] q[t][k])
+//   L8_DX  dX[t][k] = sum_n dy[t][n] (wscale[n] w[n][k])
+// Written below as C (M x N) = sum over K of A B.
 //
-//   y[t][n]  = scale[t] wscale[n] sum_k q[t][k] w[n][k] + bias[n]
-//   dW[n][k] = sum_t dy[t][n] scale[t] q[t][k]
-//   dX[t][k] = sum_n dy[t][n] wscale[n] w[n][k]
-// Simple forms: the forward product with one 32 x 32 tile per wave and
-// fragments straight from global memory; the gradients with 64 x 64 tiles in
-// shared memory and fp32 FMAs.
+// A workgroup owns a T x T tile of C (T = 256: 8 waves of 128 x 64 outputs,
+// two per SIMD; T = 128: 4 waves of 64 x 64) and walks K in stages of 128
+// bytes per row: 128 values of int8, or 64 of bf16.  Two stages live in LDS.
+//
+// L8_Y: both operands row-major int8, copied global -> LDS without a register
+// round trip; v_mfma_i32_32x32x32_i8, sums exact in 32-bit integers.
+//
+// L8_DW, L8_DX: v_mfma_f32_32x32x16_bf16.  The 8-bit operand lies K-major
+// (row s of the storage is summation index s) with one scale per summation
+// row, which no epilogue can apply.  It is loaded to registers, turned into
+// bf16 (q * scale; exact, the scale being a power of two) once per workgroup
+// and written to LDS, between the MFMAs of the stage before; converting in
+// front of the MFMAs instead would repeat it in every wave that shares the
+// columns.  Fragments come out of LDS transposed (ds_read_b64_tr_b16).  dy is
+// row-major for dX, K-major for dW.
+//   A_DIRECT  bf16 dy, 16-byte aligned rows, sizes multiples of 8: copied
+//             global -> LDS directly
+//   A_REG16   bf16 dy of any alignment, through registers
+//   A_REG32   fp32 dy through registers, as three bf16 pieces that sum to it
+//             exactly (8 significant bits each): K is walked three times.
+//
+// K may be split over workgroups that then leave partial tiles in the
+// workspace (PART); linear8_join_kernel adds them in order.
 #pragma once
 
 #include "device_common.hpp"
+#include "gemm.hpp"
 #include "kernel_args.hpp"
+#include "row_ops.hpp"
 
 namespace muon {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
-__device__ __forceinline__ float any_f32(const void* p, int dt, int64_t i) {
-  return dt == DT_F32 ? as_global(static_cast<const float*>(p))[i] : to_f32(as_global(static_cast<const bf16*>(p))[i]);
+enum : int { L8_Y = 0, L8_DW = 1, L8_DX = 2 };
+enum : int { A_DIRECT = 0, A_REG16 = 1, A_REG32 = 2 };
+
+template <bool INT> struct Acc8;
+template <> struct Acc8<true> {
+  typedef i32x16 type;
+  __device__ __forceinline__ static void mma(i32x16& c, const u32x4& a, const u32x4& b) {
+    c = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+  }
+};
+template <> struct Acc8<false> {
+  typedef f32x16 type;
+  __device__ __forceinline__ static void mma(f32x16& c, const u32x4& a, const u32x4& b) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                0, 0);
+  }
+};
+
+// Piece p (0, 1, 2) of fp32 x as bf16 bits in the high half of the result.
+// Cutting off mantissa bits leaves at most 24 - 8 - 8 = 8 significant bits
+// for the last piece, so the three add up to x exactly; an infinity or NaN is
+// all in the first piece (a NaN keeps a mantissa bit).
+__device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  if ((u & 0x7f800000u) == 0x7f800000u) return p ? 0u : (u | ((u & 0x7fffffu) ? 0x400000u : 0u));
+  uint32_t hi = u & 0xffff0000u;
+  if (p == 0) return hi;
+  float r = x - __builtin_bit_cast(float, hi);
+  hi = __builtin_bit_cast(uint32_t, r) & 0xffff0000u;
+  if (p == 1) return hi;
+  r -= __builtin_bit_cast(float, hi);
+  return __builtin_bit_cast(uint32_t, r) & 0xffff0000u;
 }
 
-template <typename TO>
-__global__ __launch_bounds__(256) void linear8_forward_kernel(const Linear8Args a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int l32 = lane & 31, half = lane >> 5;
-  const int64_t t0 = (int64_t)blockIdx.y * 64 + (wave >> 1) * 32;
-  const int64_t n0 = (int64_t)blockIdx.x * 64 + (wave & 1) * 32;
-  const bool tok = t0 + l32 < a.tokens, ch = n0 + l32 < a.out;
-  const int8_t* qa = a.q + (t0 + l32) * a.ldq;
-  const int8_t* wb = a.w + (n0 + l32) * a.ldw;
-  i32x16 acc;
+// Raw 8 elements of dy of which the first `valid` exist (may be <= 0 or >= 8).
+template <int ASRC> struct Dy8;
+template <> struct Dy8<A_REG16> {
+  u32x4 w;
+  __device__ __forceinline__ void load(const void* base, int64_t off, int valid) {
+    const bf16* p = static_cast<const bf16*>(base) + off;
+    if (valid >= 8) {
+      w = as_global(reinterpret_cast<const u32x4_e2*>(p))->v;
+    } else {
+      w = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0;
-  for (int k = 0; k < a.in; k += 32) {
-    const int kk = k + 16 * half;
-    i32x4 fa = {0, 0, 0, 0}, fb = {0, 0, 0, 0};
-    // a 16-byte chunk that starts before the end of the row is inside its storage
-    if (tok && kk < a.in) fa = *as_global(reinterpret_cast<const i32x4*>(qa + kk));
-    if (ch && kk < a.in) fb = *as_global(reinterpret_cast<const i32x4*>(wb + kk));
-    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa, fb, acc, 0, 0, 0);
-  }
-  if (!ch) return;
-  const int64_t n = n0 + l32;
-  const float ws = as_global(a.wscale)[n];
-  const float b = a.bias ? any_f32(a.bias, a.bias_dtype, n) : 0.f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int64_t t = t0 + 8 * (e >> 2) + 4 * half + (e & 3);
-    if (t < a.tokens)
-      as_global(static_cast<TO*>(a.o))[t * a.ldo + n] = from_f32<TO>((float)acc[e] * as_global(a.scale)[t] * ws + b);
-  }
-}
-
-// WG: rows of the result are outputs n, summed over tokens; else rows are
-// tokens, summed over outputs.
-template <bool WG, typename TD, typename TO>
-__global__ __launch_bounds__(256) void linear8_grad_kernel(const Linear8Args a) {
-  __shared__ float sa[16][65], sq[16][65];
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-  const int64_t rows = WG ? a.out : a.tokens, sum = WG ? a.tokens : a.out;
-  const int8_t* q = WG ? a.q : a.w;
-  const float* sc = WG ? a.scale : a.wscale;
-  const int64_t ldq = WG ? a.ldq : a.ldw;
-  const TD* dy = static_cast<const TD*>(a.dy);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t s0 = 0; s0 < sum; s0 += 16) {
-    for (int i = threadIdx.x; i < 16 * 64; i += 256) {
-      int ss, rr;
-      if (WG) { ss = i >> 6; rr = i & 63; } else { ss = i & 15; rr = i >> 4; }
-      const int64_t s = s0 + ss, r = r0 + rr;
-      sa[ss][rr] = s < sum && r < rows ? to_f32(as_global(dy)[WG ? s * a.lddy + r : r * a.lddy + s]) : 0.f;
-      const int64_t sq_ = s0 + (i >> 6), c = c0 + (i & 63);
-      sq[i >> 6][i & 63] =
-          sq_ < sum && c < a.in ? (float)as_global(q)[sq_ * ldq + c] * as_global(sc)[sq_] : 0.f;
+      for (int e = 0; e < 7; ++e)
+        if (e < valid) w[e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(p))[e] << (16 * (e & 1));
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sq[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
   }
+  __device__ __forceinline__ u32x4 piece(int) const { return w; }
+};
+template <> struct Dy8<A_REG32> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const void* base, int64_t off, int valid) {
+    const float* p = static_cast<const float*>(base) + off;
+    if (valid >= 8) {
+      a = as_global(reinterpret_cast<const f32x4_e4*>(p))->v;
+      b = as_global(reinterpret_cast<const f32x4_e4*>(p + 4))->v;
+    } else {
+      a = b = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = r0 + ty * 4 + i, c = c0 + tx * 4 + j;
-      if (r < rows && c < a.in) {
-        TO* o = static_cast<TO*>(a.o) + r * a.ldo + c;
-        const float old = WG && a.accumulate ? to_f32(*as_global(o)) : 0.f;
-        *as_global(o) = from_f32<TO>(acc[i][j] + old);
+      for (int e = 0; e < 4; ++e) {
+        if (e < valid) a[e] = as_global(p)[e];
+        if (e + 4 < valid) b[e] = as_global(p)[e + 4];
       }
     }
+  }
+  __device__ __forceinline__ u32x4 piece(int p) const {
+    u32x4 w;
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = (bf16_piece(v[2 * j], p) >> 16) | bf16_piece(v[2 * j + 1], p);
+    return w;
+  }
+};
+template <> struct Dy8<A_DIRECT> {};
+
+// Workgroup -> (split, tile row, tile column), spread over the XCDs in
+// groups of 4 tile rows as the optimizer's products are (gemm.hpp).
+__device__ __forceinline__ void linear8_tile(const Linear8Args& a, int& split, int& bi, int& bj) {
+  const int per = a.tilesM * a.tilesN, tot = per * a.splits;
+  const int b = blockIdx.x, xcd = b & 7, loc = b >> 3;
+  const int S = 8 * a.tilesN;
+  const int full = tot / (8 * S);
+  int logical;
+  if (loc < full * S) {
+    logical = (loc / S) * 8 * S + xcd * S + loc % S;
+  } else {
+    const int rest = tot - full * 8 * S, q = rest >> 3, r = rest & 7;
+    logical = full * 8 * S + xcd * q + (xcd < r ? xcd : r) + (loc - full * S);
+  }
+  split = __builtin_amdgcn_readfirstlane(logical / per);
+  const int tt = __builtin_amdgcn_readfirstlane(logical - split * per);
+  constexpr int GROUP = 4;
+  const int g = tt / (GROUP * a.tilesN);
+  const int first = g * GROUP;
+  const int gm = min(a.tilesM - first, GROUP);
+  const int w = tt - g * GROUP * a.tilesN;
+  bi = __builtin_amdgcn_readfirstlane(first + w % gm);
+  bj = __builtin_amdgcn_readfirstlane(w / gm);
+}
+
+template <int MODE, int ASRC, int T, int NW, typename TO, bool PART>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(T == 128 ? 2 : NW / 4, T == 128 ? 2 : NW / 4)))
+void linear8_kernel(const Linear8Args a) {
+  constexpr bool INT = MODE == L8_Y;
+  constexpr bool AKM = MODE == L8_DW;      // A lies K-major
+  constexpr int ES = INT ? 1 : 2;
+  constexpr int EPC = 16 / ES;             // elements per 16-byte chunk
+  constexpr int BK = 8 * EPC;              // K per stage
+  constexpr int WGN = NW / 2;              // waves: 2 along M, NW / 2 along N
+  constexpr int WTM = T / 64, WN = T / WGN, WTN = WN / 32;
+  constexpr int OPS = T * 8;               // chunks of one operand's stage
+  constexpr int STG = 2 * OPS;
+  constexpr int NQ = OPS / (64 * NW);      // 16-byte pieces of one operand a thread moves per stage
+  constexpr int NDR = WTM + WTN, NPAIR = WTM * WTN;
+  constexpr int CR = T / 8;                // chunks per K-row of a K-major stage
+  constexpr int RPC = 64 / CR;             // K-rows per wave-wide copy
+  constexpr int PIECES = ASRC == A_REG32 ? 3 : 1;
+  constexpr int RSTEP = 64 * NW / CR;      // rows between a thread's pieces of the 8-bit operand
+  static_assert(NQ * 8 * NW == T && RSTEP % 4 == 0, "chunks shared out evenly");
+  __shared__ u32x4 ring[2][STG];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wid / WGN, wn = wid % WGN;
+  const int half = lane >> 5, l32 = lane & 31;
+  int split, bi, bj;
+  linear8_tile(a, split, bi, bj);
+  const int row0 = bi * T, col0 = bj * T;
+
+  // stages of this split: K-stages [ks0, ks1), walked once per piece of dy
+  const int nks = (a.K + BK - 1) / BK;
+  const int ks0 = min(split * a.per_split, nks), ks1 = min(ks0 + a.per_split, nks);
+  const int nst = (ks1 - ks0) * PIECES;
+
+  auto swz_t = [](int krow) { return ((krow & 1) << 2) ^ (((krow >> 1) & 1) * 10); };
+
+  // ---- operand A (and B for L8_Y), row-major: rows of the tile
+  const int rows_a = min(T, a.M - row0);
+  const char* Abase = static_cast<const char*>(a.A) + (AKM ? 0 : (int64_t)row0 * a.lda * ES);
+  const __amdgpu_buffer_rsrc_t ars = make_rsrc(
+      Abase, INT ? (uint32_t)((int64_t)rows_a * a.lda)
+                 : (uint32_t)((((int64_t)rows_a - 1) * a.lda + a.K) * 2));  // dy's last row ends at K
+  const int rows_b = min(T, a.N - col0);
+  const __amdgpu_buffer_rsrc_t brs =
+      make_rsrc(a.B + (INT ? (int64_t)col0 * a.ldb : 0), (uint32_t)((int64_t)rows_b * a.ldb));
+  const int crow = wid * (8 * NQ) + (lane >> 3);              // tile row of copy 0
+  const int ck[2] = {((lane & 7) ^ (lane >> 3)) * EPC, ((lane & 7) ^ (lane >> 3) ^ 1) * EPC};
+  auto copy_row_major = [&](__amdgpu_buffer_rsrc_t r, int64_t ld, int region, int q, int v, int ks) {
+    const int k = ks * BK + ck[q & 1];
+    const uint32_t off = k < a.K ? (uint32_t)(((crow + 8 * q) * ld + k) * ES) : OOB;
+    copy16_to_lds(r, &ring[v & 1][region + (wid * NQ + q) * 64], off);
+  };
+  // ---- operand A of dW, K-major: rows of the stage, columns row0 .. of dy
+  uint32_t tb[2] = {0u, 0u};
+  if constexpr (AKM && ASRC == A_DIRECT) {
+#pragma unroll
+    for (int par = 0; par < 2; ++par) {
+      const int krow = (wid * NQ + par) * RPC + lane / CR;
+      const int col = row0 + ((lane % CR) ^ swz_t(krow)) * 8;
+      tb[par] = col < a.M ? (uint32_t)(((int64_t)krow * a.lda + col) * 2) : OOB;
+    }
+  }
+  auto copy_a = [&](int q, int v, int ks) {
+    if constexpr (AKM) {
+      const int nk = max(0, min(BK, a.K - ks * BK));
+      const char* p = static_cast<const char*>(a.A) + (int64_t)ks * BK * a.lda * 2;
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(p, nk ? (uint32_t)((((int64_t)nk - 1) * a.lda + a.M) * 2) : 0u);
+      copy16_to_lds(r, &ring[v & 1][(wid * NQ + q) * 64], tb[q & 1] + (uint32_t)((int64_t)((q & ~1) * RPC) * a.lda * 2));
+    } else {
+      copy_row_major(ars, a.lda, 0, q, v, ks);
+    }
+  };
+  // through registers: the same chunks, loaded ahead of being written; fp32 in
+  // two halves, since all four chunks do not fit beside the accumulators
+  constexpr int NH = ASRC == A_REG32 ? NQ / 2 : NQ;
+  Dy8<ASRC> da[NH];
+  auto load_a = [&](int q, int ks) {
+    if constexpr (ASRC != A_DIRECT) {
+      if constexpr (AKM) {
+        const int slot = (wid * NQ + q) * 64 + lane;
+        const int krow = slot / CR, col = row0 + ((slot % CR) ^ swz_t(krow)) * 8;
+        const int k = ks * BK + krow;
+        da[q % NH].load(a.A, (int64_t)k * a.lda + col, k < a.K ? a.M - col : 0);
+      } else {
+        const int r = crow + 8 * q, k = ks * BK + ck[q & 1];
+        da[q % NH].load(a.A, (int64_t)(row0 + r) * a.lda + k, r < rows_a ? a.K - k : 0);
+      }
+    }
+  };
+  auto store_a = [&](int q, int v, int piece) {
+    if constexpr (ASRC != A_DIRECT) ring[v & 1][(wid * NQ + q) * 64 + lane] = da[q % NH].piece(piece);
+  };
+
+  // ---- 8-bit operand of the gradients: piece i of a thread is row RSTEP i +
+  // tid / CR of the stage, columns 8 (tid % CR) .. + 7 of the tile
+  u32x2 bq[NQ];
+  float bs[NQ];
+  const int brow = tid / CR, bcol = (tid % CR) * 8;
+  const uint32_t boff = col0 + bcol < a.ldb ? (uint32_t)(brow * a.ldb + col0 + bcol) : OOB;
+  const int bslot = OPS + brow * CR + ((tid % CR) ^ swz_t(brow));
+  auto load_b = [&](int ks) {
+    if constexpr (!INT) {
+      const int nk = max(0, min(BK, a.K - ks * BK));
+      const __amdgpu_buffer_rsrc_t r =
+          make_rsrc(a.B + (int64_t)ks * BK * a.ldb, (uint32_t)((int64_t)nk * a.ldb));
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.sb + (int64_t)ks * BK, (uint32_t)(nk * 4));
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        bq[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, boff + (uint32_t)(i * RSTEP * a.ldb), 0, 0));
+        bs[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(RSTEP * i + brow) * 4, 0, 0));
+      }
+    }
+  };
+  u32x4 bw;
+  auto convert_b = [&](int idx, int v) {  // pair idx of the thread's 8 NQ values; the fourth pair of a piece stores it
+    if constexpr (!INT) {
+      const int i = idx >> 2, j = idx & 3;
+      const uint32_t w = bq[i][j >> 1] >> (16 * (j & 1));
+      bw[j] = pack2<bf16>((float)(int8_t)w * bs[i], (float)(int8_t)(w >> 8) * bs[i]);
+      if (j == 3) ring[v & 1][bslot + i * RSTEP * CR] = bw;
+    }
+  };
+
+  typename Acc8<INT>::type acc[WTM][WTN];
+#pragma unroll
+  for (int i = 0; i < WTM; ++i)
+#pragma unroll
+    for (int j = 0; j < WTN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  // ---- fragments, double buffered by k-step
+  u32x4 fa[2][WTM], fb[2][WTN];
+  const int rswz = (l32 & 7) ^ ((l32 >> 3) & 1);
+  constexpr int ROWB = CR * 16;
+  uint32_t tbase[NDR];
+#pragma unroll
+  for (int r = 0; r < NDR; ++r) {
+    const int e = (lane >> 2) & 3, q = lane & 3;
+    const int region = r < WTM ? 0 : OPS;
+    const int rb = r < WTM ? wm * (T / 2) + r * 32 : wn * WN + (r - WTM) * 32;
+    const int col = rb + 16 * ((lane >> 4) & 1) + 4 * q;
+    tbase[r] = (uint32_t)(uintptr_t)(lds_ptr_t)&ring[0][0] +
+               (uint32_t)(region * 16 + (8 * half + e) * ROWB + ((col >> 3) ^ swz_t(e)) * 16 + (col & 7) * 2);
+  }
+  auto read_one = [&](int r, int v, int s, int slot) {
+    const bool isA = r < WTM;
+    const int rb = isA ? wm * (T / 2) + r * 32 : wn * WN + (r - WTM) * 32;
+    u32x4 f;
+    if (INT || (isA && !AKM)) {
+      f = ring[v & 1][(isA ? 0 : OPS) + (rb + l32) * 8 + ((2 * s + half) ^ rswz)];
+    } else {
+      const uint32_t p = tbase[r] + (uint32_t)((v & 1) * STG * 16);
+#pragma unroll
+      for (int kq = 0; kq < 2; ++kq) {
+        const uint2 w = lds_read_tr16_step<ROWB>(p, 2 * s + kq);
+        f[2 * kq] = w.x;
+        f[2 * kq + 1] = w.y;
+      }
+    }
+    if (isA) fa[slot][r] = f;
+    else fb[slot][r - WTM] = f;
+  };
+  // reads in the order of first use: A0, B0 .. B(WTN-1), A1 .. A(WTM-1)
+  auto ro = [](int p) { return p == 0 ? 0 : (p <= WTN ? WTM + p - 1 : p - WTN); };
+  // The compiler does not track the transposed reads.  LDS instructions of a
+  // wave complete in order, so before MFMA p it is enough that at most as
+  // many are outstanding as were issued after the fragment that p is the
+  // first to use: this step's later fragments and the next step's first p
+  // ones (two instructions each; untransposed reads and register writes are
+  // not counted, which only waits for more).  Waiting for all of them once
+  // per step cost 0.2 us of a 1.6 us stage.
+  auto wait_frag = [&](auto pc) {
+    if constexpr (!INT) {
+      constexpr int p = decltype(pc)::value;
+      constexpr int i = p / WTN, j = p % WTN;
+      constexpr bool needA = j == 0 && AKM, needB = i == 0;  // first uses among the transposed
+      if constexpr (needA || needB) {
+        // position of that fragment in the reading order
+        constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : WTN + i);
+        constexpr int later_a = AKM ? (WTM - 1 - (at > WTN ? at - WTN : 0)) : 0;
+        constexpr int later_b = at <= WTN ? WTN - at : 0;
+        constexpr int now = p < NDR ? p : NDR;  // reads issued so far in this step
+        constexpr int now_a = AKM ? (now > 0 ? 1 : 0) + (now > WTN + 1 ? now - WTN - 1 : 0) : 0;
+        constexpr int now_b = now <= 1 ? 0 : (now - 1 < WTN ? now - 1 : WTN);
+        constexpr int n = 2 * (later_a + later_b + now_a + now_b);
+        __builtin_amdgcn_s_waitcnt(0xc07f | ((n < 15 ? n : 15) << 8));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  auto mfma_pair = [&](int p, int slot) {
+    Acc8<INT>::mma(acc[p / WTN][p % WTN], fa[slot][p / WTN], fb[slot][p % WTN]);
+  };
+  // stage v -> (K-stage, piece); v past the end only refills a slot nobody reads
+  int ksn = ks0, pcn = 0;  // of the stage that is loaded next
+  auto advance = [&] {
+    if (++ksn == ks1) {
+      ksn = ks0;
+      ++pcn;
+    }
+  };
+
+  if (nst > 0) {
+    // ---- prologue: stage 0 in LDS, stage 1 on its way
+    if constexpr (INT) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) copy_row_major(ars, a.lda, 0, q, v, ks0 + v);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) copy_row_major(brs, a.ldb, OPS, q, v, ks0 + v);
+      }
+      ksn = ks0 + 2;
+      wait_vmcnt<2 * NQ>();
+    } else {
+      load_b(ksn);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if constexpr (ASRC == A_DIRECT) {
+          copy_a(q, 0, ksn);
+        } else {
+          load_a(q, ksn);
+          store_a(q, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * NQ; ++i) convert_b(i, 0);
+      advance();
+      wait_vmcnt<0>();
+      load_b(ksn);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        if constexpr (ASRC == A_DIRECT) copy_a(q, 1, ksn);
+#pragma unroll
+      for (int q = 0; q < NH; ++q) load_a(q, ksn);
+    }
+    int ks_held = ksn, pc_held = pcn;  // stage whose dy is (half) held in registers
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < NDR; ++r) read_one(ro(r), 0, 0, 0);
+
+    for (int v = 0; v < nst; ++v) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        // loads of dy branch at the edges: no untracked read is under way then
+        if (ASRC == A_REG32 && s == 1) {
+          wait_lgkm0();
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int q = 0; q < NH; ++q) store_a(q, v + 1, pc_held);
+#pragma unroll
+          for (int q = NH; q < NQ; ++q) load_a(q, ks_held);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        static_for<0, NPAIR>([&](auto pc) __attribute__((always_inline)) {
+          constexpr int p = decltype(pc)::value;
+          wait_frag(pc);
+          mfma_pair(p, s & 1);
+          // the fragment reads of a step before its register writes: those wait
+#pragma unroll
+          for (int r = p; r < NDR; r += NPAIR) read_one(ro(r), v, s + 1, (s + 1) & 1);
+          if constexpr (!INT) {
+            // 4 NQ pairs of B over the 3 NPAIR MFMAs, after a head start for the loads
+            constexpr int SLOTS = 3 * NPAIR, HEAD = NPAIR >= 8 ? 6 : 2;
+            constexpr int PER = (4 * NQ + SLOTS - HEAD - 1) / (SLOTS - HEAD);
+            const int at = s * NPAIR + p - HEAD;
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+              if (at >= 0 && at * PER + c < 4 * NQ) convert_b(at * PER + c, v + 1);
+            if constexpr (ASRC != A_DIRECT) {
+              if (s == 2 && p < NH) store_a(NQ - NH + p, v + 1, pc_held);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      }
+      // stage v + 1 is whole and this wave is done reading stage v; after the
+      // barrier that holds for every wave
+      wait_vmcnt_lgkm0<0>();
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (!INT) {
+        advance();
+        ks_held = ksn;
+        pc_held = pcn;
+        load_b(ksn);
+        if constexpr (ASRC != A_DIRECT) {
+#pragma unroll
+          for (int q = 0; q < NH; ++q) load_a(q, ksn);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < NPAIR; ++p) {
+        mfma_pair(p, 1);
+        if constexpr (INT) {
+#pragma unroll
+          for (int c = p; c < 2 * NQ; c += NPAIR) {
+            if (c < NQ) copy_row_major(ars, a.lda, 0, c, v + 2, ksn);
+            else copy_row_major(brs, a.ldb, OPS, c - NQ, v + 2, ksn);
+          }
+        } else if constexpr (ASRC == A_DIRECT) {
+          if (p < NQ) copy_a(p, v + 2, ksn);
+        }
+#pragma unroll
+        for (int r = p; r < NDR; r += NPAIR) read_one(ro(r), v + 1, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (INT) ++ksn;
+    }
+    wait_vmcnt_lgkm0<0>();  // trailing copies and reads
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __syncthreads();
+
+  // ---- epilogue: 32-row strips of a wave through its part of the ring, then
+  // rows of 8 values per lane
+  constexpr int SROW = WN + 8;
+  static_assert(NW * 32 * SROW * 4 <= 2 * STG * 16, "strips fit in the ring");
+  constexpr int CW = WN / 8, DRS = 64 / CW, NT = 32 / DRS;
+  float* strip = reinterpret_cast<float*>(&ring[0][0]) + wid * (32 * SROW);
+  const int dr0 = lane / CW, dc8 = (lane % CW) * 8;
+  const int gj = col0 + wn * WN + dc8;
+  float cs[8], cb[8];
+  if constexpr (INT && !PART) {
+    if (gj < a.N) {
+      piece_load(a.sb, gj, a.N, cs);
+      if (a.bias) vec_load(a.bias, a.bias_dtype, gj, a.N, cb);
+    }
+  }
+  static_for<0, WTM>([&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    const int gr0 = row0 + wm * (T / 2) + i * 32;
+#pragma unroll
+    for (int j = 0; j < WTN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float x;
+        if constexpr (INT && PART) x = __builtin_bit_cast(float, (int32_t)acc[i][j][e]);
+        else x = (float)acc[i][j][e];
+        strip[((e >> 2) * 8 + half * 4 + (e & 3)) * SROW + j * 32 + l32] = x;
+      }
+    wave_lds_sync();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = gr0 + dr0 + DRS * t;
+      const float* sp = strip + (dr0 + DRS * t) * SROW + dc8;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(sp);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(sp + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (r < a.M && gj < a.N) {
+        if constexpr (PART) {
+          float* o = a.ws + ((int64_t)split * a.M + r) * a.ldws + gj;
+          *as_global(reinterpret_cast<f32x4*>(o)) = lo;
+          *as_global(reinterpret_cast<f32x4*>(o + 4)) = hi;
+        } else {
+          TO* o = static_cast<TO*>(a.o) + (int64_t)r * a.ldo;
+          if constexpr (INT) {
+            const float sr = as_global(a.sa)[r];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * sr * cs[e];
+            if (a.bias) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] += cb[e];
+            }
+          } else if (a.accumulate) {
+            float old[8];
+            piece_load(o, gj, a.N, old);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += old[e];
+          }
+          piece_store(o, gj, a.N, v);
+        }
+      }
+    }
+    wave_lds_sync();
+  });
+}
+
+// Adds the partial tiles of a split product in order and finishes it as the
+// epilogue above does.  8 columns per thread.
+template <bool INT, typename TO>
+__global__ __launch_bounds__(256) void linear8_join_kernel(const Linear8Args a) {
+  const int per_row = (a.N + 7) / 8;
+  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (p >= (int64_t)a.M * per_row) return;
+  const int64_t r = p / per_row;
+  const int c = (int)(p - r * per_row) * 8;
+  const float* w = a.ws + r * a.ldws + c;
+  const int64_t step = (int64_t)a.M * a.ldws;
+  float v[8];
+  if constexpr (INT) {
+    int32_t s[8] = {};
+    for (int z = 0; z < a.splits; ++z)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const i32x4 x = *as_global(reinterpret_cast<const i32x4*>(w + z * step + 4 * h));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[4 * h + e] += x[e];
+      }
+    const float sr = as_global(a.sa)[r];
+    float cs[8];
+    piece_load(a.sb, c, a.N, cs);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)s[e] * sr * cs[e];
+    if (a.bias) {
+      vec_load(a.bias, a.bias_dtype, c, a.N, cs);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += cs[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(w + z * step + 4 * h));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * h + e] += x[e];
+      }
+  }
+  TO* o = static_cast<TO*>(a.o) + r * a.ldo;
+  if (!INT && a.accumulate) {
+    float old[8];
+    piece_load(o, c, a.N, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += old[e];
+  }
+  piece_store(o, c, a.N, v);
 }
 
 }  // namespace muon

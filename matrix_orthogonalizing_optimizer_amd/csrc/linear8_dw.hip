@@ -1,0 +1,8 @@
+// Weight gradient of the linear layer on 8-bit rows.
+#include "linear8_inst.hpp"
+
+namespace muon {
+hipError_t launch_linear8_dw(int tile, int asrc, int odt, const Linear8Args& a, hipStream_t s) {
+  return linear8_grad_any<L8_DW>(tile, asrc, odt, a, s);
+}
+}  // namespace muon

@@ -44,6 +44,43 @@ size_t norm_ws(int64_t rows, int64_t cols) {
   return (size_t)norm_parts(rows, cols) * (size_t)cols * 2 * sizeof(float) + WS_ALIGN;
 }
 
+// Tile and split of a product of the 8-bit linear layer; depends on the sizes
+// only, so that the workspace query and the call agree.
+struct Linear8Plan {
+  int tile, splits, per_split;
+  int64_t ldws;
+  size_t bytes;
+};
+Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in) {
+  const int64_t M = pass == MUON_LINEAR8_WEIGHT_GRAD ? out : tokens;
+  const int64_t N = pass == MUON_LINEAR8_FORWARD ? out : in;
+  const int64_t K = pass == MUON_LINEAR8_FORWARD ? in : pass == MUON_LINEAR8_WEIGHT_GRAD ? tokens : out;
+  const int64_t nks = (K + (pass == MUON_LINEAR8_FORWARD ? 128 : 64) - 1) / (pass == MUON_LINEAR8_FORWARD ? 128 : 64);
+  Linear8Plan p;
+  auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
+  p.tile = tiles(256) >= 192 ? 256 : 128;
+  const int64_t slots = p.tile == 256 ? 256 : 512;
+  int64_t z = std::max<int64_t>(1, slots / std::max<int64_t>(1, tiles(p.tile)));
+  z = std::max<int64_t>(1, std::min<int64_t>(z, nks / 4));
+  p.per_split = (int)std::max<int64_t>(1, (nks + z - 1) / z);
+  p.splits = (int)std::max<int64_t>(1, (nks + p.per_split - 1) / p.per_split);
+  p.ldws = (N + 7) / 8 * 8;
+  p.bytes = p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)p.ldws * sizeof(float) + WS_ALIGN : 0;
+  return p;
+}
+
+// Fills the shared part of the arguments; false if the grid does not fit.
+bool linear8_args(const Linear8Plan& p, int64_t M, int64_t N, int64_t K, void* workspace, Linear8Args& a) {
+  const int64_t tm = (M + p.tile - 1) / p.tile, tn = (N + p.tile - 1) / p.tile;
+  if (tm * tn * p.splits > 0x7fffffff) return false;
+  a.M = (int32_t)M; a.N = (int32_t)N; a.K = (int32_t)K;
+  a.tilesM = (int32_t)tm; a.tilesN = (int32_t)tn;
+  a.splits = p.splits; a.per_split = p.per_split;
+  a.ldws = p.ldws;
+  a.ws = p.splits > 1 ? reinterpret_cast<float*>(ws_base(workspace)) : nullptr;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -182,7 +219,7 @@ muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t o
   if (pass < MUON_LINEAR8_FORWARD || pass > MUON_LINEAR8_INPUT_GRAD) return MUON_E_METHOD;
   if (!side_ok(tokens) || !side_ok(out) || !side_ok(in) || (pass == MUON_LINEAR8_FORWARD && in > MAX_IN))
     return MUON_E_SHAPE;
-  *bytes = 0;
+  *bytes = tokens && out && in ? linear8_plan(pass, tokens, out, in).bytes : 0;
   return MUON_OK;
 }
 
@@ -198,18 +235,18 @@ muon_status muon_linear8_forward(const int8_t* q, int64_t ldq, const float* scal
   if (!at(scale, 4) || !at(wscale, 4) || !at(y, esize(dtype)) || (bias && !at(bias, esize(bias_dtype))) ||
       (in > 0 && (!at(q, 16) || !at(wq, 16))))
     return MUON_E_ARG;
-  (void)workspace;
-  (void)workspace_bytes;
+  const Linear8Plan p = linear8_plan(MUON_LINEAR8_FORWARD, tokens, out, in);
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MUON_E_WORKSPACE;
   Linear8Args a;
   std::memset(&a, 0, sizeof(a));
-  a.q = q; a.ldq = ldq; a.scale = scale;
-  a.w = wq; a.ldw = ldw; a.wscale = wscale;
+  if (!linear8_args(p, tokens, out, in, workspace, a)) return MUON_E_SHAPE;
+  a.A = q; a.lda = ldq; a.sa = scale;
+  a.B = wq; a.ldb = ldw; a.sb = wscale;
   a.bias = bias; a.bias_dtype = dev_dt(bias_dtype);
   a.o = y; a.ldo = ldy;
-  a.tokens = (int32_t)tokens; a.out = (int32_t)out; a.in = (int32_t)in;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
-  return done(timed(F_LINEAR8_Y, f, 0.0, s, [&] { return launch_linear8_forward(dev_dt(dtype), a, s); }));
+  return done(timed(F_LINEAR8_Y, f, 0.0, s, [&] { return launch_linear8_forward(p.tile, dev_dt(dtype), a, s); }));
 }
 
 static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* q,
@@ -224,23 +261,24 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
   if (rows == 0 || in == 0) return MUON_OK;
   if (!at(o, esize(o_dtype)) || (sum > 0 && (!at(dy, esize(dy_dtype)) || !at(q, 16) || !at(scale, 4))))
     return MUON_E_ARG;
-  (void)workspace;
-  (void)workspace_bytes;
+  const int pass = weight ? MUON_LINEAR8_WEIGHT_GRAD : MUON_LINEAR8_INPUT_GRAD;
+  const Linear8Plan p = linear8_plan(pass, tokens, out, in);
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MUON_E_WORKSPACE;
   Linear8Args a;
   std::memset(&a, 0, sizeof(a));
-  a.dy = dy; a.lddy = lddy;
-  if (weight) {
-    a.q = q; a.ldq = ldq; a.scale = scale;
-  } else {
-    a.w = q; a.ldw = ldq; a.wscale = scale;
-  }
+  if (!linear8_args(p, rows, in, sum, workspace, a)) return MUON_E_SHAPE;
+  a.A = dy; a.lda = lddy;
+  a.B = q; a.ldb = ldq; a.sb = scale;
   a.o = o; a.ldo = ldo;
   a.accumulate = accumulate;
-  a.tokens = (int32_t)tokens; a.out = (int32_t)out; a.in = (int32_t)in;
+  // direct copies of dy take 16-byte pieces that lie wholly inside a row
+  const int asrc = dy_dtype == MUON_F32 ? 2 : at(dy, 16) && lddy % 8 == 0 && out % 8 == 0 ? 0 : 1;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
-  return done(timed(weight ? F_LINEAR8_DW : F_LINEAR8_DX, f, 0.0, s,
-                    [&] { return launch_linear8_grad(weight, dev_dt(dy_dtype), dev_dt(o_dtype), a, s); }));
+  return done(timed(weight ? F_LINEAR8_DW : F_LINEAR8_DX, f, 0.0, s, [&] {
+    return weight ? launch_linear8_dw(p.tile, asrc, dev_dt(o_dtype), a, s)
+                  : launch_linear8_dx(p.tile, asrc, dev_dt(o_dtype), a, s);
+  }));
 }
 
 muon_status muon_linear8_weight_grad(const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* q, int64_t ldq,

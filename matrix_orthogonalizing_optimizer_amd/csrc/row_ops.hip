@@ -34,10 +34,10 @@ template <typename T, int KIND> hipError_t forward(const RowArgs& a, hipStream_t
 }
 
 template <typename T, int KIND> hipError_t backward(const NormBwdArgs& a, int parts, hipStream_t s) {
-  if (a.cols > ROW_MAX_COLS) {
+  if (a.cols > NORM_BWD_MAX_COLS) {
     // the column sums first: dx may overwrite dy
     if (a.partials) {
-      hipLaunchKernelGGL((norm_columns_long_kernel<T, KIND>), dim3((unsigned)((a.cols + 255) / 256), (unsigned)parts),
+      hipLaunchKernelGGL((norm_columns_long_kernel<T, KIND>), dim3((unsigned)((a.cols + 2047) / 2048), (unsigned)parts),
                          dim3(256), 0, s, a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -47,9 +47,12 @@ template <typename T, int KIND> hipError_t backward(const NormBwdArgs& a, int pa
   }
   return by_width(a.cols, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
-    hipLaunchKernelGGL((norm_backward_kernel<T, KIND, G, NV>), dim3((unsigned)parts), dim3(G < 256 ? 256 : G), 0, s,
-                       a);
-    return hipGetLastError();
+    if constexpr (G <= 512) {  // 512 x 2 pieces cover NORM_BWD_MAX_COLS
+      hipLaunchKernelGGL((norm_backward_kernel<T, KIND, G, NV>), dim3((unsigned)parts), dim3(G < 256 ? 256 : G), 0, s,
+                         a);
+      return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
   });
 }
 
@@ -76,8 +79,8 @@ hipError_t launch_norm_backward(int kind, int dt, const NormBwdArgs& a, int part
 
 hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s) {
   const dim3 g((unsigned)((a.cols + 63) / 64), a.dbeta ? 2 : 1);
-  if (vec_dtype == DT_BF16) hipLaunchKernelGGL((norm_columns_join_kernel<bf16>), g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((norm_columns_join_kernel<float>), g, dim3(256), 0, s, a);
+  if (vec_dtype == DT_BF16) hipLaunchKernelGGL((norm_columns_join_kernel<bf16>), g, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((norm_columns_join_kernel<float>), g, dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

@@ -9,7 +9,7 @@
 // All of it is bound by HBM: a row is read once and kept in registers (fp32)
 // by a group of G threads, G = 64 (one wave, no barrier) up to 1024 columns
 // and wider groups above, so that a thread holds at most two pieces of 8
-// columns.  Rows longer than 16384 columns are read again for each pass.
+// columns.  Rows longer than that allows are read again for each pass.
 #pragma once
 
 #include "device_common.hpp"
@@ -22,18 +22,22 @@ constexpr int ROW_VE = 8;  // columns per piece
 // Vectors at the alignment of their elements only: global accesses may be
 // unaligned on gfx950, so rows of odd widths and odd starts take the same
 // path as aligned ones.
-typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
+struct __attribute__((packed, aligned(2))) u32x4_e2 {
+  u32x4 v;
+};
+struct __attribute__((packed, aligned(4))) f32x4_e4 {
+  f32x4 v;
+};
 
 template <typename T> __device__ __forceinline__ void row_load8(const T* p, float (&v)[8]) {
   if constexpr (sizeof(T) == 2) {
-    const u32x4_e2 w = *as_global(reinterpret_cast<const u32x4_e2*>(p));
+    const u32x4 w = as_global(reinterpret_cast<const u32x4_e2*>(p))->v;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       v[e] = __builtin_bit_cast(float, (e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
   } else {
-    const f32x4_e4 a = *as_global(reinterpret_cast<const f32x4_e4*>(p));
-    const f32x4_e4 b = *as_global(reinterpret_cast<const f32x4_e4*>(p + 4));
+    const f32x4 a = as_global(reinterpret_cast<const f32x4_e4*>(p))->v;
+    const f32x4 b = as_global(reinterpret_cast<const f32x4_e4*>(p + 4))->v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[e + 4] = b[e]; }
   }
@@ -41,13 +45,13 @@ template <typename T> __device__ __forceinline__ void row_load8(const T* p, floa
 
 template <typename T> __device__ __forceinline__ void row_store8(T* p, const float (&v)[8]) {
   if constexpr (sizeof(T) == 2) {
-    u32x4_e2 w;
+    u32x4 w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
-    *as_global(reinterpret_cast<u32x4_e2*>(p)) = w;
+    as_global(reinterpret_cast<u32x4_e2*>(p))->v = w;
   } else {
-    *as_global(reinterpret_cast<f32x4_e4*>(p)) = f32x4_e4{v[0], v[1], v[2], v[3]};
-    *as_global(reinterpret_cast<f32x4_e4*>(p + 4)) = f32x4_e4{v[4], v[5], v[6], v[7]};
+    as_global(reinterpret_cast<f32x4_e4*>(p))->v = f32x4{v[0], v[1], v[2], v[3]};
+    as_global(reinterpret_cast<f32x4_e4*>(p + 4))->v = f32x4{v[4], v[5], v[6], v[7]};
   }
 }
 
@@ -97,10 +101,16 @@ __device__ __forceinline__ void group_sum(float (&v)[N], GroupRed<G, N>& red, in
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      float s = red.slot[buf][0][k];
+      if constexpr (G <= 256) {
+        float s = red.slot[buf][0][k];
 #pragma unroll
-      for (int i = 1; i < G / 64; ++i) s += red.slot[buf][i][k];
-      v[k] = s;
+        for (int i = 1; i < G / 64; ++i) s += red.slot[buf][i][k];
+        v[k] = s;
+      } else {  // many waves: one read per lane and a butterfly, not a register per wave
+        v[k] = red.slot[buf][threadIdx.x & (G / 64 - 1)][k];
+#pragma unroll
+        for (int off = G / 128; off >= 1; off >>= 1) v[k] += __shfl_xor(v[k], off, 64);
+      }
     }
   }
 }
@@ -362,9 +372,44 @@ __global__ __launch_bounds__(256) void row_restore_kernel(const RestoreArgs a) {
   }
 }
 
+// 8 raw elements of T, so that a 16-bit row takes half the registers of its
+// fp32 values while the next row is on its way.
+template <typename T> struct RowRaw {
+  u32x4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* row, int c, int cols) {
+    if (c + 8 <= cols) {
+      if constexpr (sizeof(T) == 2) {
+        w[0] = as_global(reinterpret_cast<const u32x4_e2*>(row + c))->v;
+      } else {
+        w[0] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c))->v);
+        w[1] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c + 4))->v);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < (int)(sizeof(T) / 2); ++h) w[h] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < cols) {
+          if constexpr (sizeof(T) == 2)
+            w[0][e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(row))[c + e] << (16 * (e & 1));
+          else
+            w[e >> 2][e & 3] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
+        }
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 2)
+      return __builtin_bit_cast(float, (e & 1) ? (w[0][e >> 1] & 0xffff0000u) : (w[0][e >> 1] << 16));
+    else
+      return __builtin_bit_cast(f32x4, w[e >> 2])[e & 3];
+  }
+};
+
 // Norm backward: workgroups loop over rows; a thread keeps its columns' gamma
 // and its sums of dy h and dy in registers over all of them, and the sums go
-// to workspace once per workgroup (partials[2][workgroups][cols]).
+// to workspace once per workgroup (partials[2][workgroups][cols]).  The next
+// row's loads are issued before this row's sums, so that few workgroups
+// (and few partial rows) keep enough bytes in flight.
 template <typename T, int KIND, int G, int NV>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const NormBwdArgs a) {
   constexpr int RPW = G < 256 ? 256 / G : 1;
@@ -379,29 +424,44 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
 #pragma unroll
     for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.f;
   }
-  int buf = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < a.rows; row += (int64_t)gridDim.x * RPW) {
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
-    float h[NV][8], g[NV][8];
+  const int64_t stride = (int64_t)gridDim.x * RPW;
+  int64_t row = (int64_t)blockIdx.x * RPW + sub;
+  RowRaw<T> x[NV], dy[NV];
+  float r = 0.f, mean = 0.f;
+  auto fetch = [&](int64_t at) {
+    const T* xp = static_cast<const T*>(a.x) + at * a.ldx;
+    const T* dp = static_cast<const T*>(a.dy) + at * a.lddy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      piece_load(x, (i * G + t) * ROW_VE, a.cols, h[i]);
-      piece_load(dy, (i * G + t) * ROW_VE, a.cols, g[i]);
+      x[i].load(xp, (i * G + t) * ROW_VE, a.cols);
+      dy[i].load(dp, (i * G + t) * ROW_VE, a.cols);
     }
-    const float r = as_global(a.rstd)[row];
-    const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f;
+    r = as_global(a.rstd)[at];
+    if (KIND == 0) mean = as_global(a.mean)[at];
+  };
+  if (row < a.rows) fetch(row);
+  int buf = 0;
+  while (row < a.rows) {
+    const int64_t next = row + stride;
+    RowRaw<T> cx[NV], cd[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      cx[i] = x[i];
+      cd[i] = dy[i];
+    }
+    const float cr = r, cm = mean;
+    if (next < a.rows) fetch(next);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[i][e] = (h[i][e] - mean) * r;
-        sg[i][e] = fmaf(g[i][e], h[i][e], sg[i][e]);
-        if (KIND == 0) sb[i][e] += g[i][e];
-        g[i][e] *= gam[i][e];
-        s[0] = fmaf(g[i][e], h[i][e], s[0]);
-        if (KIND == 0) s[1] += g[i][e];
+        const float h = (cx[i].get(e) - cm) * cr, d = cd[i].get(e);
+        sg[i][e] = fmaf(d, h, sg[i][e]);
+        if (KIND == 0) sb[i][e] += d;
+        const float g = d * gam[i][e];
+        s[0] = fmaf(g, h, s[0]);
+        if (KIND == 0) s[1] += g;
       }
     group_sum<G, 2>(s, red, buf);
     buf ^= 1;
@@ -409,10 +469,278 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
     T* dx = static_cast<T*>(a.dx) + row * a.lddx;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      const int c = (i * G + t) * ROW_VE;
+      float w[8];
+      vec_load(a.gamma, a.vec_dtype, c, a.cols, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - c1 - h[i][e] * c2);
-      if ((i * G + t) * ROW_VE < a.cols) piece_store(dx, (i * G + t) * ROW_VE, a.cols, g[i]);
+      for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * w[e];
+      if (a.beta) {
+        vec_load(a.beta, a.vec_dtype, c, a.cols, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] += w[e];
+      }
     }
+    if (a.y) {
+      T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) piece_store(y, (i * G + t) * ROW_VE, a.cols, v[i]);
+    }
+  }
+  if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // a NaN's padding products (0 * NaN) sit in columns past the end
+        const uint32_t b = (i * G + t) * ROW_VE + e < a.cols ? mag_bits(v[i][e]) : 0u;
+        m = m > b ? m : b;
+      }
+    m = group_umax<G>(m, red, 0);
+    float s, inv, lim;
+    row_scale(m, s, inv, lim);
+    const bool fine = m < 0x7f800000u;
+    if (t == 0) as_global(a.scale)[row] = s;
+    int8_t* q = a.q + row * a.ldq;
+    const int cpad = (a.cols + 15) & ~15;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * G + t) * ROW_VE;
+      if (c < cpad) *as_global(reinterpret_cast<u32x2*>(q + c)) = quant8(v[i], inv, lim, fine);
+    }
+  }
+}
+
+// The same for rows of any length, which are read again for every pass.  A
+// thread rereads only pieces that it alone writes, so y may be x.
+template <typename T, int KIND>
+__global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a) {
+  constexpr int G = 1024;
+  __shared__ GroupRed<G, 1> red;
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  float mean = 0.f, r = 1.f;
+  if constexpr (KIND != ROW_COPY) {
+    if constexpr (KIND == 0) {
+      float s[1] = {0.f};
+      for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+        float v[8];
+        piece_load(x, (int)c, a.cols, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[0] += v[e];
+      }
+      group_sum<G, 1>(s, red, 0);
+      mean = s[0] / (float)a.cols;
+    }
+    float s[1] = {0.f};
+    for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+      float v[8];
+      piece_load(x, (int)c, a.cols, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = c + e < a.cols ? v[e] - mean : 0.f;
+        s[0] = fmaf(d, d, s[0]);
+      }
+    }
+    group_sum<G, 1>(s, red, 1);
+    r = 1.f / sqrtf(s[0] / (float)a.cols + a.eps);
+    if (t == 0) {
+      if (a.mean) as_global(a.mean)[row] = mean;
+      if (a.rstd) as_global(a.rstd)[row] = r;
+    }
+    if (!a.y && !a.scale) return;
+  }
+  auto value = [&](int64_t c, float (&v)[8]) {
+    piece_load(x, (int)c, a.cols, v);
+    if constexpr (KIND != ROW_COPY) {
+      float w[8];
+      vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * r * w[e];
+      if (a.beta) {
+        vec_load(a.beta, a.vec_dtype, (int)c, a.cols, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += w[e];
+      }
+    }
+  };
+  float s = 0.f, inv = 0.f, lim = 0.f;
+  bool fine = false;
+  if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
+    uint32_t m = 0;
+    for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
+      float v[8];
+      value(c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = c + e < a.cols ? mag_bits(v[e]) : 0u;
+        m = m > b ? m : b;
+      }
+    }
+    m = group_umax<G>(m, red, 0);
+    row_scale(m, s, inv, lim);
+    fine = m < 0x7f800000u;
+    if (t == 0) as_global(a.scale)[row] = s;
+  }
+  const int64_t cpad = ((int64_t)a.cols + 15) & ~(int64_t)15;
+  for (int64_t c = (int64_t)t * ROW_VE; c < cpad; c += G * ROW_VE) {
+    float v[8];
+    value(c, v);
+    if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = c + e < a.cols ? v[e] : 0.f;
+      *as_global(reinterpret_cast<u32x2*>(a.q + row * a.ldq + c)) = quant8(z, inv, lim, fine);
+    }
+    if (KIND != ROW_COPY && a.y) piece_store(static_cast<T*>(a.y) + row * a.ldy, (int)c, a.cols, v);
+  }
+}
+
+// Restore: y = q * scale.  16 columns per thread; a workgroup takes 1024
+// consecutive pieces of the rows x ceil(cols / 16) grid of pieces.
+constexpr int DEQ_PIECES = 1024;
+template <typename T>
+__global__ __launch_bounds__(256) void row_restore_kernel(const RestoreArgs a) {
+  const int64_t total = a.rows * a.per_row;
+  const int64_t base = (int64_t)blockIdx.x * DEQ_PIECES;
+  const int64_t row0 = base / a.per_row;
+  const uint32_t first = (uint32_t)(base - row0 * a.per_row);
+#pragma unroll
+  for (int i = 0; i < DEQ_PIECES / 256; ++i) {
+    const uint32_t p = i * 256 + threadIdx.x;
+    if (base + p >= total) return;
+    const uint32_t dr = (first + p) / (uint32_t)a.per_row;
+    const int c = (int)((first + p) - dr * (uint32_t)a.per_row) * 16;
+    const int64_t row = row0 + dr;
+    const u32x4 w = *as_global(reinterpret_cast<const u32x4*>(a.q + row * a.ldq + c));
+    const float s = as_global(a.scale)[row];
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(w[2 * h + (e >> 2)] >> (8 * (e & 3))) * s;
+      if (c + 8 * h < a.cols) piece_store(y, c + 8 * h, a.cols, v);
+    }
+  }
+}
+
+// 8 raw elements of T, so that a 16-bit row takes half the registers of its
+// fp32 values while the next row is on its way.
+template <typename T> struct RowRaw {
+  u32x4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* row, int c, int cols) {
+    if (c + 8 <= cols) {
+      if constexpr (sizeof(T) == 2) {
+        w[0] = as_global(reinterpret_cast<const u32x4_e2*>(row + c))->v;
+      } else {
+        w[0] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c))->v);
+        w[1] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c + 4))->v);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < (int)(sizeof(T) / 2); ++h) w[h] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < cols) {
+          if constexpr (sizeof(T) == 2)
+            w[0][e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(row))[c + e] << (16 * (e & 1));
+          else
+            w[e >> 2][e & 3] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
+        }
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 2)
+      return __builtin_bit_cast(float, (e & 1) ? (w[0][e >> 1] & 0xffff0000u) : (w[0][e >> 1] << 16));
+    else
+      return __builtin_bit_cast(f32x4, w[e >> 2])[e & 3];
+  }
+};
+
+// Norm backward: workgroups loop over rows; a thread keeps its columns' gamma
+// and its sums of dy h and dy in registers over all of them, and the sums go
+// to workspace once per workgroup (partials[2][workgroups][cols]).  The next
+// row's loads are issued before this row's sums, so that few workgroups
+// (and few partial rows) keep enough bytes in flight.
+template <typename T, int KIND, int G, int NV>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const NormBwdArgs a) {
+  constexpr int RPW = G < 256 ? 256 / G : 1;
+  __shared__ GroupRed<G, 2> red;
+  __shared__ float comb[RPW > 1 ? RPW * G * NV * 8 : 1];
+  const int t = threadIdx.x % G;
+  const int sub = threadIdx.x / G;
+  float gam[NV][8], sg[NV][8], sb[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    vec_load(a.gamma, a.vec_dtype, (i * G + t) * ROW_VE, a.cols, gam[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.f;
+  }
+  const int64_t stride = (int64_t)gridDim.x * RPW;
+  int64_t row = (int64_t)blockIdx.x * RPW + sub;
+  RowRaw<T> x[NV], dy[NV];
+  float r = 0.f, mean = 0.f;
+  auto fetch = [&](int64_t at) {
+    const T* xp = static_cast<const T*>(a.x) + at * a.ldx;
+    const T* dp = static_cast<const T*>(a.dy) + at * a.lddy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i].load(xp, (i * G + t) * ROW_VE, a.cols);
+      dy[i].load(dp, (i * G + t) * ROW_VE, a.cols);
+    }
+    r = as_global(a.rstd)[at];
+    if (KIND == 0) mean = as_global(a.mean)[at];
+  };
+  if (row < a.rows) fetch(row);
+  int buf = 0;
+  while (row < a.rows) {
+    const int64_t next = row + stride;
+    RowRaw<T> cx[NV], cd[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      cx[i] = x[i];
+      cd[i] = dy[i];
+    }
+    const float cr = r, cm = mean;
+    if (next < a.rows) fetch(next);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float h = (cx[i].get(e) - cm) * cr, d = cd[i].get(e);
+        sg[i][e] = fmaf(d, h, sg[i][e]);
+        if (KIND == 0) sb[i][e] += d;
+        const float g = d * gam[i][e];
+        s[0] = fmaf(g, h, s[0]);
+        if (KIND == 0) s[1] += g;
+      }
+    group_sum<G, 2>(s, red, buf);
+    buf ^= 1;
+    const float c2 = s[0] / (float)a.cols, c1 = KIND == 0 ? s[1] / (float)a.cols : 0.f;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+    // 1024 threads: h and dy are unpacked again below, or their fp32 values
+    // would be kept over the sum and spill
+    if constexpr (G == 1024) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int h = 0; h < (int)(sizeof(T) / 2); ++h) asm volatile("" : "+v"(cx[i].w[h]), "+v"(cd[i].w[h]));
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * G + t) * ROW_VE;
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float h = (cx[i].get(e) - cm) * cr;
+        o[e] = cr * (cd[i].get(e) * gam[i][e] - c1 - h * c2);
+      }
+      if (c < a.cols) piece_store(dx, c, a.cols, o);
+    }
+    row = next;
   }
   if (!a.partials) return;
   auto put = [&](float (&v)[NV][8], int which) {
@@ -445,7 +773,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
   if constexpr (KIND == 0) put(sb, 1);
 }
 
-// Long rows: dx with the row read twice, and the column sums on their own.
+// Rows above NORM_BWD_MAX_COLS (a thread would hold too much of one): dx with
+// the row read twice, and the column sums on their own.
 template <typename T, int KIND>
 __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdArgs a) {
   constexpr int G = 1024;
@@ -483,35 +812,40 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
   }
 }
 
-// partials[2][gridDim.y][cols] of the columns of 256 threads x 1 column.
+// partials[2][gridDim.y][cols]: 8 columns per thread, every gridDim.y-th row.
 template <typename T, int KIND>
 __global__ __launch_bounds__(256) void norm_columns_long_kernel(const NormBwdArgs a) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * ROW_VE;
   if (c >= a.cols) return;
-  float sg = 0.f, sb = 0.f;
+  float sg[8] = {}, sb[8] = {};
+#pragma unroll 2
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    const float g = to_f32(as_global(static_cast<const T*>(a.dy))[row * a.lddy + c]);
-    const float x = to_f32(as_global(static_cast<const T*>(a.x))[row * a.ldx + c]);
-    const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f;
-    sg = fmaf(g, (x - mean) * as_global(a.rstd)[row], sg);
-    sb += g;
+    float g[8], x[8];
+    piece_load(static_cast<const T*>(a.dy) + row * a.lddy, (int)c, a.cols, g);
+    piece_load(static_cast<const T*>(a.x) + row * a.ldx, (int)c, a.cols, x);
+    const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f, r = as_global(a.rstd)[row];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      sg[e] = fmaf(g[e], (x[e] - mean) * r, sg[e]);
+      sb[e] += g[e];
+    }
   }
-  as_global(a.partials)[(int64_t)blockIdx.y * a.cols + c] = sg;
-  if (KIND == 0) as_global(a.partials)[((int64_t)gridDim.y + blockIdx.y) * a.cols + c] = sb;
+  piece_store(a.partials + (int64_t)blockIdx.y * a.cols, (int)c, a.cols, sg);
+  if (KIND == 0) piece_store(a.partials + ((int64_t)gridDim.y + blockIdx.y) * a.cols, (int)c, a.cols, sb);
 }
 
-// Joins the workgroups' column sums in order: 64 columns per workgroup, 4
-// waves each a quarter of the partials, in fixed order.
+// Joins the workgroups' column sums in order: 64 columns per workgroup, 16
+// waves each a sixteenth of the partials.
 template <typename TV>
-__global__ __launch_bounds__(256) void norm_columns_join_kernel(const JoinArgs a) {
-  __shared__ float part[4][64];
+__global__ __launch_bounds__(1024) void norm_columns_join_kernel(const JoinArgs a) {
+  __shared__ float part[16][64];
   const int which = blockIdx.y;
   TV* out = static_cast<TV*>(which == 0 ? a.dgamma : a.dbeta);
   if (!out) return;  // uniform
   const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + l;
   const float* p = a.partials + (int64_t)which * a.parts * a.cols;
-  const int per = (a.parts + 3) / 4;
+  const int per = (a.parts + 15) / 16;
   const int hi = min(a.parts, (w + 1) * per);
   float s = 0.f;
   if (c < a.cols) {
@@ -521,7 +855,8 @@ __global__ __launch_bounds__(256) void norm_columns_join_kernel(const JoinArgs a
   part[w][l] = s;
   __syncthreads();
   if (w == 0 && c < a.cols) {
-    s = (part[0][l] + part[1][l]) + (part[2][l] + part[3][l]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += part[i][l];
     if (a.accumulate) s += to_f32(as_global(out)[c]);
     as_global(out)[c] = from_f32<TV>(s);
   }

@@ -9,7 +9,7 @@ import pytest
 
 from matrix_orthogonalizing_optimizer_amd import build as B
 
-SOURCES = ["row_ops.hip", "linear8.hip"]
+SOURCES = ["row_ops.hip", "linear8_y.hip", "linear8_dw.hip", "linear8_dx.hip"]
 
 
 @pytest.mark.parametrize("src", SOURCES)
