@@ -470,268 +470,6 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * G + t) * ROW_VE;
-      float w[8];
-      vec_load(a.gamma, a.vec_dtype, c, a.cols, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * w[e];
-      if (a.beta) {
-        vec_load(a.beta, a.vec_dtype, c, a.cols, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] += w[e];
-      }
-    }
-    if (a.y) {
-      T* y = static_cast<T*>(a.y) + row * a.ldy;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) piece_store(y, (i * G + t) * ROW_VE, a.cols, v[i]);
-    }
-  }
-  if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // a NaN's padding products (0 * NaN) sit in columns past the end
-        const uint32_t b = (i * G + t) * ROW_VE + e < a.cols ? mag_bits(v[i][e]) : 0u;
-        m = m > b ? m : b;
-      }
-    m = group_umax<G>(m, red, 0);
-    float s, inv, lim;
-    row_scale(m, s, inv, lim);
-    const bool fine = m < 0x7f800000u;
-    if (t == 0) as_global(a.scale)[row] = s;
-    int8_t* q = a.q + row * a.ldq;
-    const int cpad = (a.cols + 15) & ~15;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * G + t) * ROW_VE;
-      if (c < cpad) *as_global(reinterpret_cast<u32x2*>(q + c)) = quant8(v[i], inv, lim, fine);
-    }
-  }
-}
-
-// The same for rows of any length, which are read again for every pass.  A
-// thread rereads only pieces that it alone writes, so y may be x.
-template <typename T, int KIND>
-__global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a) {
-  constexpr int G = 1024;
-  __shared__ GroupRed<G, 1> red;
-  const int t = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  float mean = 0.f, r = 1.f;
-  if constexpr (KIND != ROW_COPY) {
-    if constexpr (KIND == 0) {
-      float s[1] = {0.f};
-      for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
-        float v[8];
-        piece_load(x, (int)c, a.cols, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += v[e];
-      }
-      group_sum<G, 1>(s, red, 0);
-      mean = s[0] / (float)a.cols;
-    }
-    float s[1] = {0.f};
-    for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
-      float v[8];
-      piece_load(x, (int)c, a.cols, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = c + e < a.cols ? v[e] - mean : 0.f;
-        s[0] = fmaf(d, d, s[0]);
-      }
-    }
-    group_sum<G, 1>(s, red, 1);
-    r = 1.f / sqrtf(s[0] / (float)a.cols + a.eps);
-    if (t == 0) {
-      if (a.mean) as_global(a.mean)[row] = mean;
-      if (a.rstd) as_global(a.rstd)[row] = r;
-    }
-    if (!a.y && !a.scale) return;
-  }
-  auto value = [&](int64_t c, float (&v)[8]) {
-    piece_load(x, (int)c, a.cols, v);
-    if constexpr (KIND != ROW_COPY) {
-      float w[8];
-      vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * r * w[e];
-      if (a.beta) {
-        vec_load(a.beta, a.vec_dtype, (int)c, a.cols, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += w[e];
-      }
-    }
-  };
-  float s = 0.f, inv = 0.f, lim = 0.f;
-  bool fine = false;
-  if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
-    uint32_t m = 0;
-    for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
-      float v[8];
-      value(c, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = c + e < a.cols ? mag_bits(v[e]) : 0u;
-        m = m > b ? m : b;
-      }
-    }
-    m = group_umax<G>(m, red, 0);
-    row_scale(m, s, inv, lim);
-    fine = m < 0x7f800000u;
-    if (t == 0) as_global(a.scale)[row] = s;
-  }
-  const int64_t cpad = ((int64_t)a.cols + 15) & ~(int64_t)15;
-  for (int64_t c = (int64_t)t * ROW_VE; c < cpad; c += G * ROW_VE) {
-    float v[8];
-    value(c, v);
-    if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
-      float z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = c + e < a.cols ? v[e] : 0.f;
-      *as_global(reinterpret_cast<u32x2*>(a.q + row * a.ldq + c)) = quant8(z, inv, lim, fine);
-    }
-    if (KIND != ROW_COPY && a.y) piece_store(static_cast<T*>(a.y) + row * a.ldy, (int)c, a.cols, v);
-  }
-}
-
-// Restore: y = q * scale.  16 columns per thread; a workgroup takes 1024
-// consecutive pieces of the rows x ceil(cols / 16) grid of pieces.
-constexpr int DEQ_PIECES = 1024;
-template <typename T>
-__global__ __launch_bounds__(256) void row_restore_kernel(const RestoreArgs a) {
-  const int64_t total = a.rows * a.per_row;
-  const int64_t base = (int64_t)blockIdx.x * DEQ_PIECES;
-  const int64_t row0 = base / a.per_row;
-  const uint32_t first = (uint32_t)(base - row0 * a.per_row);
-#pragma unroll
-  for (int i = 0; i < DEQ_PIECES / 256; ++i) {
-    const uint32_t p = i * 256 + threadIdx.x;
-    if (base + p >= total) return;
-    const uint32_t dr = (first + p) / (uint32_t)a.per_row;
-    const int c = (int)((first + p) - dr * (uint32_t)a.per_row) * 16;
-    const int64_t row = row0 + dr;
-    const u32x4 w = *as_global(reinterpret_cast<const u32x4*>(a.q + row * a.ldq + c));
-    const float s = as_global(a.scale)[row];
-    T* y = static_cast<T*>(a.y) + row * a.ldy;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(w[2 * h + (e >> 2)] >> (8 * (e & 3))) * s;
-      if (c + 8 * h < a.cols) piece_store(y, c + 8 * h, a.cols, v);
-    }
-  }
-}
-
-// 8 raw elements of T, so that a 16-bit row takes half the registers of its
-// fp32 values while the next row is on its way.
-template <typename T> struct RowRaw {
-  u32x4 w[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* row, int c, int cols) {
-    if (c + 8 <= cols) {
-      if constexpr (sizeof(T) == 2) {
-        w[0] = as_global(reinterpret_cast<const u32x4_e2*>(row + c))->v;
-      } else {
-        w[0] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c))->v);
-        w[1] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c + 4))->v);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < (int)(sizeof(T) / 2); ++h) w[h] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < cols) {
-          if constexpr (sizeof(T) == 2)
-            w[0][e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(row))[c + e] << (16 * (e & 1));
-          else
-            w[e >> 2][e & 3] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
-        }
-    }
-  }
-  __device__ __forceinline__ float get(int e) const {
-    if constexpr (sizeof(T) == 2)
-      return __builtin_bit_cast(float, (e & 1) ? (w[0][e >> 1] & 0xffff0000u) : (w[0][e >> 1] << 16));
-    else
-      return __builtin_bit_cast(f32x4, w[e >> 2])[e & 3];
-  }
-};
-
-// Norm backward: workgroups loop over rows; a thread keeps its columns' gamma
-// and its sums of dy h and dy in registers over all of them, and the sums go
-// to workspace once per workgroup (partials[2][workgroups][cols]).  The next
-// row's loads are issued before this row's sums, so that few workgroups
-// (and few partial rows) keep enough bytes in flight.
-template <typename T, int KIND, int G, int NV>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const NormBwdArgs a) {
-  constexpr int RPW = G < 256 ? 256 / G : 1;
-  __shared__ GroupRed<G, 2> red;
-  __shared__ float comb[RPW > 1 ? RPW * G * NV * 8 : 1];
-  const int t = threadIdx.x % G;
-  const int sub = threadIdx.x / G;
-  float gam[NV][8], sg[NV][8], sb[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    vec_load(a.gamma, a.vec_dtype, (i * G + t) * ROW_VE, a.cols, gam[i]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.f;
-  }
-  const int64_t stride = (int64_t)gridDim.x * RPW;
-  int64_t row = (int64_t)blockIdx.x * RPW + sub;
-  RowRaw<T> x[NV], dy[NV];
-  float r = 0.f, mean = 0.f;
-  auto fetch = [&](int64_t at) {
-    const T* xp = static_cast<const T*>(a.x) + at * a.ldx;
-    const T* dp = static_cast<const T*>(a.dy) + at * a.lddy;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      x[i].load(xp, (i * G + t) * ROW_VE, a.cols);
-      dy[i].load(dp, (i * G + t) * ROW_VE, a.cols);
-    }
-    r = as_global(a.rstd)[at];
-    if (KIND == 0) mean = as_global(a.mean)[at];
-  };
-  if (row < a.rows) fetch(row);
-  int buf = 0;
-  while (row < a.rows) {
-    const int64_t next = row + stride;
-    RowRaw<T> cx[NV], cd[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      cx[i] = x[i];
-      cd[i] = dy[i];
-    }
-    const float cr = r, cm = mean;
-    if (next < a.rows) fetch(next);
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float h = (cx[i].get(e) - cm) * cr, d = cd[i].get(e);
-        sg[i][e] = fmaf(d, h, sg[i][e]);
-        if (KIND == 0) sb[i][e] += d;
-        const float g = d * gam[i][e];
-        s[0] = fmaf(g, h, s[0]);
-        if (KIND == 0) s[1] += g;
-      }
-    group_sum<G, 2>(s, red, buf);
-    buf ^= 1;
-    const float c2 = s[0] / (float)a.cols, c1 = KIND == 0 ? s[1] / (float)a.cols : 0.f;
-    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
-    // 1024 threads: h and dy are unpacked again below, or their fp32 values
-    // would be kept over the sum and spill
-    if constexpr (G == 1024) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int h = 0; h < (int)(sizeof(T) / 2); ++h) asm volatile("" : "+v"(cx[i].w[h]), "+v"(cd[i].w[h]));
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * G + t) * ROW_VE;
       float o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
