@@ -104,7 +104,7 @@ struct JoinArgs {
 //   input gradient   A = dy (tokens x out, K-contiguous), B = w (out x in, K-major)
 struct Linear8Args {
   const void* A;
-  const int8_t* B;
+  const void* B;      // int8; bf16 where the 8-bit operand was expanded
   const float* sa;    // forward: one per row of C
   const float* sb;    // forward: one per column of C; gradients: one per summation index
   const void* bias;   // forward: one per column of C, or null

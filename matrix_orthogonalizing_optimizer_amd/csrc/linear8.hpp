@@ -19,6 +19,11 @@
 // front of the MFMAs instead would repeat it in every wave that shares the
 // columns.  Fragments come out of LDS transposed (ds_read_b64_tr_b16).  dy is
 // row-major for dX, K-major for dW.
+// Where many tile rows share the 8-bit operand it is turned into bf16 in the
+// workspace first (B_BF16; row_restore_kernel) and then copied to LDS like
+// dy: that takes 3 bytes of HBM traffic per element once, and saves every
+// workgroup the conversion and its register writes to LDS (1.8 -> 1.5 us per
+// 256 x 256 x 64 stage).  linear8_plan in ops.cpp chooses.
 //   A_DIRECT  bf16 dy, 16-byte aligned rows, sizes multiples of 8: copied
 //             global -> LDS directly
 //   A_REG16   bf16 dy of any alignment, through registers
@@ -41,6 +46,7 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
 enum : int { L8_Y = 0, L8_DW = 1, L8_DX = 2 };
 enum : int { A_DIRECT = 0, A_REG16 = 1, A_REG32 = 2 };
+enum : int { B_Q8 = 0, B_BF16 = 1 };
 
 template <bool INT> struct Acc8;
 template <> struct Acc8<true> {
@@ -141,10 +147,11 @@ __device__ __forceinline__ void linear8_tile(const Linear8Args& a, int& split, i
   bj = __builtin_amdgcn_readfirstlane(w / gm);
 }
 
-template <int MODE, int ASRC, int T, int NW, typename TO, bool PART>
+template <int MODE, int ASRC, int BSRC, int T, int NW, typename TO, bool PART>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(T == 128 ? 2 : NW / 4, T == 128 ? 2 : NW / 4)))
 void linear8_kernel(const Linear8Args a) {
   constexpr bool INT = MODE == L8_Y;
+  constexpr bool CVT = !INT && BSRC == B_Q8;  // the 8-bit operand is converted here
   constexpr bool AKM = MODE == L8_DW;      // A lies K-major
   constexpr int ES = INT ? 1 : 2;
   constexpr int EPC = 16 / ES;             // elements per 16-byte chunk
@@ -185,7 +192,7 @@ void linear8_kernel(const Linear8Args a) {
                  : (uint32_t)((((int64_t)rows_a - 1) * a.lda + a.K) * 2));  // dy's last row ends at K
   const int rows_b = min(T, a.N - col0);
   const __amdgpu_buffer_rsrc_t brs =
-      make_rsrc(a.B + (INT ? (int64_t)col0 * a.ldb : 0), (uint32_t)((int64_t)rows_b * a.ldb));
+      make_rsrc(static_cast<const int8_t*>(a.B) + (INT ? (int64_t)col0 * a.ldb : 0), (uint32_t)((int64_t)rows_b * a.ldb));
   const int crow = wid * (8 * NQ) + (lane >> 3);              // tile row of copy 0
   const int ck[2] = {((lane & 7) ^ (lane >> 3)) * EPC, ((lane & 7) ^ (lane >> 3) ^ 1) * EPC};
   auto copy_row_major = [&](__amdgpu_buffer_rsrc_t r, int64_t ld, int region, int q, int v, int ks) {
@@ -194,24 +201,28 @@ void linear8_kernel(const Linear8Args a) {
     copy16_to_lds(r, &ring[v & 1][region + (wid * NQ + q) * 64], off);
   };
   // ---- operand A of dW, K-major: rows of the stage, columns row0 .. of dy
-  uint32_t tb[2] = {0u, 0u};
-  if constexpr (AKM && ASRC == A_DIRECT) {
-#pragma unroll
-    for (int par = 0; par < 2; ++par) {
-      const int krow = (wid * NQ + par) * RPC + lane / CR;
-      const int col = row0 + ((lane % CR) ^ swz_t(krow)) * 8;
-      tb[par] = col < a.M ? (uint32_t)(((int64_t)krow * a.lda + col) * 2) : OOB;
-    }
-  }
+  // (and B when it is bf16): a lane's K-row and chunk of copy q depend on q
+  // only through q & 1, as in gemm.hpp
+  auto km_offset = [&](int par, int64_t ld, int c0, int cols) {
+    const int krow = (wid * NQ + par) * RPC + lane / CR;
+    const int col = c0 + ((lane % CR) ^ swz_t(krow)) * 8;
+    return col < cols ? (uint32_t)(((int64_t)krow * ld + col) * 2) : OOB;
+  };
+  const uint32_t ta[2] = {km_offset(0, a.lda, row0, a.M), km_offset(1, a.lda, row0, a.M)};
+  const uint32_t tbb[2] = {km_offset(0, a.ldb, col0, a.N), km_offset(1, a.ldb, col0, a.N)};
+  auto copy_k_major = [&](const void* base, int64_t ld, int cols, const uint32_t(&t)[2], int region, int q, int v, int ks) {
+    const int nk = max(0, min(BK, a.K - ks * BK));
+    const char* p = static_cast<const char*>(base) + (int64_t)ks * BK * ld * 2;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(p, nk ? (uint32_t)((((int64_t)nk - 1) * ld + cols) * 2) : 0u);
+    copy16_to_lds(r, &ring[v & 1][region + (wid * NQ + q) * 64], t[q & 1] + (uint32_t)((int64_t)((q & ~1) * RPC) * ld * 2));
+  };
   auto copy_a = [&](int q, int v, int ks) {
-    if constexpr (AKM) {
-      const int nk = max(0, min(BK, a.K - ks * BK));
-      const char* p = static_cast<const char*>(a.A) + (int64_t)ks * BK * a.lda * 2;
-      const __amdgpu_buffer_rsrc_t r = make_rsrc(p, nk ? (uint32_t)((((int64_t)nk - 1) * a.lda + a.M) * 2) : 0u);
-      copy16_to_lds(r, &ring[v & 1][(wid * NQ + q) * 64], tb[q & 1] + (uint32_t)((int64_t)((q & ~1) * RPC) * a.lda * 2));
-    } else {
-      copy_row_major(ars, a.lda, 0, q, v, ks);
-    }
+    if constexpr (AKM) copy_k_major(a.A, a.lda, a.M, ta, 0, q, v, ks);
+    else copy_row_major(ars, a.lda, 0, q, v, ks);
+  };
+  // expanded B has whole 16-byte chunks behind its last column
+  auto copy_b = [&](int q, int v, int ks) {
+    copy_k_major(a.B, a.ldb, (a.N + 7) & ~7, tbb, OPS, q, v, ks);
   };
   // through registers: the same chunks, loaded ahead of being written; fp32 in
   // two halves, since all four chunks do not fit beside the accumulators
@@ -242,10 +253,10 @@ void linear8_kernel(const Linear8Args a) {
   const uint32_t boff = col0 + bcol < a.ldb ? (uint32_t)(brow * a.ldb + col0 + bcol) : OOB;
   const int bslot = OPS + brow * CR + ((tid % CR) ^ swz_t(brow));
   auto load_b = [&](int ks) {
-    if constexpr (!INT) {
+    if constexpr (CVT) {
       const int nk = max(0, min(BK, a.K - ks * BK));
       const __amdgpu_buffer_rsrc_t r =
-          make_rsrc(a.B + (int64_t)ks * BK * a.ldb, (uint32_t)((int64_t)nk * a.ldb));
+          make_rsrc(static_cast<const int8_t*>(a.B) + (int64_t)ks * BK * a.ldb, (uint32_t)((int64_t)nk * a.ldb));
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.sb + (int64_t)ks * BK, (uint32_t)(nk * 4));
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
@@ -256,7 +267,7 @@ void linear8_kernel(const Linear8Args a) {
   };
   u32x4 bw;
   auto convert_b = [&](int idx, int v) {  // pair idx of the thread's 8 NQ values; the fourth pair of a piece stores it
-    if constexpr (!INT) {
+    if constexpr (CVT) {
       const int i = idx >> 2, j = idx & 3;
       const uint32_t w = bq[i][j >> 1] >> (16 * (j & 1));
       bw[j] = pack2<bf16>((float)(int8_t)w * bs[i], (float)(int8_t)(w >> 8) * bs[i]);
@@ -318,7 +329,14 @@ void linear8_kernel(const Linear8Args a) {
       constexpr int p = decltype(pc)::value;
       constexpr int i = p / WTN, j = p % WTN;
       constexpr bool needA = j == 0 && AKM, needB = i == 0;  // first uses among the transposed
-      if constexpr (needA || needB) {
+      if constexpr (ASRC != A_DIRECT) {
+        // these variants reload arguments in the loop; scalar loads share the
+        // counter and complete out of order, so only zero says anything
+        if constexpr (p == 0) {
+          wait_lgkm0();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else if constexpr (needA || needB) {
         // position of that fragment in the reading order
         constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : WTN + i);
         constexpr int later_a = AKM ? (WTM - 1 - (at > WTN ? at - WTN : 0)) : 0;
@@ -367,14 +385,20 @@ void linear8_kernel(const Linear8Args a) {
           store_a(q, 0, 0);
         }
       }
+      if constexpr (BSRC == B_BF16) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) copy_b(q, 0, ksn);
+      }
 #pragma unroll
       for (int i = 0; i < 4 * NQ; ++i) convert_b(i, 0);
       advance();
       wait_vmcnt<0>();
       load_b(ksn);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q)
+      for (int q = 0; q < NQ; ++q) {
         if constexpr (ASRC == A_DIRECT) copy_a(q, 1, ksn);
+        if constexpr (BSRC == B_BF16) copy_b(q, 1, ksn);
+      }
 #pragma unroll
       for (int q = 0; q < NH; ++q) load_a(q, ksn);
     }
@@ -404,7 +428,7 @@ void linear8_kernel(const Linear8Args a) {
           // the fragment reads of a step before its register writes: those wait
 #pragma unroll
           for (int r = p; r < NDR; r += NPAIR) read_one(ro(r), v, s + 1, (s + 1) & 1);
-          if constexpr (!INT) {
+          if constexpr (CVT) {
             // 4 NQ pairs of B over the 3 NPAIR MFMAs, after a head start for the loads
             constexpr int SLOTS = 3 * NPAIR, HEAD = NPAIR >= 8 ? 6 : 2;
             constexpr int PER = (4 * NQ + SLOTS - HEAD - 1) / (SLOTS - HEAD);
@@ -412,9 +436,9 @@ void linear8_kernel(const Linear8Args a) {
 #pragma unroll
             for (int c = 0; c < PER; ++c)
               if (at >= 0 && at * PER + c < 4 * NQ) convert_b(at * PER + c, v + 1);
-            if constexpr (ASRC != A_DIRECT) {
-              if (s == 2 && p < NH) store_a(NQ - NH + p, v + 1, pc_held);
-            }
+          }
+          if constexpr (!INT && ASRC != A_DIRECT) {
+            if (s == 2 && p < NH) store_a(NQ - NH + p, v + 1, pc_held);
           }
           __builtin_amdgcn_sched_barrier(0);
         });
@@ -444,8 +468,16 @@ void linear8_kernel(const Linear8Args a) {
             if (c < NQ) copy_row_major(ars, a.lda, 0, c, v + 2, ksn);
             else copy_row_major(brs, a.ldb, OPS, c - NQ, v + 2, ksn);
           }
-        } else if constexpr (ASRC == A_DIRECT) {
-          if (p < NQ) copy_a(p, v + 2, ksn);
+        } else {
+#pragma unroll
+          for (int c = p; c < 2 * NQ; c += NPAIR) {
+            if constexpr (ASRC == A_DIRECT) {
+              if (c < NQ) copy_a(c, v + 2, ksn);
+            }
+            if constexpr (BSRC == B_BF16) {
+              if (c >= NQ) copy_b(c - NQ, v + 2, ksn);
+            }
+          }
         }
 #pragma unroll
         for (int r = p; r < NDR; r += NPAIR) read_one(ro(r), v + 1, 0, 0);

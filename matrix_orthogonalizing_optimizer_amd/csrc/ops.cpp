@@ -47,8 +47,11 @@ size_t norm_ws(int64_t rows, int64_t cols) {
 // Tile and split of a product of the 8-bit linear layer; depends on the sizes
 // only, so that the workspace query and the call agree.
 struct Linear8Plan {
+  bool few;       // few tokens: no tiles
+  bool expanded;  // gradients: the 8-bit operand as bf16 in the workspace first
   int tile, splits, per_split;
-  int64_t ldws;
+  int64_t ldws, ldx;
+  size_t ws_off;  // partial results behind the expanded operand
   size_t bytes;
 };
 Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in) {
@@ -57,6 +60,22 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in) {
   const int64_t K = pass == MUON_LINEAR8_FORWARD ? in : pass == MUON_LINEAR8_WEIGHT_GRAD ? tokens : out;
   const int64_t nks = (K + (pass == MUON_LINEAR8_FORWARD ? 128 : 64) - 1) / (pass == MUON_LINEAR8_FORWARD ? 128 : 64);
   Linear8Plan p;
+  // Few tokens: up to 16 the kernel bound by the weights is ahead at every size
+  // measured (14336 x 4096, 16 tokens: 20.9 against 24 us in tiles), up to 64
+  // it is while the weights are few (4096 x 4096, 64 tokens: 14.9 against 15.9
+  // us; 14336 x 4096, 32 tokens: 29.8 against 24).
+  p.few = pass == MUON_LINEAR8_FORWARD && (tokens <= 16 || (tokens <= 64 && out * in <= ((int64_t)1 << 24)));
+  p.expanded = false;
+  p.ldx = 0;
+  p.ws_off = 0;
+  if (p.few) {
+    p.tile = 128;
+    p.splits = 1;
+    p.per_split = (int)nks;
+    p.ldws = 0;
+    p.bytes = 0;
+    return p;
+  }
   auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
   p.tile = tiles(256) >= 192 ? 256 : 128;
   const int64_t slots = p.tile == 256 ? 256 : 512;
@@ -65,7 +84,13 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in) {
   p.per_split = (int)std::max<int64_t>(1, (nks + z - 1) / z);
   p.splits = (int)std::max<int64_t>(1, (nks + p.per_split - 1) / p.per_split);
   p.ldws = (N + 7) / 8 * 8;
-  p.bytes = p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)p.ldws * sizeof(float) + WS_ALIGN : 0;
+  p.expanded = pass != MUON_LINEAR8_FORWARD && p.tile == 256 && M >= 2048;
+  if (p.expanded) {
+    p.ldx = (N + 63) / 64 * 64;
+    p.ws_off = (size_t)K * (size_t)p.ldx * 2;
+  }
+  p.bytes = p.ws_off + (p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)p.ldws * sizeof(float) : 0);
+  if (p.bytes) p.bytes += WS_ALIGN;
   return p;
 }
 
@@ -77,7 +102,7 @@ bool linear8_args(const Linear8Plan& p, int64_t M, int64_t N, int64_t K, void* w
   a.tilesM = (int32_t)tm; a.tilesN = (int32_t)tn;
   a.splits = p.splits; a.per_split = p.per_split;
   a.ldws = p.ldws;
-  a.ws = p.splits > 1 ? reinterpret_cast<float*>(ws_base(workspace)) : nullptr;
+  a.ws = p.splits > 1 ? reinterpret_cast<float*>(ws_base(workspace) + p.ws_off) : nullptr;
   return true;
 }
 
@@ -246,7 +271,9 @@ muon_status muon_linear8_forward(const int8_t* q, int64_t ldq, const float* scal
   a.o = y; a.ldo = ldy;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
-  return done(timed(F_LINEAR8_Y, f, 0.0, s, [&] { return launch_linear8_forward(p.tile, dev_dt(dtype), a, s); }));
+  return done(timed(F_LINEAR8_Y, f, 0.0, s, [&] {
+    return p.few ? launch_linear8_few(dev_dt(dtype), a, s) : launch_linear8_forward(p.tile, dev_dt(dtype), a, s);
+  }));
 }
 
 static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32_t dy_dtype, const int8_t* q,
@@ -271,13 +298,25 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
   a.B = q; a.ldb = ldq; a.sb = scale;
   a.o = o; a.ldo = ldo;
   a.accumulate = accumulate;
+  RestoreArgs x;
+  std::memset(&x, 0, sizeof(x));
+  if (p.expanded) {
+    x.q = q; x.ldq = ldq; x.scale = scale;
+    x.y = ws_base(workspace); x.ldy = p.ldx;
+    x.rows = sum; x.cols = (int32_t)in; x.per_row = (in + 15) / 16;
+    a.B = x.y; a.ldb = p.ldx;
+  }
   // direct copies of dy take 16-byte pieces that lie wholly inside a row
   const int asrc = dy_dtype == MUON_F32 ? 2 : at(dy, 16) && lddy % 8 == 0 && out % 8 == 0 ? 0 : 1;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
   return done(timed(weight ? F_LINEAR8_DW : F_LINEAR8_DX, f, 0.0, s, [&] {
-    return weight ? launch_linear8_dw(p.tile, asrc, dev_dt(o_dtype), a, s)
-                  : launch_linear8_dx(p.tile, asrc, dev_dt(o_dtype), a, s);
+    if (p.expanded) {
+      const hipError_t e = launch_row_restore(DT_BF16, x, s);
+      if (e != hipSuccess) return e;
+    }
+    return weight ? launch_linear8_dw(p.tile, p.expanded, asrc, dev_dt(o_dtype), a, s)
+                  : launch_linear8_dx(p.tile, p.expanded, asrc, dev_dt(o_dtype), a, s);
   }));
 }
 
