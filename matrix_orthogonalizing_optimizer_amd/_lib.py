@@ -128,7 +128,7 @@ def lib():
     L.muon_linear8_forward.argtypes = [vp, i64, vp, vp, i64, vp, vp, i32, i64, i64, i64, vp, i64, i32, vp, sz, vp]
     L.muon_linear8_weight_grad.argtypes = [vp, i64, i32, vp, i64, vp, i64, i64, i64, vp, i64, i32, i32, vp, sz, vp]
     L.muon_linear8_input_grad.argtypes = [vp, i64, i32, vp, i64, vp, i64, i64, i64, vp, i64, i32, vp, sz, vp]
-    L.muon_linear8_workspace_bytes.argtypes = [i32, i64, i64, i64, ctypes.POINTER(sz)]
+    L.muon_linear8_workspace_bytes.argtypes = [i32, i64, i64, i64, vp, i64, i32, ctypes.POINTER(sz)]
     for n in ("muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
               "muon_norm_backward_workspace_bytes", "muon_linear8_forward", "muon_linear8_weight_grad",
               "muon_linear8_input_grad", "muon_linear8_workspace_bytes"):
@@ -701,11 +701,13 @@ def muon_norm_backward(dy, x, gamma, mean, rstd, kind=MUON_NORM_LAYER, dx=None, 
     return dx
 
 
-def muon_linear8_workspace_bytes(kind: int, tokens: int, out: int, in_: int) -> int:
-    """Workspace of one pass (MUON_LINEAR8_FORWARD, _WEIGHT_GRAD, _INPUT_GRAD)."""
+def muon_linear8_workspace_bytes(kind: int, tokens: int, out: int, in_: int, dy=None) -> int:
+    """Workspace of one pass (MUON_LINEAR8_FORWARD, _WEIGHT_GRAD, _INPUT_GRAD);
+    dy: the gradient call's tensor (for its dtype and alignment)."""
     b = ctypes.c_size_t()
+    p, ld, dt = (0, 0, MUON_BF16) if dy is None else (dy.data_ptr(),) + _matrix("dy", dy)[2:]
     _check("muon_linear8_workspace_bytes",
-           lib().muon_linear8_workspace_bytes(kind, tokens, out, in_, ctypes.byref(b)))
+           lib().muon_linear8_workspace_bytes(kind, tokens, out, in_, p, ld, dt, ctypes.byref(b)))
     return b.value
 
 
@@ -751,7 +753,7 @@ def muon_linear8_weight_grad(dy, q, scale, dw=None, dtype=None, accumulate=False
     r, c, lddw, dt = _matrix("dw", dw)
     if (r, c) != (out, in_):
         raise ValueError(f"dw: expected {(out, in_)}, got {(r, c)}")
-    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_WEIGHT_GRAD, tokens, out, in_)
+    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_WEIGHT_GRAD, tokens, out, in_, dy)
     workspace, wp, wsz = _scratch(on, workspace, nb)
     on.call("muon_linear8_weight_grad", dy.data_ptr(), lddy, dydt, q.data_ptr(), ldq, scale.data_ptr(), tokens, out,
             in_, dw.data_ptr(), lddw, dt, 1 if accumulate else 0, wp, wsz)
@@ -771,7 +773,7 @@ def muon_linear8_input_grad(dy, wq, wscale, dx=None, dtype=None, workspace=None,
     r, c, lddx, dt = _matrix("dx", dx)
     if (r, c) != (tokens, in_):
         raise ValueError(f"dx: expected {(tokens, in_)}, got {(r, c)}")
-    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_INPUT_GRAD, tokens, out, in_)
+    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_INPUT_GRAD, tokens, out, in_, dy)
     workspace, wp, wsz = _scratch(on, workspace, nb)
     on.call("muon_linear8_input_grad", dy.data_ptr(), lddy, dydt, wq.data_ptr(), ldw, wscale.data_ptr(), tokens, out,
             in_, dx.data_ptr(), lddx, dt, wp, wsz)

@@ -116,6 +116,16 @@ struct Linear8Args {
   int32_t per_split;  // K-stages (128 bytes of a row) per split
   int32_t bias_dtype;
   int32_t accumulate;
+  int32_t planes;     // gradients: bf16 planes of dy that sum to it
+  int64_t plane;      // elements between them
+};
+// dy as bf16 planes (see linear8_planes_kernel).
+struct PlanesArgs {
+  const void* dy;
+  void* o;
+  int64_t ld, ldo, plane;
+  int64_t rows, per_row;  // per_row: pieces of 8 columns
+  int32_t cols;
 };
 
 // Host table -> device memory through kernel arguments: one launch carries

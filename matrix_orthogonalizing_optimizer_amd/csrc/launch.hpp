@@ -35,11 +35,11 @@ hipError_t launch_norm_backward(int kind, int dt, const NormBwdArgs& a, int part
 hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s);
 
 // Linear layer on 8-bit rows.  tile: 128 or 256; odt: dtype of the result;
-// expanded: a.B is the 8-bit operand turned into bf16 (256 tiles only);
-// asrc: how dy is read (A_DIRECT, A_REG16, A_REG32 in linear8.hpp).
+// expanded: a.B is the 8-bit operand turned into bf16 (256 tiles only).
 hipError_t launch_linear8_forward(int tile, int odt, const Linear8Args& a, hipStream_t s);
 hipError_t launch_linear8_few(int odt, const Linear8Args& a, hipStream_t s);  // at most 64 tokens
-hipError_t launch_linear8_dw(int tile, bool expanded, int asrc, int odt, const Linear8Args& a, hipStream_t s);
-hipError_t launch_linear8_dx(int tile, bool expanded, int asrc, int odt, const Linear8Args& a, hipStream_t s);
+hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s);
+hipError_t launch_linear8_dw(int tile, bool expanded, int odt, const Linear8Args& a, hipStream_t s);
+hipError_t launch_linear8_dx(int tile, bool expanded, int odt, const Linear8Args& a, hipStream_t s);
 
 }  // namespace muon

@@ -24,11 +24,11 @@
 // dy: that takes 3 bytes of HBM traffic per element once, and saves every
 // workgroup the conversion and its register writes to LDS (1.8 -> 1.5 us per
 // 256 x 256 x 64 stage).  linear8_plan in ops.cpp chooses.
-//   A_DIRECT  bf16 dy, 16-byte aligned rows, sizes multiples of 8: copied
-//             global -> LDS directly
-//   A_REG16   bf16 dy of any alignment, through registers
-//   A_REG32   fp32 dy through registers, as three bf16 pieces that sum to it
-//             exactly (8 significant bits each): K is walked three times.
+// dy is copied to LDS directly as well, which takes bf16 rows in whole
+// 16-byte pieces.  Any other dy is laid out so in the workspace first
+// (linear8_planes_kernel): bf16 rows of odd widths or addresses as they are,
+// fp32 as three bf16 planes that sum to it exactly (8 significant bits each);
+// K is then walked once per plane.
 //
 // K may be split over workgroups that then leave partial tiles in the
 // workspace (PART); linear8_join_kernel adds them in order.
@@ -45,7 +45,6 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 
 enum : int { L8_Y = 0, L8_DW = 1, L8_DX = 2 };
-enum : int { A_DIRECT = 0, A_REG16 = 1, A_REG32 = 2 };
 enum : int { B_Q8 = 0, B_BF16 = 1 };
 
 template <bool INT> struct Acc8;
@@ -79,48 +78,29 @@ __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
   return __builtin_bit_cast(uint32_t, r) & 0xffff0000u;
 }
 
-// Raw 8 elements of dy of which the first `valid` exist (may be <= 0 or >= 8).
-template <int ASRC> struct Dy8;
-template <> struct Dy8<A_REG16> {
-  u32x4 w;
-  __device__ __forceinline__ void load(const void* base, int64_t off, int valid) {
-    const bf16* p = static_cast<const bf16*>(base) + off;
-    if (valid >= 8) {
-      w = as_global(reinterpret_cast<const u32x4_e2*>(p))->v;
-    } else {
-      w = u32x4{0u, 0u, 0u, 0u};
+// dy (rows x cols, any alignment) -> PIECES planes of bf16, rows ldo apart (a
+// multiple of 8), zero up to a multiple of 8 columns; 8 columns per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void linear8_planes_kernel(const PlanesArgs a) {
+  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (p >= a.rows * a.per_row) return;
+  const int64_t row = p / a.per_row;
+  const int c = (int)(p - row * a.per_row) * 8;
+  RowRaw<T> x;
+  x.load(static_cast<const T*>(a.dy) + row * a.ld, c, a.cols);
+  bf16* o = static_cast<bf16*>(a.o) + row * a.ldo + c;
+  if constexpr (sizeof(T) == 2) {
+    *as_global(reinterpret_cast<u32x4*>(o)) = x.w[0];
+  } else {
 #pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e < valid) w[e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(p))[e] << (16 * (e & 1));
+    for (int pc = 0; pc < 3; ++pc) {
+      u32x4 w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = (bf16_piece(x.get(2 * j), pc) >> 16) | bf16_piece(x.get(2 * j + 1), pc);
+      *as_global(reinterpret_cast<u32x4*>(o + pc * a.plane)) = w;
     }
   }
-  __device__ __forceinline__ u32x4 piece(int) const { return w; }
-};
-template <> struct Dy8<A_REG32> {
-  f32x4 a, b;
-  __device__ __forceinline__ void load(const void* base, int64_t off, int valid) {
-    const float* p = static_cast<const float*>(base) + off;
-    if (valid >= 8) {
-      a = as_global(reinterpret_cast<const f32x4_e4*>(p))->v;
-      b = as_global(reinterpret_cast<const f32x4_e4*>(p + 4))->v;
-    } else {
-      a = b = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (e < valid) a[e] = as_global(p)[e];
-        if (e + 4 < valid) b[e] = as_global(p)[e + 4];
-      }
-    }
-  }
-  __device__ __forceinline__ u32x4 piece(int p) const {
-    u32x4 w;
-    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = (bf16_piece(v[2 * j], p) >> 16) | bf16_piece(v[2 * j + 1], p);
-    return w;
-  }
-};
-template <> struct Dy8<A_DIRECT> {};
+}
 
 // Workgroup -> (split, tile row, tile column), spread over the XCDs in
 // groups of 4 tile rows as the optimizer's products are (gemm.hpp).
@@ -147,7 +127,7 @@ __device__ __forceinline__ void linear8_tile(const Linear8Args& a, int& split, i
   bj = __builtin_amdgcn_readfirstlane(w / gm);
 }
 
-template <int MODE, int ASRC, int BSRC, int T, int NW, typename TO, bool PART>
+template <int MODE, int BSRC, int T, int NW, typename TO, bool PART>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(T == 128 ? 2 : NW / 4, T == 128 ? 2 : NW / 4)))
 void linear8_kernel(const Linear8Args a) {
   constexpr bool INT = MODE == L8_Y;
@@ -164,7 +144,6 @@ void linear8_kernel(const Linear8Args a) {
   constexpr int NDR = WTM + WTN, NPAIR = WTM * WTN;
   constexpr int CR = T / 8;                // chunks per K-row of a K-major stage
   constexpr int RPC = 64 / CR;             // K-rows per wave-wide copy
-  constexpr int PIECES = ASRC == A_REG32 ? 3 : 1;
   constexpr int RSTEP = 64 * NW / CR;      // rows between a thread's pieces of the 8-bit operand
   static_assert(NQ * 8 * NW == T && RSTEP % 4 == 0, "chunks shared out evenly");
   __shared__ u32x4 ring[2][STG];
@@ -180,16 +159,16 @@ void linear8_kernel(const Linear8Args a) {
   // stages of this split: K-stages [ks0, ks1), walked once per piece of dy
   const int nks = (a.K + BK - 1) / BK;
   const int ks0 = min(split * a.per_split, nks), ks1 = min(ks0 + a.per_split, nks);
-  const int nst = (ks1 - ks0) * PIECES;
+  const int nst = (ks1 - ks0) * a.planes;
 
   auto swz_t = [](int krow) { return ((krow & 1) << 2) ^ (((krow >> 1) & 1) * 10); };
 
   // ---- operand A (and B for L8_Y), row-major: rows of the tile
   const int rows_a = min(T, a.M - row0);
   const char* Abase = static_cast<const char*>(a.A) + (AKM ? 0 : (int64_t)row0 * a.lda * ES);
-  const __amdgpu_buffer_rsrc_t ars = make_rsrc(
-      Abase, INT ? (uint32_t)((int64_t)rows_a * a.lda)
-                 : (uint32_t)((((int64_t)rows_a - 1) * a.lda + a.K) * 2));  // dy's last row ends at K
+  // 8-bit rows have all their ld bytes, the last row of dy whole 16-byte pieces
+  const uint32_t Abytes = INT ? (uint32_t)((int64_t)rows_a * a.lda)
+                              : (uint32_t)((((int64_t)rows_a - 1) * a.lda + ((a.K + 7) & ~7)) * 2);
   const int rows_b = min(T, a.N - col0);
   const __amdgpu_buffer_rsrc_t brs =
       make_rsrc(static_cast<const int8_t*>(a.B) + (INT ? (int64_t)col0 * a.ldb : 0), (uint32_t)((int64_t)rows_b * a.ldb));
@@ -216,35 +195,15 @@ void linear8_kernel(const Linear8Args a) {
     const __amdgpu_buffer_rsrc_t r = make_rsrc(p, nk ? (uint32_t)((((int64_t)nk - 1) * ld + cols) * 2) : 0u);
     copy16_to_lds(r, &ring[v & 1][region + (wid * NQ + q) * 64], t[q & 1] + (uint32_t)((int64_t)((q & ~1) * RPC) * ld * 2));
   };
-  auto copy_a = [&](int q, int v, int ks) {
-    if constexpr (AKM) copy_k_major(a.A, a.lda, a.M, ta, 0, q, v, ks);
-    else copy_row_major(ars, a.lda, 0, q, v, ks);
+  auto copy_a = [&](int q, int v, int ks, int plane) {
+    const char* base = Abase + (INT ? 0 : plane * a.plane * 2);
+    if constexpr (AKM) copy_k_major(base, a.lda, (a.M + 7) & ~7, ta, 0, q, v, ks);
+    else copy_row_major(make_rsrc(base, Abytes), a.lda, 0, q, v, ks);
   };
   // expanded B has whole 16-byte chunks behind its last column
   auto copy_b = [&](int q, int v, int ks) {
     copy_k_major(a.B, a.ldb, (a.N + 7) & ~7, tbb, OPS, q, v, ks);
   };
-  // through registers: the same chunks, loaded ahead of being written; fp32 in
-  // two halves, since all four chunks do not fit beside the accumulators
-  constexpr int NH = ASRC == A_REG32 ? NQ / 2 : NQ;
-  Dy8<ASRC> da[NH];
-  auto load_a = [&](int q, int ks) {
-    if constexpr (ASRC != A_DIRECT) {
-      if constexpr (AKM) {
-        const int slot = (wid * NQ + q) * 64 + lane;
-        const int krow = slot / CR, col = row0 + ((slot % CR) ^ swz_t(krow)) * 8;
-        const int k = ks * BK + krow;
-        da[q % NH].load(a.A, (int64_t)k * a.lda + col, k < a.K ? a.M - col : 0);
-      } else {
-        const int r = crow + 8 * q, k = ks * BK + ck[q & 1];
-        da[q % NH].load(a.A, (int64_t)(row0 + r) * a.lda + k, r < rows_a ? a.K - k : 0);
-      }
-    }
-  };
-  auto store_a = [&](int q, int v, int piece) {
-    if constexpr (ASRC != A_DIRECT) ring[v & 1][(wid * NQ + q) * 64 + lane] = da[q % NH].piece(piece);
-  };
-
   // ---- 8-bit operand of the gradients: piece i of a thread is row RSTEP i +
   // tid / CR of the stage, columns 8 (tid % CR) .. + 7 of the tile
   u32x2 bq[NQ];
@@ -329,14 +288,7 @@ void linear8_kernel(const Linear8Args a) {
       constexpr int p = decltype(pc)::value;
       constexpr int i = p / WTN, j = p % WTN;
       constexpr bool needA = j == 0 && AKM, needB = i == 0;  // first uses among the transposed
-      if constexpr (ASRC != A_DIRECT) {
-        // these variants reload arguments in the loop; scalar loads share the
-        // counter and complete out of order, so only zero says anything
-        if constexpr (p == 0) {
-          wait_lgkm0();
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      } else if constexpr (needA || needB) {
+      if constexpr (needA || needB) {
         // position of that fragment in the reading order
         constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : WTN + i);
         constexpr int later_a = AKM ? (WTM - 1 - (at > WTN ? at - WTN : 0)) : 0;
@@ -353,10 +305,11 @@ void linear8_kernel(const Linear8Args a) {
   auto mfma_pair = [&](int p, int slot) {
     Acc8<INT>::mma(acc[p / WTN][p % WTN], fa[slot][p / WTN], fb[slot][p % WTN]);
   };
-  // stage v -> (K-stage, piece); v past the end only refills a slot nobody reads
-  int ksn = ks0, pcn = 0;  // of the stage that is loaded next
+  // K-stage and plane of the stage that is loaded next; past the end the loads
+  // only refill a slot that nobody reads
+  int ksn = ks0, pcn = 0;
   auto advance = [&] {
-    if (++ksn == ks1) {
+    if (++ksn == ks1 && pcn + 1 < a.planes) {
       ksn = ks0;
       ++pcn;
     }
@@ -364,45 +317,23 @@ void linear8_kernel(const Linear8Args a) {
 
   if (nst > 0) {
     // ---- prologue: stage 0 in LDS, stage 1 on its way
-    if constexpr (INT) {
+    auto copies = [&](int v) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) copy_row_major(ars, a.lda, 0, q, v, ks0 + v);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) copy_row_major(brs, a.ldb, OPS, q, v, ks0 + v);
-      }
-      ksn = ks0 + 2;
-      wait_vmcnt<2 * NQ>();
-    } else {
-      load_b(ksn);
+      for (int q = 0; q < NQ; ++q) copy_a(q, v, ksn, pcn);
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        if constexpr (ASRC == A_DIRECT) {
-          copy_a(q, 0, ksn);
-        } else {
-          load_a(q, ksn);
-          store_a(q, 0, 0);
-        }
+        if constexpr (INT) copy_row_major(brs, a.ldb, OPS, q, v, ksn);
+        else if constexpr (!CVT) copy_b(q, v, ksn);
       }
-      if constexpr (BSRC == B_BF16) {
+    };
+    load_b(ksn);
+    copies(0);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) copy_b(q, 0, ksn);
-      }
-#pragma unroll
-      for (int i = 0; i < 4 * NQ; ++i) convert_b(i, 0);
-      advance();
-      wait_vmcnt<0>();
-      load_b(ksn);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if constexpr (ASRC == A_DIRECT) copy_a(q, 1, ksn);
-        if constexpr (BSRC == B_BF16) copy_b(q, 1, ksn);
-      }
-#pragma unroll
-      for (int q = 0; q < NH; ++q) load_a(q, ksn);
-    }
-    int ks_held = ksn, pc_held = pcn;  // stage whose dy is (half) held in registers
+    for (int i = 0; i < 4 * NQ; ++i) convert_b(i, 0);
+    advance();
+    load_b(ksn);
+    copies(1);
+    wait_vmcnt<(CVT ? 3 : 2) * NQ>();  // what was issued for stage 1 may be under way
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < NDR; ++r) read_one(ro(r), 0, 0, 0);
@@ -411,16 +342,6 @@ void linear8_kernel(const Linear8Args a) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int s = 0; s < 3; ++s) {
-        // loads of dy branch at the edges: no untracked read is under way then
-        if (ASRC == A_REG32 && s == 1) {
-          wait_lgkm0();
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int q = 0; q < NH; ++q) store_a(q, v + 1, pc_held);
-#pragma unroll
-          for (int q = NH; q < NQ; ++q) load_a(q, ks_held);
-          __builtin_amdgcn_sched_barrier(0);
-        }
         static_for<0, NPAIR>([&](auto pc) __attribute__((always_inline)) {
           constexpr int p = decltype(pc)::value;
           wait_frag(pc);
@@ -437,9 +358,6 @@ void linear8_kernel(const Linear8Args a) {
             for (int c = 0; c < PER; ++c)
               if (at >= 0 && at * PER + c < 4 * NQ) convert_b(at * PER + c, v + 1);
           }
-          if constexpr (!INT && ASRC != A_DIRECT) {
-            if (s == 2 && p < NH) store_a(NQ - NH + p, v + 1, pc_held);
-          }
           __builtin_amdgcn_sched_barrier(0);
         });
       }
@@ -448,42 +366,21 @@ void linear8_kernel(const Linear8Args a) {
       wait_vmcnt_lgkm0<0>();
       __syncthreads();
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (!INT) {
-        advance();
-        ks_held = ksn;
-        pc_held = pcn;
-        load_b(ksn);
-        if constexpr (ASRC != A_DIRECT) {
-#pragma unroll
-          for (int q = 0; q < NH; ++q) load_a(q, ksn);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+      advance();
+      load_b(ksn);
 #pragma unroll
       for (int p = 0; p < NPAIR; ++p) {
         mfma_pair(p, 1);
-        if constexpr (INT) {
 #pragma unroll
-          for (int c = p; c < 2 * NQ; c += NPAIR) {
-            if (c < NQ) copy_row_major(ars, a.lda, 0, c, v + 2, ksn);
-            else copy_row_major(brs, a.ldb, OPS, c - NQ, v + 2, ksn);
-          }
-        } else {
-#pragma unroll
-          for (int c = p; c < 2 * NQ; c += NPAIR) {
-            if constexpr (ASRC == A_DIRECT) {
-              if (c < NQ) copy_a(c, v + 2, ksn);
-            }
-            if constexpr (BSRC == B_BF16) {
-              if (c >= NQ) copy_b(c - NQ, v + 2, ksn);
-            }
-          }
+        for (int c = p; c < 2 * NQ; c += NPAIR) {
+          if (c < NQ) copy_a(c, v + 2, ksn, pcn);
+          else if constexpr (INT) copy_row_major(brs, a.ldb, OPS, c - NQ, v + 2, ksn);
+          else if constexpr (!CVT) copy_b(c - NQ, v + 2, ksn);
         }
 #pragma unroll
         for (int r = p; r < NDR; r += NPAIR) read_one(ro(r), v + 1, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (INT) ++ksn;
     }
     wait_vmcnt_lgkm0<0>();  // trailing copies and reads
     __builtin_amdgcn_sched_barrier(0);

@@ -6,11 +6,11 @@
 
 namespace muon {
 
-template <int MODE, int ASRC, int BSRC, int T> hipError_t linear8_go(int odt, const Linear8Args& a, hipStream_t s) {
+template <int MODE, int BSRC, int T> hipError_t linear8_go(int odt, const Linear8Args& a, hipStream_t s) {
   constexpr int NW = T / 32;
   const dim3 g((unsigned)(a.tilesM * a.tilesN * a.splits)), b(64 * NW);
   if (a.splits > 1) {
-    hipLaunchKernelGGL((linear8_kernel<MODE, ASRC, BSRC, T, NW, float, true>), g, b, 0, s, a);
+    hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, float, true>), g, b, 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t pieces = (int64_t)a.M * ((a.N + 7) / 8);
@@ -19,21 +19,14 @@ template <int MODE, int ASRC, int BSRC, int T> hipError_t linear8_go(int odt, co
     else hipLaunchKernelGGL((linear8_join_kernel<MODE == L8_Y, float>), gj, dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  if (odt == DT_BF16) hipLaunchKernelGGL((linear8_kernel<MODE, ASRC, BSRC, T, NW, bf16, false>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((linear8_kernel<MODE, ASRC, BSRC, T, NW, float, false>), g, b, 0, s, a);
+  if (odt == DT_BF16) hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, bf16, false>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, float, false>), g, b, 0, s, a);
   return hipGetLastError();
 }
 
-template <int MODE, int BSRC, int T> hipError_t linear8_by_dy(int asrc, int odt, const Linear8Args& a, hipStream_t s) {
-  if (asrc == A_DIRECT) return linear8_go<MODE, A_DIRECT, BSRC, T>(odt, a, s);
-  if (asrc == A_REG16) return linear8_go<MODE, A_REG16, BSRC, T>(odt, a, s);
-  return linear8_go<MODE, A_REG32, BSRC, T>(odt, a, s);
-}
-
-template <int MODE>
-hipError_t linear8_grad_any(int tile, bool expanded, int asrc, int odt, const Linear8Args& a, hipStream_t s) {
-  if (tile == 128) return linear8_by_dy<MODE, B_Q8, 128>(asrc, odt, a, s);
-  return expanded ? linear8_by_dy<MODE, B_BF16, 256>(asrc, odt, a, s) : linear8_by_dy<MODE, B_Q8, 256>(asrc, odt, a, s);
+template <int MODE> hipError_t linear8_grad_any(int tile, bool expanded, int odt, const Linear8Args& a, hipStream_t s) {
+  if (tile == 128) return linear8_go<MODE, B_Q8, 128>(odt, a, s);
+  return expanded ? linear8_go<MODE, B_BF16, 256>(odt, a, s) : linear8_go<MODE, B_Q8, 256>(odt, a, s);
 }
 
 }  // namespace muon

@@ -17,8 +17,16 @@ hipError_t launch_linear8_few(int odt, const Linear8Args& a, hipStream_t s) {
   return a.M <= 16 ? few<1>(odt, a, s) : a.M <= 32 ? few<2>(odt, a, s) : few<4>(odt, a, s);
 }
 
+hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s) {
+  const int64_t blocks = (a.rows * a.per_row + 255) / 256;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (dt == DT_BF16) hipLaunchKernelGGL((linear8_planes_kernel<bf16>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((linear8_planes_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_linear8_forward(int tile, int odt, const Linear8Args& a, hipStream_t s) {
-  return tile == 256 ? linear8_go<L8_Y, A_DIRECT, B_Q8, 256>(odt, a, s)
-                     : linear8_go<L8_Y, A_DIRECT, B_Q8, 128>(odt, a, s);
+  return tile == 256 ? linear8_go<L8_Y, B_Q8, 256>(odt, a, s)
+                     : linear8_go<L8_Y, B_Q8, 128>(odt, a, s);
 }
 }  // namespace muon

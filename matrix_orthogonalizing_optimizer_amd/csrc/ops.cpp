@@ -44,17 +44,23 @@ size_t norm_ws(int64_t rows, int64_t cols) {
   return (size_t)norm_parts(rows, cols) * (size_t)cols * 2 * sizeof(float) + WS_ALIGN;
 }
 
-// Tile and split of a product of the 8-bit linear layer; depends on the sizes
-// only, so that the workspace query and the call agree.
+// How dy enters a gradient product: as it lies (0 planes to make), or laid out
+// as bf16 planes in the workspace.
+int dy_planes(const void* dy, int64_t lddy, int64_t out, int32_t dtype) {
+  if (dtype == MUON_F32) return 3;
+  return at_or_null(dy, 16) && lddy % 8 == 0 && out % 8 == 0 ? 0 : 1;
+}
+
+// Tile, split and workspace of a product of the 8-bit linear layer.
 struct Linear8Plan {
   bool few;       // few tokens: no tiles
   bool expanded;  // gradients: the 8-bit operand as bf16 in the workspace first
   int tile, splits, per_split;
-  int64_t ldws, ldx;
-  size_t ws_off;  // partial results behind the expanded operand
+  int64_t ldws, ldx, lddy;
+  size_t dy_off, ws_off;  // workspace: expanded operand, planes of dy, partial results
   size_t bytes;
 };
-Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in) {
+Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int planes) {
   const int64_t M = pass == MUON_LINEAR8_WEIGHT_GRAD ? out : tokens;
   const int64_t N = pass == MUON_LINEAR8_FORWARD ? out : in;
   const int64_t K = pass == MUON_LINEAR8_FORWARD ? in : pass == MUON_LINEAR8_WEIGHT_GRAD ? tokens : out;
@@ -66,8 +72,8 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in) {
   // us; 14336 x 4096, 32 tokens: 29.8 against 24).
   p.few = pass == MUON_LINEAR8_FORWARD && (tokens <= 16 || (tokens <= 64 && out * in <= ((int64_t)1 << 24)));
   p.expanded = false;
-  p.ldx = 0;
-  p.ws_off = 0;
+  p.ldx = p.lddy = 0;
+  p.dy_off = p.ws_off = 0;
   if (p.few) {
     p.tile = 128;
     p.splits = 1;
@@ -87,7 +93,12 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in) {
   p.expanded = pass != MUON_LINEAR8_FORWARD && p.tile == 256 && M >= 2048;
   if (p.expanded) {
     p.ldx = (N + 63) / 64 * 64;
-    p.ws_off = (size_t)K * (size_t)p.ldx * 2;
+    p.dy_off = (size_t)K * (size_t)p.ldx * 2;
+  }
+  p.ws_off = p.dy_off;
+  if (planes) {
+    p.lddy = (out + 63) / 64 * 64;
+    p.ws_off += (size_t)planes * (size_t)tokens * (size_t)p.lddy * 2;
   }
   p.bytes = p.ws_off + (p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)p.ldws * sizeof(float) : 0);
   if (p.bytes) p.bytes += WS_ALIGN;
@@ -239,12 +250,16 @@ muon_status muon_norm_backward(int32_t kind, const void* dy, int64_t lddy, const
   return MUON_OK;
 }
 
-muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t out, int64_t in, size_t* bytes) {
+muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t out, int64_t in, const void* dy,
+                                         int64_t lddy, int32_t dy_dtype, size_t* bytes) {
   if (!bytes) return MUON_E_ARG;
   if (pass < MUON_LINEAR8_FORWARD || pass > MUON_LINEAR8_INPUT_GRAD) return MUON_E_METHOD;
   if (!side_ok(tokens) || !side_ok(out) || !side_ok(in) || (pass == MUON_LINEAR8_FORWARD && in > MAX_IN))
     return MUON_E_SHAPE;
-  *bytes = tokens && out && in ? linear8_plan(pass, tokens, out, in).bytes : 0;
+  const bool grad = pass != MUON_LINEAR8_FORWARD;
+  if (grad && !dtype_ok(dy_dtype)) return MUON_E_DTYPE;
+  const int planes = grad ? dy_planes(dy, lddy, out, dy_dtype) : 0;
+  *bytes = tokens && out && in ? linear8_plan(pass, tokens, out, in, planes).bytes : 0;
   return MUON_OK;
 }
 
@@ -260,7 +275,7 @@ muon_status muon_linear8_forward(const int8_t* q, int64_t ldq, const float* scal
   if (!at(scale, 4) || !at(wscale, 4) || !at(y, esize(dtype)) || (bias && !at(bias, esize(bias_dtype))) ||
       (in > 0 && (!at(q, 16) || !at(wq, 16))))
     return MUON_E_ARG;
-  const Linear8Plan p = linear8_plan(MUON_LINEAR8_FORWARD, tokens, out, in);
+  const Linear8Plan p = linear8_plan(MUON_LINEAR8_FORWARD, tokens, out, in, 0);
   if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MUON_E_WORKSPACE;
   Linear8Args a;
   std::memset(&a, 0, sizeof(a));
@@ -269,6 +284,7 @@ muon_status muon_linear8_forward(const int8_t* q, int64_t ldq, const float* scal
   a.B = wq; a.ldb = ldw; a.sb = wscale;
   a.bias = bias; a.bias_dtype = dev_dt(bias_dtype);
   a.o = y; a.ldo = ldy;
+  a.planes = 1;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
   return done(timed(F_LINEAR8_Y, f, 0.0, s, [&] {
@@ -289,12 +305,24 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
   if (!at(o, esize(o_dtype)) || (sum > 0 && (!at(dy, esize(dy_dtype)) || !at(q, 16) || !at(scale, 4))))
     return MUON_E_ARG;
   const int pass = weight ? MUON_LINEAR8_WEIGHT_GRAD : MUON_LINEAR8_INPUT_GRAD;
-  const Linear8Plan p = linear8_plan(pass, tokens, out, in);
+  const int planes = sum > 0 ? dy_planes(dy, lddy, out, dy_dtype) : 0;
+  const Linear8Plan p = linear8_plan(pass, tokens, out, in, planes);
   if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MUON_E_WORKSPACE;
   Linear8Args a;
   std::memset(&a, 0, sizeof(a));
   if (!linear8_args(p, rows, in, sum, workspace, a)) return MUON_E_SHAPE;
   a.A = dy; a.lda = lddy;
+  a.planes = planes ? planes : 1;
+  PlanesArgs d;
+  std::memset(&d, 0, sizeof(d));
+  if (planes) {
+    d.dy = dy; d.ld = lddy;
+    d.o = ws_base(workspace) + p.dy_off; d.ldo = p.lddy;
+    d.plane = tokens * p.lddy;
+    d.rows = tokens; d.cols = (int32_t)out; d.per_row = (out + 7) / 8;
+    a.A = d.o; a.lda = p.lddy;
+    a.plane = d.plane;
+  }
   a.B = q; a.ldb = ldq; a.sb = scale;
   a.o = o; a.ldo = ldo;
   a.accumulate = accumulate;
@@ -306,17 +334,19 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
     x.rows = sum; x.cols = (int32_t)in; x.per_row = (in + 15) / 16;
     a.B = x.y; a.ldb = p.ldx;
   }
-  // direct copies of dy take 16-byte pieces that lie wholly inside a row
-  const int asrc = dy_dtype == MUON_F32 ? 2 : at(dy, 16) && lddy % 8 == 0 && out % 8 == 0 ? 0 : 1;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
   return done(timed(weight ? F_LINEAR8_DW : F_LINEAR8_DX, f, 0.0, s, [&] {
+    if (planes) {
+      const hipError_t e = launch_linear8_planes(dev_dt(dy_dtype), d, s);
+      if (e != hipSuccess) return e;
+    }
     if (p.expanded) {
       const hipError_t e = launch_row_restore(DT_BF16, x, s);
       if (e != hipSuccess) return e;
     }
-    return weight ? launch_linear8_dw(p.tile, p.expanded, asrc, dev_dt(o_dtype), a, s)
-                  : launch_linear8_dx(p.tile, p.expanded, asrc, dev_dt(o_dtype), a, s);
+    return weight ? launch_linear8_dw(p.tile, p.expanded, dev_dt(o_dtype), a, s)
+                  : launch_linear8_dx(p.tile, p.expanded, dev_dt(o_dtype), a, s);
   }));
 }
 

@@ -178,10 +178,11 @@ def test_workspace_queries():
     n = ctypes.c_size_t()
     assert L.muon_norm_backward_workspace_bytes(8, 8, None) == E_ARG
     assert L.muon_norm_backward_workspace_bytes(-1, 8, ctypes.byref(n)) == E_SHAPE
-    assert L.muon_linear8_workspace_bytes(0, 8, 8, 8, None) == E_ARG
-    assert L.muon_linear8_workspace_bytes(3, 8, 8, 8, ctypes.byref(n)) == E_METHOD
-    assert L.muon_linear8_workspace_bytes(1, 8, -8, 8, ctypes.byref(n)) == E_SHAPE
-    assert L.muon_linear8_workspace_bytes(0, 8, 8, 1 << 20, ctypes.byref(n)) == E_SHAPE
+    assert L.muon_linear8_workspace_bytes(0, 8, 8, 8, None, 0, 0, None) == E_ARG
+    assert L.muon_linear8_workspace_bytes(3, 8, 8, 8, None, 0, 0, ctypes.byref(n)) == E_METHOD
+    assert L.muon_linear8_workspace_bytes(1, 8, 8, 8, None, 8, 2, ctypes.byref(n)) == E_DTYPE
+    assert L.muon_linear8_workspace_bytes(1, 8, -8, 8, None, 0, 0, ctypes.byref(n)) == E_SHAPE
+    assert L.muon_linear8_workspace_bytes(0, 8, 8, 1 << 20, None, 0, 0, ctypes.byref(n)) == E_SHAPE
     assert mo.muon_norm_backward_workspace_bytes(0, 8) == 0
     assert mo.muon_norm_backward_workspace_bytes(100, 8) >= 2 * 8 * 4
 
