@@ -60,6 +60,34 @@ struct Linear8Plan {
   size_t dy_off, ws_off;  // workspace: expanded operand, planes of dy, partial results
   size_t bytes;
 };
+// Estimated time of a tiled product in us, from measurements of these kernels on
+// one MI355X (what the choice between tiles and splits rests on; within 15% of
+// the measured times on 17 shapes from 512 x 512 x 512 to 4096 x 4096 x 2048).
+// Per stage of K (128 bytes of a row):
+//   128 tiles   one workgroup on a CU 1.06 (forward 0.60), two 1.58 (1.05):
+//               bound by issue and LDS latency, not by memory (a ring of four
+//               stages was no faster)
+//   256 tiles   1.75 converting the 8-bit operand, 1.5 on the expanded one or
+//               for the forward product: bound by power at full load
+// and per round of workgroups 4 (2) or 12 for prologue and epilogue, 4 for the
+// second launch of a split product, and its partial tiles at 6 TB/s.
+double linear8_cost(bool fwd, int tile, bool expanded, int64_t M, int64_t N, int64_t K, int64_t nks, int64_t z,
+                    int planes) {
+  const int64_t wgs = ((M + tile - 1) / tile) * ((N + tile - 1) / tile) * z;
+  const double stages = (double)((nks + z - 1) / z) * planes;
+  double us;
+  if (tile == 128) {
+    const double alone = stages * (fwd ? 0.60 : 1.06) + (fwd ? 2 : 4), pair = stages * (fwd ? 1.05 : 1.58) + (fwd ? 2 : 4);
+    const int64_t rem = wgs % 512;
+    us = (double)(wgs / 512) * pair + (rem == 0 ? 0.0 : rem <= 256 ? alone : pair);
+  } else {
+    us = (double)((wgs + 255) / 256) * (stages * (fwd || expanded ? 1.5 : 1.75) + 12);
+  }
+  if (z > 1) us += 4 + 8.0 * (double)z * (double)M * (double)N / 6e6;
+  if (expanded) us += 4 + 3.0 * (double)K * (double)N / 5e6;  // one byte read, two written
+  return us;
+}
+
 Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int planes) {
   const int64_t M = pass == MUON_LINEAR8_WEIGHT_GRAD ? out : tokens;
   const int64_t N = pass == MUON_LINEAR8_FORWARD ? out : in;
@@ -82,15 +110,25 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
     p.bytes = 0;
     return p;
   }
-  auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
-  p.tile = tiles(256) >= 192 ? 256 : 128;
-  const int64_t slots = p.tile == 256 ? 256 : 512;
-  int64_t z = std::max<int64_t>(1, slots / std::max<int64_t>(1, tiles(p.tile)));
-  z = std::max<int64_t>(1, std::min<int64_t>(z, nks / 4));
+  const bool fwd = pass == MUON_LINEAR8_FORWARD;
+  double best = 0.0;
+  int64_t z = 0;
+  for (int option = 0; option < (fwd ? 2 : 3); ++option) {
+    const int tile = option == 0 ? 128 : 256;
+    const bool expanded = option == 2;
+    for (int64_t t = 1; t <= std::max<int64_t>(1, std::min<int64_t>(nks, 32)); ++t) {
+      const double us = linear8_cost(fwd, tile, expanded, M, N, K, nks, t, planes ? planes : 1);
+      if (z == 0 || us < best) {
+        best = us;
+        p.tile = tile;
+        p.expanded = expanded;
+        z = t;
+      }
+    }
+  }
   p.per_split = (int)std::max<int64_t>(1, (nks + z - 1) / z);
   p.splits = (int)std::max<int64_t>(1, (nks + p.per_split - 1) / p.per_split);
   p.ldws = (N + 7) / 8 * 8;
-  p.expanded = pass != MUON_LINEAR8_FORWARD && p.tile == 256 && M >= 2048;
   if (p.expanded) {
     p.ldx = (N + 63) / 64 * 64;
     p.dy_off = (size_t)K * (size_t)p.ldx * 2;
