@@ -73,7 +73,6 @@ struct RestoreArgs {
   const float* scale;
   void* y;
   int64_t ldq, ldy, rows;
-  int64_t per_row;  // pieces of 16 columns per row
   int32_t cols;
 };
 struct NormBwdArgs {

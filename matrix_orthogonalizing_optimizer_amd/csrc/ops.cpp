@@ -188,7 +188,7 @@ muon_status muon_rows8_dequantize(const int8_t* q, int64_t ldq, const float* sca
   std::memset(&a, 0, sizeof(a));
   a.q = q; a.ldq = ldq; a.scale = scale;
   a.y = y; a.ldy = ldy;
-  a.rows = rows; a.cols = (int32_t)cols; a.per_row = (cols + 15) / 16;
+  a.rows = rows; a.cols = (int32_t)cols;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double n = (double)rows * (double)cols;
   return done(timed(F_ROWS8, 0.0, n * (double)(esize(dtype) + 1), s,
@@ -369,7 +369,7 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
   if (p.expanded) {
     x.q = q; x.ldq = ldq; x.scale = scale;
     x.y = ws_base(workspace); x.ldy = p.ldx;
-    x.rows = sum; x.cols = (int32_t)in; x.per_row = (in + 15) / 16;
+    x.rows = sum; x.cols = (int32_t)in;
     a.B = x.y; a.ldb = p.ldx;
   }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -64,12 +64,20 @@ hipError_t launch_row_forward(int kind, int dt, const RowArgs& a, hipStream_t s)
   return kind == 0 ? forward<float, 0>(a, s) : kind == 1 ? forward<float, 1>(a, s) : forward<float, ROW_COPY>(a, s);
 }
 
+namespace {
+template <typename T> hipError_t restore(const RestoreArgs& a, hipStream_t s) {
+  return by_width(a.cols, [&](auto g, auto nv) {
+    constexpr int G = decltype(g)::value, NV = decltype(nv)::value;
+    constexpr int RPW = G < 256 ? 256 / G : 1;
+    hipLaunchKernelGGL((row_restore_kernel<T, G, NV>), dim3((unsigned)((a.rows + RPW - 1) / RPW)),
+                       dim3(G < 256 ? 256 : G), 0, s, a);
+    return hipGetLastError();
+  });
+}
+}  // namespace
+
 hipError_t launch_row_restore(int dt, const RestoreArgs& a, hipStream_t s) {
-  const int64_t blocks = (a.rows * a.per_row + DEQ_PIECES - 1) / DEQ_PIECES;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (dt == DT_BF16) hipLaunchKernelGGL((row_restore_kernel<bf16>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((row_restore_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return dt == DT_BF16 ? restore<bf16>(a, s) : restore<float>(a, s);
 }
 
 hipError_t launch_norm_backward(int kind, int dt, const NormBwdArgs& a, int parts, hipStream_t s) {

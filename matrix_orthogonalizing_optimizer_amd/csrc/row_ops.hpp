@@ -343,31 +343,28 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
   }
 }
 
-// Restore: y = q * scale.  16 columns per thread; a workgroup takes 1024
-// consecutive pieces of the rows x ceil(cols / 16) grid of pieces.
-constexpr int DEQ_PIECES = 1024;
-template <typename T>
-__global__ __launch_bounds__(256) void row_restore_kernel(const RestoreArgs a) {
-  const int64_t total = a.rows * a.per_row;
-  const int64_t base = (int64_t)blockIdx.x * DEQ_PIECES;
-  const int64_t row0 = base / a.per_row;
-  const uint32_t first = (uint32_t)(base - row0 * a.per_row);
+// Restore: y = q * scale.  A row per group of G threads, NV pieces of 8
+// columns each at a time (8-byte loads, 16- or 32-byte stores).
+template <typename T, int G, int NV>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void row_restore_kernel(const RestoreArgs a) {
+  constexpr int RPW = G < 256 ? 256 / G : 1;
+  const int t = threadIdx.x % G;
+  const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / G;
+  if (row >= a.rows) return;
+  const int8_t* q = a.q + row * a.ldq;
+  T* y = static_cast<T*>(a.y) + row * a.ldy;
+  const float s = as_global(a.scale)[row];
+  for (int64_t c0 = (int64_t)t * ROW_VE; c0 < a.cols; c0 += NV * G * ROW_VE) {
+    u32x2 w[NV];
 #pragma unroll
-  for (int i = 0; i < DEQ_PIECES / 256; ++i) {
-    const uint32_t p = i * 256 + threadIdx.x;
-    if (base + p >= total) return;
-    const uint32_t dr = (first + p) / (uint32_t)a.per_row;
-    const int c = (int)((first + p) - dr * (uint32_t)a.per_row) * 16;
-    const int64_t row = row0 + dr;
-    const u32x4 w = *as_global(reinterpret_cast<const u32x4*>(a.q + row * a.ldq + c));
-    const float s = as_global(a.scale)[row];
-    T* y = static_cast<T*>(a.y) + row * a.ldy;
+    for (int i = 0; i < NV; ++i)
+      if (c0 + i * G * ROW_VE < a.cols) w[i] = *as_global(reinterpret_cast<const u32x2*>(q + c0 + i * G * ROW_VE));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < NV; ++i) {
       float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(w[2 * h + (e >> 2)] >> (8 * (e & 3))) * s;
-      if (c + 8 * h < a.cols) piece_store(y, c + 8 * h, a.cols, v);
+      for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(w[i][e >> 2] >> (8 * (e & 3))) * s;
+      if (c0 + i * G * ROW_VE < a.cols) piece_store(y, (int)(c0 + i * G * ROW_VE), a.cols, v);
     }
   }
 }
