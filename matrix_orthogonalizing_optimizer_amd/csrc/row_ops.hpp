@@ -7,9 +7,9 @@
 //   dgamma = sum_rows dy h,  dbeta = sum_rows dy;
 //   8-bit rows: s = 2^e with max|y| <= 127 s, q = rne(y / s).
 // All of it is bound by HBM: a row is read once and kept in registers (fp32)
-// by a group of G threads, G = 64 (one wave, no barrier) up to 1024 columns
-// and wider groups above, so that a thread holds at most two pieces of 8
-// columns.  Rows longer than that allows are read again for each pass.
+// by a group of G threads: a part of a wave or a wave up to 1024 columns (no
+// barrier), 256 to 1024 threads with one or two pieces of 8 columns each above.
+// Rows longer than that allows are read again for each pass.
 #pragma once
 
 #include "device_common.hpp"
@@ -80,18 +80,20 @@ __device__ __forceinline__ void vec_load(const void* p, int dt, int c, int cols,
   else piece_load(static_cast<const bf16*>(p), c, cols, v);
 }
 
-// Deterministic sums over a group of G threads (a whole number of waves):
-// butterfly inside a wave, waves in order.  G > 64: all threads of the
+// Deterministic sums over a group of G threads (a part of a wave, or whole
+// waves): butterfly inside a wave, waves in order.  G > 64: all threads of the
 // workgroup take part and `red` is one of two alternating buffers, so one
 // barrier per sum is enough (a wave writes a buffer again only after the
 // barrier of the sum in between, which every reader of it has passed).
 template <int G, int N> struct GroupRed {
-  float slot[2][G / 64][N];
+  float slot[2][G < 64 ? 1 : G / 64][N];
 };
 template <int G, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], GroupRed<G, N>& red, int buf) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+  for (int off = (G < 64 ? G : 64) / 2; off >= 1; off >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], off, 64);
   if constexpr (G > 64) {
     const int w = (threadIdx.x % G) >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -117,7 +119,7 @@ __device__ __forceinline__ void group_sum(float (&v)[N], GroupRed<G, N>& red, in
 template <int G>
 __device__ __forceinline__ uint32_t group_umax(uint32_t v, GroupRed<G, 1>& red, int buf) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
+  for (int off = (G < 64 ? G : 64) / 2; off >= 1; off >>= 1) {
     const uint32_t o = (uint32_t)__shfl_xor((int)v, off, 64);
     v = v > o ? v : o;
   }
@@ -181,7 +183,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_forward_kernel(const Ro
   __shared__ GroupRed<G, 1> red;
   const int t = threadIdx.x % G;
   const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / G;
-  if (G < 256 && row >= a.rows) return;  // whole waves, and no barrier below when G == 64
+  if (G < 256 && row >= a.rows) return;  // whole groups, and no barrier below when G < 256
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   float v[NV][8];
 #pragma unroll
