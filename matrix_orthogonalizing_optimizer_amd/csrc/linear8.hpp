@@ -163,6 +163,10 @@ void linear8_kernel(const Linear8Args a) {
 
   auto swz_t = [](int krow) { return ((krow & 1) << 2) ^ (((krow >> 1) & 1) * 10); };
 
+  // summation rows of K-stage ks.  The clamp compiles to a vector instruction:
+  // back to a scalar register, or the buffer resources built from it count as
+  // divergent and each load runs in a waterfall loop (0.3 us of a stage)
+  auto stage_rows = [&](int ks) { return __builtin_amdgcn_readfirstlane(max(0, min(BK, a.K - ks * BK))); };
   // ---- operand A (and B for L8_Y), row-major: rows of the tile
   const int rows_a = min(T, a.M - row0);
   const char* Abase = static_cast<const char*>(a.A) + (AKM ? 0 : (int64_t)row0 * a.lda * ES);
@@ -190,7 +194,7 @@ void linear8_kernel(const Linear8Args a) {
   const uint32_t ta[2] = {km_offset(0, a.lda, row0, a.M), km_offset(1, a.lda, row0, a.M)};
   const uint32_t tbb[2] = {km_offset(0, a.ldb, col0, a.N), km_offset(1, a.ldb, col0, a.N)};
   auto copy_k_major = [&](const void* base, int64_t ld, int cols, const uint32_t(&t)[2], int region, int q, int v, int ks) {
-    const int nk = max(0, min(BK, a.K - ks * BK));
+    const int nk = stage_rows(ks);
     const char* p = static_cast<const char*>(base) + (int64_t)ks * BK * ld * 2;
     const __amdgpu_buffer_rsrc_t r = make_rsrc(p, nk ? (uint32_t)((((int64_t)nk - 1) * ld + cols) * 2) : 0u);
     copy16_to_lds(r, &ring[v & 1][region + (wid * NQ + q) * 64], t[q & 1] + (uint32_t)((int64_t)((q & ~1) * RPC) * ld * 2));
@@ -213,7 +217,7 @@ void linear8_kernel(const Linear8Args a) {
   const int bslot = OPS + brow * CR + ((tid % CR) ^ swz_t(brow));
   auto load_b = [&](int ks) {
     if constexpr (CVT) {
-      const int nk = max(0, min(BK, a.K - ks * BK));
+      const int nk = stage_rows(ks);
       const __amdgpu_buffer_rsrc_t r =
           make_rsrc(static_cast<const int8_t*>(a.B) + (int64_t)ks * BK * a.ldb, (uint32_t)((int64_t)nk * a.ldb));
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.sb + (int64_t)ks * BK, (uint32_t)(nk * 4));
