@@ -63,31 +63,36 @@ struct Linear8Plan {
   size_t dy_off, ws_off;  // workspace: expanded operand, planes of dy, partial results
   size_t bytes;
 };
-// Estimated time of a tiled product in us, from measurements of these kernels on
-// one MI355X (what the choice between tiles and splits rests on; within 15% of
-// the measured times on 17 shapes from 512 x 512 x 512 to 4096 x 4096 x 2048).
-// Per stage of K (128 bytes of a row):
-//   128 tiles   one workgroup on a CU 1.06 (forward 0.60), two 1.58 (1.05):
-//               bound by issue and LDS latency, not by memory (a ring of four
-//               stages was no faster)
-//   256 tiles   1.75 converting the 8-bit operand, 1.5 on the expanded one or
-//               for the forward product: bound by power at full load
-// and per round of workgroups 4 (2) or 12 for prologue and epilogue, 4 for the
-// second launch of a split product, and its partial tiles at 6 TB/s.
+// Estimated time of a tiled product in us: what the choice between tiles,
+// splits and expansion rests on.  The constants are fitted to 1018 timings of
+// these kernels on one MI355X (21 shapes from 512 x 512 x 512 to 8192 x 4096 x
+// 14336, all three passes; 10% rms; the choice costs 3% against the best one
+// timed).  Per stage of K (128 bytes of a row):
+//   128 tiles  0.86 with one workgroup on a CU, 1.19 with two (forward 0.55,
+//              0.96): bound by issue and LDS, not by memory (a ring of four
+//              stages in LDS was no faster)
+//   256 tiles  1.71 converting the 8-bit operand, 1.32 on the expanded one (forward
+//              1.44) with all CUs at work, down to 0.84 (0.69) of it with few:
+//              bound by power at full load
+// and a constant per round of workgroups; a second launch and partial tiles for
+// a split; a launch and 3 bytes per element for the expansion.
 double linear8_cost(bool fwd, int tile, bool expanded, int64_t M, int64_t N, int64_t K, int64_t nks, int64_t z,
                     int planes) {
   const int64_t wgs = ((M + tile - 1) / tile) * ((N + tile - 1) / tile) * z;
   const double stages = (double)((nks + z - 1) / z) * planes;
   double us;
   if (tile == 128) {
-    const double alone = stages * (fwd ? 0.60 : 1.06) + (fwd ? 2 : 4), pair = stages * (fwd ? 1.05 : 1.58) + (fwd ? 2 : 4);
+    const double once = fwd ? 6.1 : 4.9;
+    const double alone = stages * (fwd ? 0.55 : 0.86) + once, pair = stages * (fwd ? 0.96 : 1.19) + once;
     const int64_t rem = wgs % 512;
     us = (double)(wgs / 512) * pair + (rem == 0 ? 0.0 : rem <= 256 ? alone : pair);
   } else {
-    us = (double)((wgs + 255) / 256) * (stages * (fwd || expanded ? 1.5 : 1.75) + 12);
+    const double low = fwd ? 0.69 : 0.84, fill = std::min(1.0, (double)wgs / 256.0);
+    const double stage = (fwd ? 1.44 : expanded ? 1.32 : 1.71) * (low + (1.0 - low) * fill);
+    us = (double)((wgs + 255) / 256) * (stages * stage + (fwd ? 9.3 : 7.6));
   }
-  if (z > 1) us += 4 + 8.0 * (double)z * (double)M * (double)N / 6e6;
-  if (expanded) us += 4 + 3.0 * (double)K * (double)N / 5e6;  // one byte read, two written
+  if (z > 1) us += (fwd ? 3.3 : 5.9) + 8.0 * (double)z * (double)M * (double)N / (fwd ? 7.7e6 : 9.0e6);
+  if (expanded) us += 3.3 + 3.0 * (double)K * (double)N / 5.3e6;
   return us;
 }
 
