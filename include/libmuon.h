@@ -455,7 +455,8 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
  * gradient is; with in == 0 y is the bias.
  * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, in above
  * 131071 for the forward product, a leading dimension below its column count
- * or above 2^21, ldq or ldw not a multiple of 16); MUON_E_ARG (a pointer null
+ * or above 2^21, ldq or ldw not a multiple of 16, a result of more than 2^24
+ * 128 x 128 tiles); MUON_E_ARG (a pointer null
  * or misaligned: 8-bit rows to 16 bytes, others to their element);
  * MUON_E_WORKSPACE (workspace smaller than muon_linear8_workspace_bytes);
  * MUON_E_HIP. */

@@ -108,10 +108,12 @@ struct Linear8Args {
   const float* sb;    // forward: one per column of C; gradients: one per summation index
   const void* bias;   // forward: one per column of C, or null
   void* o;            // C
-  float* ws;          // [splits][M][ldws] partial results
-  int64_t lda, ldb, ldo, ldws;
+  float* ws;          // partial tiles
+  int64_t lda, ldb, ldo;
   int32_t M, N, K;
-  int32_t tilesM, tilesN, splits;
+  int32_t tilesM, tilesN;
+  int32_t whole;      // tiles computed whole; the others in `splits` parts (all whole if splits is 1)
+  int32_t splits;
   int32_t per_split;  // K-stages (128 bytes of a row) per split
   int32_t bias_dtype;
   int32_t accumulate;

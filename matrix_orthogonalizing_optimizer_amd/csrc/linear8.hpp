@@ -30,8 +30,10 @@
 // fp32 as three bf16 planes that sum to it exactly (8 significant bits each);
 // K is then walked once per plane.
 //
-// K may be split over workgroups that then leave partial tiles in the
-// workspace (PART); linear8_join_kernel adds them in order.
+// The first `whole` tiles, as many as fill the chip in full rounds, are computed
+// by one workgroup each; the K of the others (all of them, if the product has
+// few) is split over workgroups that leave partial tiles in the workspace, and
+// linear8_join_kernel adds those in order.
 #pragma once
 
 #include "device_common.hpp"
@@ -102,32 +104,32 @@ __global__ __launch_bounds__(256) void linear8_planes_kernel(const PlanesArgs a)
   }
 }
 
-// Workgroup -> (split, tile row, tile column), spread over the XCDs in
-// groups of 4 tile rows as the optimizer's products are (gemm.hpp).
-__device__ __forceinline__ void linear8_tile(const Linear8Args& a, int& split, int& bi, int& bj) {
-  const int per = a.tilesM * a.tilesN, tot = per * a.splits;
-  const int b = blockIdx.x, xcd = b & 7, loc = b >> 3;
-  const int S = 8 * a.tilesN;
+// Workgroups are spread over the XCDs in chunks of S consecutive pieces of
+// work, as the optimizer's products are (gemm.hpp): a bijection of [0, tot).
+__device__ __forceinline__ int linear8_deal(int b, int tot, int S) {
+  const int xcd = b & 7, loc = b >> 3;
   const int full = tot / (8 * S);
-  int logical;
-  if (loc < full * S) {
-    logical = (loc / S) * 8 * S + xcd * S + loc % S;
-  } else {
-    const int rest = tot - full * 8 * S, q = rest >> 3, r = rest & 7;
-    logical = full * 8 * S + xcd * q + (xcd < r ? xcd : r) + (loc - full * S);
-  }
-  split = __builtin_amdgcn_readfirstlane(logical / per);
-  const int tt = __builtin_amdgcn_readfirstlane(logical - split * per);
+  if (loc < full * S) return (loc / S) * 8 * S + xcd * S + loc % S;
+  const int rest = tot - full * 8 * S, q = rest >> 3, r = rest & 7;
+  return full * 8 * S + xcd * q + (xcd < r ? xcd : r) + (loc - full * S);
+}
+// Tile number -> tile row and column: groups of 4 tile rows, column by column.
+__device__ __forceinline__ void linear8_tile(const Linear8Args& a, int tile, int& bi, int& bj) {
   constexpr int GROUP = 4;
-  const int g = tt / (GROUP * a.tilesN);
+  const int g = tile / (GROUP * a.tilesN);
   const int first = g * GROUP;
   const int gm = min(a.tilesM - first, GROUP);
-  const int w = tt - g * GROUP * a.tilesN;
-  bi = __builtin_amdgcn_readfirstlane(first + w % gm);
-  bj = __builtin_amdgcn_readfirstlane(w / gm);
+  const int w = tile - g * GROUP * a.tilesN;
+  bi = first + w % gm;
+  bj = w / gm;
 }
 
-template <int MODE, int BSRC, int T, int NW, typename TO, bool PART>
+// Partial tile of a split: [splits][tiles from `whole` on][T][T] in the workspace.
+template <int T> __device__ __forceinline__ int64_t linear8_part(const Linear8Args& a, int tile, int split) {
+  return ((int64_t)split * (a.tilesM * a.tilesN - a.whole) + (tile - a.whole)) * (T * T);
+}
+
+template <int MODE, int BSRC, int T, int NW, typename TO>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(T == 128 ? 2 : NW / 4, T == 128 ? 2 : NW / 4)))
 void linear8_kernel(const Linear8Args a) {
   constexpr bool INT = MODE == L8_Y;
@@ -152,13 +154,28 @@ void linear8_kernel(const Linear8Args a) {
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / WGN, wn = wid % WGN;
   const int half = lane >> 5, l32 = lane & 31;
-  int split, bi, bj;
-  linear8_tile(a, split, bi, bj);
+  // the division runs on the vector unit: results back to scalar registers
+  const bool part = a.splits > 1 && (int)blockIdx.x >= a.whole;
+  int split = 0, tile, bi, bj;
+  if (!part) {
+    tile = linear8_deal(blockIdx.x, a.splits > 1 ? a.whole : a.tilesM * a.tilesN, 8 * a.tilesN);
+  } else {
+    const int rem = a.tilesM * a.tilesN - a.whole;
+    const int w = linear8_deal(blockIdx.x - a.whole, rem * a.splits, 8 * a.tilesN);
+    split = w / rem;
+    tile = a.whole + w % rem;
+  }
+  split = __builtin_amdgcn_readfirstlane(split);
+  tile = __builtin_amdgcn_readfirstlane(tile);
+  linear8_tile(a, tile, bi, bj);
+  bi = __builtin_amdgcn_readfirstlane(bi);
+  bj = __builtin_amdgcn_readfirstlane(bj);
   const int row0 = bi * T, col0 = bj * T;
 
   // stages of this split: K-stages [ks0, ks1), walked once per piece of dy
   const int nks = (a.K + BK - 1) / BK;
-  const int ks0 = min(split * a.per_split, nks), ks1 = min(ks0 + a.per_split, nks);
+  const int per = part ? a.per_split : nks;
+  const int ks0 = min(split * per, nks), ks1 = min(ks0 + per, nks);
   const int nst = (ks1 - ks0) * a.planes;
 
   auto swz_t = [](int krow) { return ((krow & 1) << 2) ^ (((krow >> 1) & 1) * 10); };
@@ -400,8 +417,8 @@ void linear8_kernel(const Linear8Args a) {
   const int dr0 = lane / CW, dc8 = (lane % CW) * 8;
   const int gj = col0 + wn * WN + dc8;
   float cs[8], cb[8];
-  if constexpr (INT && !PART) {
-    if (gj < a.N) {
+  if constexpr (INT) {
+    if (!part && gj < a.N) {
       piece_load(a.sb, gj, a.N, cs);
       if (a.bias) vec_load(a.bias, a.bias_dtype, gj, a.N, cb);
     }
@@ -413,10 +430,8 @@ void linear8_kernel(const Linear8Args a) {
     for (int j = 0; j < WTN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        float x;
-        if constexpr (INT && PART) x = __builtin_bit_cast(float, (int32_t)acc[i][j][e]);
-        else x = (float)acc[i][j][e];
-        strip[((e >> 2) * 8 + half * 4 + (e & 3)) * SROW + j * 32 + l32] = x;
+        const auto x = acc[i][j][e];
+        strip[((e >> 2) * 8 + half * 4 + (e & 3)) * SROW + j * 32 + l32] = __builtin_bit_cast(float, x);
       }
     wave_lds_sync();
 #pragma unroll
@@ -427,8 +442,8 @@ void linear8_kernel(const Linear8Args a) {
       const f32x4 hi = *reinterpret_cast<const f32x4*>(sp + 4);
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       if (r < a.M && gj < a.N) {
-        if constexpr (PART) {
-          float* o = a.ws + ((int64_t)split * a.M + r) * a.ldws + gj;
+        if (part) {
+          float* o = a.ws + linear8_part<T>(a, tile, split) + (r - row0) * T + (gj - col0);
           *as_global(reinterpret_cast<f32x4*>(o)) = lo;
           *as_global(reinterpret_cast<f32x4*>(o + 4)) = hi;
         } else {
@@ -436,7 +451,7 @@ void linear8_kernel(const Linear8Args a) {
           if constexpr (INT) {
             const float sr = as_global(a.sa)[r];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * sr * cs[e];
+            for (int e = 0; e < 8; ++e) v[e] = (float)__builtin_bit_cast(int32_t, v[e]) * sr * cs[e];
             if (a.bias) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] += cb[e];
@@ -456,16 +471,19 @@ void linear8_kernel(const Linear8Args a) {
 }
 
 // Adds the partial tiles of a split product in order and finishes it as the
-// epilogue above does.  8 columns per thread.
-template <bool INT, typename TO>
+// epilogue above does.  8 columns per thread, T * T / 2048 workgroups per tile.
+template <bool INT, int T, typename TO>
 __global__ __launch_bounds__(256) void linear8_join_kernel(const Linear8Args a) {
-  const int per_row = (a.N + 7) / 8;
-  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (p >= (int64_t)a.M * per_row) return;
-  const int64_t r = p / per_row;
-  const int c = (int)(p - r * per_row) * 8;
-  const float* w = a.ws + r * a.ldws + c;
-  const int64_t step = (int64_t)a.M * a.ldws;
+  constexpr int WGS = T * T / 2048;
+  const int tile = a.whole + (int)(blockIdx.x / WGS);
+  const int in = (int)(blockIdx.x % WGS) * 2048 + threadIdx.x * 8;  // first value within the tile
+  int bi, bj;
+  linear8_tile(a, tile, bi, bj);
+  const int64_t r = (int64_t)bi * T + in / T;
+  const int c = bj * T + in % T;
+  if (r >= a.M || c >= a.N) return;
+  const float* w = a.ws + linear8_part<T>(a, tile, 0) + in;
+  const int64_t step = (int64_t)(a.tilesM * a.tilesN - a.whole) * (T * T);
   float v[8];
   if constexpr (INT) {
     int32_t s[8] = {};

@@ -8,19 +8,15 @@ namespace muon {
 
 template <int MODE, int BSRC, int T> hipError_t linear8_go(int odt, const Linear8Args& a, hipStream_t s) {
   constexpr int NW = T / 32;
-  const dim3 g((unsigned)(a.tilesM * a.tilesN * a.splits)), b(64 * NW);
-  if (a.splits > 1) {
-    hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, float, true>), g, b, 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int64_t pieces = (int64_t)a.M * ((a.N + 7) / 8);
-    const dim3 gj((unsigned)((pieces + 255) / 256));
-    if (odt == DT_BF16) hipLaunchKernelGGL((linear8_join_kernel<MODE == L8_Y, bf16>), gj, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((linear8_join_kernel<MODE == L8_Y, float>), gj, dim3(256), 0, s, a);
-    return hipGetLastError();
-  }
-  if (odt == DT_BF16) hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, bf16, false>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, float, false>), g, b, 0, s, a);
+  const int tiles = a.tilesM * a.tilesN, rem = a.splits > 1 ? tiles - a.whole : 0;
+  const dim3 g((unsigned)(tiles - rem + rem * a.splits)), b(64 * NW);
+  if (odt == DT_BF16) hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, bf16>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, float>), g, b, 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || rem == 0) return e;
+  const dim3 gj((unsigned)(rem * (T * T / 2048)));
+  if (odt == DT_BF16) hipLaunchKernelGGL((linear8_join_kernel<MODE == L8_Y, T, bf16>), gj, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((linear8_join_kernel<MODE == L8_Y, T, float>), gj, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -59,7 +59,8 @@ struct Linear8Plan {
   bool few;       // few tokens: no tiles
   bool expanded;  // gradients: the 8-bit operand as bf16 in the workspace first
   int tile, splits, per_split;
-  int64_t ldws, ldx, lddy;
+  int64_t whole;  // tiles that are not split
+  int64_t ldx, lddy;
   size_t dy_off, ws_off;  // workspace: expanded operand, planes of dy, partial results
   size_t bytes;
 };
@@ -76,22 +77,25 @@ struct Linear8Plan {
 //              bound by power at full load
 // and a constant per round of workgroups; a second launch and partial tiles for
 // a split; a launch and 3 bytes per element for the expansion.
+// z parts of the tiles that do not fill a round (the chip holds 256 workgroups of
+// 256 tiles, 512 of 128): 14336 x 4096 has 3.5 rounds of 256 tiles, and its last
+// half round takes as long as a whole one unless it is split.
 double linear8_cost(bool fwd, int tile, bool expanded, int64_t M, int64_t N, int64_t K, int64_t nks, int64_t z,
                     int planes) {
-  const int64_t wgs = ((M + tile - 1) / tile) * ((N + tile - 1) / tile) * z;
-  const double stages = (double)((nks + z - 1) / z) * planes;
-  double us;
-  if (tile == 128) {
-    const double once = fwd ? 6.1 : 4.9;
-    const double alone = stages * (fwd ? 0.55 : 0.86) + once, pair = stages * (fwd ? 0.96 : 1.19) + once;
-    const int64_t rem = wgs % 512;
-    us = (double)(wgs / 512) * pair + (rem == 0 ? 0.0 : rem <= 256 ? alone : pair);
-  } else {
-    const double low = fwd ? 0.69 : 0.84, fill = std::min(1.0, (double)wgs / 256.0);
-    const double stage = (fwd ? 1.44 : expanded ? 1.32 : 1.71) * (low + (1.0 - low) * fill);
-    us = (double)((wgs + 255) / 256) * (stages * stage + (fwd ? 9.3 : 7.6));
-  }
-  if (z > 1) us += (fwd ? 3.3 : 5.9) + 8.0 * (double)z * (double)M * (double)N / (fwd ? 7.7e6 : 9.0e6);
+  const int64_t slots = tile == 128 ? 512 : 256;
+  const int64_t tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
+  const int64_t rounds = tiles / slots, rem = tiles % slots;
+  auto round = [&](int64_t wgs, double stages) {
+    if (tile == 128)
+      return stages * (wgs <= 256 ? (fwd ? 0.55 : 0.86) : (fwd ? 0.96 : 1.19)) + (fwd ? 6.1 : 4.9);
+    const double low = fwd ? 0.69 : 0.84, fill = (double)std::min<int64_t>(wgs, 256) / 256.0;
+    return stages * (fwd ? 1.44 : expanded ? 1.32 : 1.71) * (low + (1.0 - low) * fill) + (fwd ? 9.3 : 7.6);
+  };
+  const double all = (double)nks * planes, part = (double)((nks + z - 1) / z) * planes;
+  double us = (double)rounds * round(slots, all);
+  for (int64_t left = rem * z; left > 0; left -= slots) us += round(std::min(left, slots), part);
+  if (z > 1 && rem > 0)
+    us += (fwd ? 3.3 : 5.9) + 8.0 * (double)z * (double)rem * (double)(tile * tile) / (fwd ? 7.7e6 : 9.0e6);
   if (expanded) us += 3.3 + 3.0 * (double)K * (double)N / 5.3e6;
   return us;
 }
@@ -114,7 +118,7 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
     p.tile = 128;
     p.splits = 1;
     p.per_split = (int)nks;
-    p.ldws = 0;
+    p.whole = 0;
     p.bytes = 0;
     return p;
   }
@@ -136,7 +140,10 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
   }
   p.per_split = (int)std::max<int64_t>(1, (nks + z - 1) / z);
   p.splits = (int)std::max<int64_t>(1, (nks + p.per_split - 1) / p.per_split);
-  p.ldws = (N + 7) / 8 * 8;
+  const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + p.tile - 1) / p.tile);
+  const int64_t rem = tiles % (p.tile == 128 ? 512 : 256);
+  if (rem == 0) p.splits = 1;
+  p.whole = tiles - rem;
   if (p.expanded) {
     p.ldx = (N + 63) / 64 * 64;
     p.dy_off = (size_t)K * (size_t)p.ldx * 2;
@@ -146,7 +153,7 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
     p.lddy = (out + 63) / 64 * 64;
     p.ws_off += (size_t)planes * (size_t)tokens * (size_t)p.lddy * 2;
   }
-  p.bytes = p.ws_off + (p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)p.ldws * sizeof(float) : 0);
+  p.bytes = p.ws_off + (p.splits > 1 ? (size_t)p.splits * (size_t)rem * (size_t)(p.tile * p.tile) * sizeof(float) : 0);
   if (p.bytes) p.bytes += WS_ALIGN;
   return p;
 }
@@ -154,11 +161,11 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
 // Fills the shared part of the arguments; false if the grid does not fit.
 bool linear8_args(const Linear8Plan& p, int64_t M, int64_t N, int64_t K, void* workspace, Linear8Args& a) {
   const int64_t tm = (M + p.tile - 1) / p.tile, tn = (N + p.tile - 1) / p.tile;
-  if (tm * tn * p.splits > 0x7fffffff) return false;
+  if (tm * tn > (1 << 24)) return false;  // tiles, their splits and join within 32 bits
   a.M = (int32_t)M; a.N = (int32_t)N; a.K = (int32_t)K;
   a.tilesM = (int32_t)tm; a.tilesN = (int32_t)tn;
   a.splits = p.splits; a.per_split = p.per_split;
-  a.ldws = p.ldws;
+  a.whole = (int32_t)p.whole;
   a.ws = p.splits > 1 ? reinterpret_cast<float*>(ws_base(workspace) + p.ws_off) : nullptr;
   return true;
 }
