@@ -338,7 +338,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 extern "C" {
 
-int32_t muon_version(void) { return 200; }
+int32_t muon_version(void) { return 101; }
 
 muon_status muon_ns_coefficients(int32_t kind, int32_t steps, float* out, size_t cap) {
   if (!out || steps < 1 || steps > MAX_NS_STEPS) return MUON_E_ARG;
