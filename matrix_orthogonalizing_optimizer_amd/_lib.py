@@ -463,12 +463,24 @@ def muon_version() -> int:
 # ---------------------------------------------------------------------------
 # Operators around the step: norms, 8-bit rows, the linear layer on 8-bit rows
 
+_codes = {}  # torch dtype -> code, filled on first use
+
+
+def _dtype_code(name, t):
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: MUON_BF16, torch.float32: MUON_F32})
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
 def _matrix(name, t):
     """(rows, cols, ld, dtype code) of a 2-D tensor with unit column stride."""
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name}: expected a 2-D tensor, got {tuple(shape)}")
-    rows, cols = shape
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got {tuple(t.shape)}")
+    rows, cols = t.shape
     ld, unit = t.stride()
     if unit != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name}: columns must be contiguous")
@@ -476,131 +488,109 @@ def _matrix(name, t):
         ld = cols
     elif ld < cols:
         raise ValueError(f"{name}: rows overlap (stride {ld} for {cols} columns)")
-    return rows, cols, ld, _dtype_code(name, t)
-
-
-def _dtype_code(name, t):
-    code = _torch_codes().get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name}: must be float32 or bfloat16, got {t.dtype}")
-    return code
-
-
-_codes = {}
-
-
-def _torch_codes():
-    if not _codes:
-        import torch
-        _codes.update({torch.bfloat16: MUON_BF16, torch.float32: MUON_F32})
-    return _codes
+    return rows, cols, ld, _codes.get(t.dtype) if t.dtype in _codes else _dtype_code(name, t)
 
 
 def _rows8(name, q, scale, shape=None):
-    """(rows, cols, ldq) of 8-bit rows and their scales: int8, rows a multiple
-    of 16 bytes apart, every row's bytes up to the next one in the storage."""
+    """(rows, cols, ldq, address) of 8-bit rows, their scales checked: int8,
+    rows a multiple of 16 bytes apart, every row's bytes up to the next one in
+    the storage."""
     import torch
-    got = q.shape
-    if q.dtype != torch.int8 or len(got) != 2:
-        raise ValueError(f"{name}: expected a 2-D int8 tensor, got {q.dtype} {tuple(got)}")
-    rows, cols = got
+    if q.dtype != torch.int8 or q.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D int8 tensor, got {q.dtype} {tuple(q.shape)}")
+    rows, cols = q.shape
     if shape is not None and (rows, cols) != shape:
         raise ValueError(f"{name}: expected {shape}, got {(rows, cols)}")
     ld, unit = q.stride()
     if unit != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name}: columns must be contiguous")
-    if rows == 0 or cols == 0:
+    ptr = q.data_ptr()
+    if rows <= 1 or cols == 0:
         ld = (cols + 15) // 16 * 16
-    else:
-        if rows == 1:
-            ld = (cols + 15) // 16 * 16
-        if ld % 16 or ld < cols or q.data_ptr() % 16:
+    if rows > 0 and cols > 0:
+        if ld % 16 or ld < cols or ptr % 16:
             raise ValueError(f"{name}: rows must start 16-byte aligned and lie a multiple of 16 bytes apart")
-        if q.untyped_storage().nbytes() - q.storage_offset() < rows * ld:
+        if ld != cols and q.untyped_storage().nbytes() - q.storage_offset() < rows * ld:
             raise ValueError(f"{name}: the storage ends before the last row's {ld} bytes")
-    if scale.shape != got[:1] or scale.dtype != torch.float32 or (rows > 1 and scale.stride(0) != 1):
+    if scale.dtype != torch.float32 or scale.numel() != rows or not scale.is_contiguous() or scale.dim() != 1:
         _vector(f"scale of {name}", scale, rows, torch.float32)
-    return rows, cols, ld
+    return rows, cols, ld, ptr
 
 
 def _vector(name, t, n, dtype=None):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
 
 
-def _call_device(stream, **tensors):
+def _call_device(stream, names, *tensors):
     """Every tensor of a call lives on the GPU its kernels run on; returns
-    that GPU's index."""
+    that GPU's index.  names: the tensors' names, for the errors."""
     di = None
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is None:
             continue
         d = t.get_device()
         if d != di:
             if not t.is_cuda:
-                raise ValueError(f"{name}: a {t.device} tensor; the library needs device memory")
+                raise ValueError(f"{names.split()[i]}: a {t.device} tensor; the library needs device memory")
             if di is None:
                 di = _device_index(stream)
             if d != di:
-                raise ValueError(f"{name}: on {t.device}, the kernels run on cuda:{di}")
+                raise ValueError(f"{names.split()[i]}: on {t.device}, the kernels run on cuda:{di}")
     return di
 
 
-class _On:
-    """Allocates and launches on the call's GPU and stream: a buffer made
-    here belongs to the stream that uses it, so the allocator does not hand
-    it on while the call's kernels still run."""
-
-    __slots__ = ("di", "stream")
-
-    def __init__(self, di, stream):
-        self.di, self.stream = di, stream
-
-    def empty(self, *shape, dtype):
-        import torch
-        dev = torch.device("cuda", self.di)
-        if self.stream is None:
-            return torch.empty(*shape, dtype=dtype, device=dev)
-        s = self.stream
-        if isinstance(s, int):
-            s = torch.cuda.ExternalStream(s, device=dev) if s else torch.cuda.default_stream(dev)
-        with torch.cuda.stream(s):
-            return torch.empty(*shape, dtype=dtype, device=dev)
-
-    def rows8(self, rows, cols):
-        import torch
-        return (self.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8)[:, :cols],
-                self.empty(rows, dtype=torch.float32))
-
-    def call(self, fn, *args):
-        f = getattr(lib(), fn)
-        if self.stream is None:  # the current stream of the current device (_call_device)
-            st = f(*args, _current_stream(self.di))
-        else:
-            import torch
-            with torch.cuda.device(self.di):
-                st = f(*args, _stream(self.stream))
-        _check(fn, st)
-
-
-def _current_stream(di):
-    """Handle of the current stream; torch's direct query where this torch has
-    it (0.1 us: building a Stream object for its handle takes 2.8 us)."""
+def _empty(di, stream, *shape, dtype):
+    """A buffer that belongs to the stream that uses it, so the allocator does
+    not hand it on while the call's kernels still run."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(di) if raw is not None else torch.cuda.current_stream(di).cuda_stream
+    dev = torch.device("cuda", di)
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=dev)
 
 
-def _scratch(on, workspace, nbytes):
+def _empty_rows8(di, stream, rows, cols):
+    import torch
+    return (_empty(di, stream, rows, (cols + 15) // 16 * 16, dtype=torch.int8)[:, :cols],
+            _empty(di, stream, rows, dtype=torch.float32))
+
+
+def _scratch(di, stream, workspace, nbytes):
     """(tensor kept alive, pointer, bytes) of a call's workspace."""
     import torch
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = on.empty(nbytes, dtype=torch.uint8)
+        workspace = _empty(di, stream, nbytes, dtype=torch.uint8)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+_raw_stream = None  # torch's query of a device's current stream handle
+
+
+def _launch(fn, di, stream, *args):
+    global _raw_stream
+    f = getattr(_lib or lib(), fn)
+    if stream is None:  # the current stream of the current device (_call_device)
+        if _raw_stream is None:
+            # torch's direct query where this torch has it (0.1 us; building a
+            # Stream object for its handle takes 2.8 us)
+            import torch
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda d: torch.cuda.current_stream(d).cuda_stream)
+        st = f(*args, _raw_stream(di))
+    else:
+        import torch
+        with torch.cuda.device(di):
+            st = f(*args, _stream(stream))
+    if st != MUON_OK:
+        raise MuonError(fn, st)
 
 
 def muon_rows8_quantize(x, q=None, scale=None, stream=None):
@@ -610,11 +600,11 @@ def muon_rows8_quantize(x, q=None, scale=None, stream=None):
     rows, cols, ldx, dt = _matrix("x", x)
     if (q is None) != (scale is None):
         raise ValueError("q and scale: give both or neither")
-    on = _On(_call_device(stream, x=x, q=q, scale=scale), stream)
+    di = _call_device(stream, "x q scale", x, q, scale)
     if q is None:
-        q, scale = on.rows8(rows, cols)
-    _, _, ldq = _rows8("q", q, scale, (rows, cols))
-    on.call("muon_rows8_quantize", x.data_ptr(), rows, cols, ldx, dt, q.data_ptr(), ldq, scale.data_ptr())
+        q, scale = _empty_rows8(di, stream, rows, cols)
+    _, _, ldq, qp = _rows8("q", q, scale, (rows, cols))
+    _launch("muon_rows8_quantize", di, stream, x.data_ptr(), rows, cols, ldx, dt, qp, ldq, scale.data_ptr())
     return q, scale
 
 
@@ -622,14 +612,14 @@ def muon_rows8_dequantize(q, scale, out=None, dtype=None, stream=None):
     """The matrix that 8-bit rows stand for, q * scale per row, as ``out``
     (2-D, fp32 or bf16) or a new tensor of ``dtype`` (default bfloat16)."""
     import torch
-    rows, cols, ldq = _rows8("q", q, scale)
-    on = _On(_call_device(stream, q=q, scale=scale, out=out), stream)
+    rows, cols, ldq, qp = _rows8("q", q, scale)
+    di = _call_device(stream, "q scale out", q, scale, out)
     if out is None:
-        out = on.empty(rows, cols, dtype=dtype or torch.bfloat16)
+        out = _empty(di, stream, rows, cols, dtype=dtype or torch.bfloat16)
     r, c, ldy, dt = _matrix("out", out)
     if (r, c) != (rows, cols):
         raise ValueError(f"out: expected {(rows, cols)}, got {(r, c)}")
-    on.call("muon_rows8_dequantize", q.data_ptr(), ldq, scale.data_ptr(), rows, cols, out.data_ptr(), ldy, dt)
+    _launch("muon_rows8_dequantize", di, stream, qp, ldq, scale.data_ptr(), rows, cols, out.data_ptr(), ldy, dt)
     return out
 
 
@@ -646,6 +636,7 @@ def muon_norm_forward(x, gamma, beta=None, eps=1e-5, kind=MUON_NORM_LAYER, y=Non
     if beta is not None:
         _vector("beta", beta, cols, gamma.dtype)
     ldy = ldq = 0
+    qp = None
     if y is not None:
         r, c, ldy, ydt = _matrix("y", y)
         if (r, c) != (rows, cols) or ydt != dt:
@@ -653,13 +644,13 @@ def muon_norm_forward(x, gamma, beta=None, eps=1e-5, kind=MUON_NORM_LAYER, y=Non
     if (q is None) != (scale is None):
         raise ValueError("q and scale: give both or neither")
     if q is not None:
-        _, _, ldq = _rows8("q", q, scale, (rows, cols))
+        _, _, ldq, qp = _rows8("q", q, scale, (rows, cols))
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t is not None:
             _vector(name, t, rows, torch.float32)
-    on = _On(_call_device(stream, x=x, gamma=gamma, beta=beta, y=y, q=q, scale=scale, mean=mean, rstd=rstd), stream)
-    on.call("muon_norm_forward", kind, x.data_ptr(), rows, cols, ldx, dt, gamma.data_ptr(), _ptr(beta), vdt, eps,
-            _ptr(y), ldy, _ptr(q), ldq, _ptr(scale), _ptr(mean), _ptr(rstd))
+    di = _call_device(stream, "x gamma beta y q scale mean rstd", x, gamma, beta, y, q, scale, mean, rstd)
+    _launch("muon_norm_forward", di, stream, kind, x.data_ptr(), rows, cols, ldx, dt, gamma.data_ptr(), _ptr(beta), vdt,
+            eps, _ptr(y), ldy, qp, ldq, _ptr(scale), _ptr(mean), _ptr(rstd))
 
 
 def muon_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -687,16 +678,18 @@ def muon_norm_backward(dy, x, gamma, mean, rstd, kind=MUON_NORM_LAYER, dx=None, 
     for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
         if t is not None:
             _vector(name, t, cols, gamma.dtype)
-    on = _On(_call_device(stream, dy=dy, x=x, gamma=gamma, mean=mean, rstd=rstd, dx=dx, dgamma=dgamma, dbeta=dbeta,
-                          workspace=workspace), stream)
+    di = _call_device(stream, "dy x gamma mean rstd dx dgamma dbeta workspace", dy, x, gamma, mean, rstd, dx, dgamma,
+                      dbeta, workspace)
     if dx is None:
-        dx = on.empty(rows, cols, dtype=dy.dtype)
+        dx = _empty(di, stream, rows, cols, dtype=dy.dtype)
     r, c, lddx, ddt = _matrix("dx", dx)
     if (r, c) != (rows, cols) or ddt != dt:
         raise ValueError(f"dx: expected {(rows, cols)} of {dy.dtype}, got {(r, c)} of {dx.dtype}")
-    nb = muon_norm_backward_workspace_bytes(rows, cols) if dgamma is not None or dbeta is not None else 0
-    workspace, wp, wsz = _scratch(on, workspace, nb)
-    on.call("muon_norm_backward", kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, dt, gamma.data_ptr(), vdt,
+    nb = 0
+    if workspace is None and (dgamma is not None or dbeta is not None):
+        nb = muon_norm_backward_workspace_bytes(rows, cols)
+    workspace, wp, wsz = _scratch(di, stream, workspace, nb)
+    _launch("muon_norm_backward", di, stream, kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, dt, gamma.data_ptr(), vdt,
             _ptr(mean), _ptr(rstd), dx.data_ptr(), lddx, _ptr(dgamma), _ptr(dbeta), 1 if accumulate else 0, wp, wsz)
     return dx
 
@@ -716,24 +709,26 @@ def muon_linear8_forward(q, scale, wq, wscale, bias=None, y=None, dtype=None, wo
     as (wq, wscale) per output channel.  y: tokens x out, fp32 or bf16 (None:
     allocated, of ``dtype``, default bfloat16); returned."""
     import torch
-    tokens, in_, ldq = _rows8("q", q, scale)
-    out, win, ldw = _rows8("wq", wq, wscale)
+    tokens, in_, ldq, qp = _rows8("q", q, scale)
+    out, win, ldw, wqp = _rows8("wq", wq, wscale)
     if win != in_:
         raise ValueError(f"wq: expected {in_} columns, got {win}")
     bdt = 0
     if bias is not None:
         _vector("bias", bias, out)
         bdt = _dtype_code("bias", bias)
-    on = _On(_call_device(stream, q=q, scale=scale, wq=wq, wscale=wscale, bias=bias, y=y, workspace=workspace), stream)
+    di = _call_device(stream, "q scale wq wscale bias y workspace", q, scale, wq, wscale, bias, y, workspace)
     if y is None:
-        y = on.empty(tokens, out, dtype=dtype or torch.bfloat16)
+        y = _empty(di, stream, tokens, out, dtype=dtype or torch.bfloat16)
     r, c, ldy, dt = _matrix("y", y)
     if (r, c) != (tokens, out):
         raise ValueError(f"y: expected {(tokens, out)}, got {(r, c)}")
-    nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_FORWARD, tokens, out, in_)
-    workspace, wp, wsz = _scratch(on, workspace, nb)
-    on.call("muon_linear8_forward", q.data_ptr(), ldq, scale.data_ptr(), wq.data_ptr(), ldw, wscale.data_ptr(),
-            _ptr(bias), bdt, tokens, out, in_, y.data_ptr(), ldy, dt, wp, wsz)
+    # up to 16 tokens the library needs none (and would refuse the call if it did)
+    nb = (0 if workspace is not None or tokens <= 16 else
+          muon_linear8_workspace_bytes(MUON_LINEAR8_FORWARD, tokens, out, in_))
+    workspace, wp, wsz = _scratch(di, stream, workspace, nb)
+    _launch("muon_linear8_forward", di, stream, qp, ldq, scale.data_ptr(), wqp, ldw, wscale.data_ptr(), _ptr(bias), bdt,
+            tokens, out, in_, y.data_ptr(), ldy, dt, wp, wsz)
     return y
 
 
@@ -742,20 +737,20 @@ def muon_linear8_weight_grad(dy, q, scale, dw=None, dtype=None, accumulate=False
     gradient muon_step reads.  dw: written, or added to with accumulate
     (None: allocated, of ``dtype``, default dy's); returned."""
     tokens, out, lddy, dydt = _matrix("dy", dy)
-    rows, in_, ldq = _rows8("q", q, scale)
+    rows, in_, ldq, qp = _rows8("q", q, scale)
     if rows != tokens:
         raise ValueError(f"q: {rows} rows for {tokens} tokens")
-    on = _On(_call_device(stream, dy=dy, q=q, scale=scale, dw=dw, workspace=workspace), stream)
+    di = _call_device(stream, "dy q scale dw workspace", dy, q, scale, dw, workspace)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
-        dw = on.empty(out, in_, dtype=dtype or dy.dtype)
+        dw = _empty(di, stream, out, in_, dtype=dtype or dy.dtype)
     r, c, lddw, dt = _matrix("dw", dw)
     if (r, c) != (out, in_):
         raise ValueError(f"dw: expected {(out, in_)}, got {(r, c)}")
     nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_WEIGHT_GRAD, tokens, out, in_, dy)
-    workspace, wp, wsz = _scratch(on, workspace, nb)
-    on.call("muon_linear8_weight_grad", dy.data_ptr(), lddy, dydt, q.data_ptr(), ldq, scale.data_ptr(), tokens, out,
+    workspace, wp, wsz = _scratch(di, stream, workspace, nb)
+    _launch("muon_linear8_weight_grad", di, stream, dy.data_ptr(), lddy, dydt, qp, ldq, scale.data_ptr(), tokens, out,
             in_, dw.data_ptr(), lddw, dt, 1 if accumulate else 0, wp, wsz)
     return dw
 
@@ -764,17 +759,17 @@ def muon_linear8_input_grad(dy, wq, wscale, dx=None, dtype=None, workspace=None,
     """dX = dy W (tokens x in) with W as 8-bit rows (wq, wscale).  dx: None:
     allocated, of ``dtype``, default dy's; returned."""
     tokens, out, lddy, dydt = _matrix("dy", dy)
-    rows, in_, ldw = _rows8("wq", wq, wscale)
+    rows, in_, ldw, wqp = _rows8("wq", wq, wscale)
     if rows != out:
         raise ValueError(f"wq: {rows} rows for {out} columns of dy")
-    on = _On(_call_device(stream, dy=dy, wq=wq, wscale=wscale, dx=dx, workspace=workspace), stream)
+    di = _call_device(stream, "dy wq wscale dx workspace", dy, wq, wscale, dx, workspace)
     if dx is None:
-        dx = on.empty(tokens, in_, dtype=dtype or dy.dtype)
+        dx = _empty(di, stream, tokens, in_, dtype=dtype or dy.dtype)
     r, c, lddx, dt = _matrix("dx", dx)
     if (r, c) != (tokens, in_):
         raise ValueError(f"dx: expected {(tokens, in_)}, got {(r, c)}")
     nb = 0 if workspace is not None else muon_linear8_workspace_bytes(MUON_LINEAR8_INPUT_GRAD, tokens, out, in_, dy)
-    workspace, wp, wsz = _scratch(on, workspace, nb)
-    on.call("muon_linear8_input_grad", dy.data_ptr(), lddy, dydt, wq.data_ptr(), ldw, wscale.data_ptr(), tokens, out,
+    workspace, wp, wsz = _scratch(di, stream, workspace, nb)
+    _launch("muon_linear8_input_grad", di, stream, dy.data_ptr(), lddy, dydt, wqp, ldw, wscale.data_ptr(), tokens, out,
             in_, dx.data_ptr(), lddx, dt, wp, wsz)
     return dx

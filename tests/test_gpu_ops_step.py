@@ -27,7 +27,7 @@ def test_training_step(tokens, width, out):
     x = rnd(tokens, width)
     W, gamma, beta = rnd(out, width, k=0.02), (1 + rnd(width, k=0.1)), rnd(width, k=0.1)
     # forward: the norm's output exists as 8-bit rows only; they are kept
-    q, s = mo._lib._On(0, None).rows8(tokens, width)
+    q, s = mo._lib._empty_rows8(0, None, tokens, width)
     mean, rstd = torch.empty(tokens, device=d), torch.empty(tokens, device=d)
     mo.muon_norm_forward(x, gamma, beta, EPS, q=q, scale=s, mean=mean, rstd=rstd)
     wq, ws = mo.muon_rows8_quantize(W)
