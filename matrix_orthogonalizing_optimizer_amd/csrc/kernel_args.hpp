@@ -125,7 +125,7 @@ struct PlanesArgs {
   const void* dy;
   void* o;
   int64_t ld, ldo, plane;
-  int64_t rows, per_row;  // per_row: pieces of 8 columns
+  int64_t rows;
   int32_t cols;
 };
 

@@ -81,13 +81,13 @@ __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
 }
 
 // dy (rows x cols, any alignment) -> PIECES planes of bf16, rows ldo apart (a
-// multiple of 8), zero up to a multiple of 8 columns; 8 columns per thread.
+// multiple of 8), zero up to a multiple of 8 columns; 8 columns per thread, 4
+// rows of 64 pieces per workgroup.
 template <typename T>
 __global__ __launch_bounds__(256) void linear8_planes_kernel(const PlanesArgs a) {
-  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (p >= a.rows * a.per_row) return;
-  const int64_t row = p / a.per_row;
-  const int c = (int)(p - row * a.per_row) * 8;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int c = (int)(blockIdx.y * 64 + (threadIdx.x & 63)) * 8;
+  if (row >= a.rows || c >= a.cols) return;
   RowRaw<T> x;
   x.load(static_cast<const T*>(a.dy) + row * a.ld, c, a.cols);
   bf16* o = static_cast<bf16*>(a.o) + row * a.ldo + c;

@@ -18,10 +18,9 @@ hipError_t launch_linear8_few(int odt, const Linear8Args& a, hipStream_t s) {
 }
 
 hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s) {
-  const int64_t blocks = (a.rows * a.per_row + 255) / 256;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (dt == DT_BF16) hipLaunchKernelGGL((linear8_planes_kernel<bf16>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((linear8_planes_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  const dim3 g((unsigned)((a.rows + 3) / 4), (unsigned)((a.cols + 511) / 512));
+  if (dt == DT_BF16) hipLaunchKernelGGL((linear8_planes_kernel<bf16>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((linear8_planes_kernel<float>), g, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -372,7 +372,7 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
     d.dy = dy; d.ld = lddy;
     d.o = ws_base(workspace) + p.dy_off; d.ldo = p.lddy;
     d.plane = tokens * p.lddy;
-    d.rows = tokens; d.cols = (int32_t)out; d.per_row = (out + 7) / 8;
+    d.rows = tokens; d.cols = (int32_t)out;
     a.A = d.o; a.lda = p.lddy;
     a.plane = d.plane;
   }
