@@ -4,9 +4,10 @@
 //   L8_DX  dX[t][k] = sum_n dy[t][n] (wscale[n] w[n][k])
 // Written below as C (M x N) = sum over K of A B.
 //
-// A workgroup owns a T x T tile of C (T = 256: 8 waves of 128 x 64 outputs,
-// two per SIMD; T = 128: 4 waves of 64 x 64) and walks K in stages of 128
-// bytes per row: 128 values of int8, or 64 of bf16.  Two stages live in LDS.
+// A workgroup of 8 waves owns a T x T tile of C (T = 256: 128 x 64 outputs per
+// wave, one workgroup per CU; T = 128: 64 x 32 per wave, two workgroups per CU; 4
+// waves of 64 x 64 read less LDS but were 10% slower with one workgroup on a CU
+// and no faster with two) and walks K in stages of 128 bytes per row: 128 values of int8, or 64 of bf16.  Two stages live in LDS.
 //
 // L8_Y: both operands row-major int8, copied global -> LDS without a register
 // round trip; v_mfma_i32_32x32x32_i8, sums exact in 32-bit integers.
@@ -130,7 +131,7 @@ template <int T> __device__ __forceinline__ int64_t linear8_part(const Linear8Ar
 }
 
 template <int MODE, int BSRC, int T, int NW, typename TO>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(T == 128 ? 2 : NW / 4, T == 128 ? 2 : NW / 4)))
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(T == 128 ? NW / 2 : NW / 4, T == 128 ? NW / 2 : NW / 4)))
 void linear8_kernel(const Linear8Args a) {
   constexpr bool INT = MODE == L8_Y;
   constexpr bool CVT = !INT && BSRC == B_Q8;  // the 8-bit operand is converted here
@@ -144,6 +145,7 @@ void linear8_kernel(const Linear8Args a) {
   constexpr int STG = 2 * OPS;
   constexpr int NQ = OPS / (64 * NW);      // 16-byte pieces of one operand a thread moves per stage
   constexpr int NDR = WTM + WTN, NPAIR = WTM * WTN;
+  constexpr int RPP = (NDR + NPAIR - 1) / NPAIR;  // fragment reads issued per MFMA
   constexpr int CR = T / 8;                // chunks per K-row of a K-major stage
   constexpr int RPC = 64 / CR;             // K-rows per wave-wide copy
   constexpr int RSTEP = 64 * NW / CR;      // rows between a thread's pieces of the 8-bit operand
@@ -314,7 +316,7 @@ void linear8_kernel(const Linear8Args a) {
         constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : WTN + i);
         constexpr int later_a = AKM ? (WTM - 1 - (at > WTN ? at - WTN : 0)) : 0;
         constexpr int later_b = at <= WTN ? WTN - at : 0;
-        constexpr int now = p < NDR ? p : NDR;  // reads issued so far in this step
+        constexpr int now = p * RPP < NDR ? p * RPP : NDR;  // reads issued so far in this step
         constexpr int now_a = AKM ? (now > 0 ? 1 : 0) + (now > WTN + 1 ? now - WTN - 1 : 0) : 0;
         constexpr int now_b = now <= 1 ? 0 : (now - 1 < WTN ? now - 1 : WTN);
         constexpr int n = 2 * (later_a + later_b + now_a + now_b);
@@ -369,7 +371,7 @@ void linear8_kernel(const Linear8Args a) {
           mfma_pair(p, s & 1);
           // the fragment reads of a step before its register writes: those wait
 #pragma unroll
-          for (int r = p; r < NDR; r += NPAIR) read_one(ro(r), v, s + 1, (s + 1) & 1);
+          for (int r = p * RPP; r < NDR && r < (p + 1) * RPP; ++r) read_one(ro(r), v, s + 1, (s + 1) & 1);
           if constexpr (CVT) {
             // 4 NQ pairs of B over the 3 NPAIR MFMAs, after a head start for the loads
             constexpr int SLOTS = 3 * NPAIR, HEAD = NPAIR >= 8 ? 6 : 2;
@@ -399,7 +401,7 @@ void linear8_kernel(const Linear8Args a) {
           else if constexpr (!CVT) copy_b(c - NQ, v + 2, ksn);
         }
 #pragma unroll
-        for (int r = p; r < NDR; r += NPAIR) read_one(ro(r), v + 1, 0, 0);
+        for (int r = p * RPP; r < NDR && r < (p + 1) * RPP; ++r) read_one(ro(r), v + 1, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
     }

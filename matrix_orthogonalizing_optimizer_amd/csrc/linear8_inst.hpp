@@ -7,7 +7,7 @@
 namespace muon {
 
 template <int MODE, int BSRC, int T> hipError_t linear8_go(int odt, const Linear8Args& a, hipStream_t s) {
-  constexpr int NW = T / 32;
+  constexpr int NW = 8;  // waves per workgroup, for both tiles (see linear8.hpp)
   const int tiles = a.tilesM * a.tilesN, rem = a.splits > 1 ? tiles - a.whole : 0;
   const dim3 g((unsigned)(tiles - rem + rem * a.splits)), b(64 * NW);
   if (odt == DT_BF16) hipLaunchKernelGGL((linear8_kernel<MODE, BSRC, T, NW, bf16>), g, b, 0, s, a);

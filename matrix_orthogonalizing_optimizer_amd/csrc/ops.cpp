@@ -69,8 +69,8 @@ struct Linear8Plan {
 // these kernels on one MI355X (21 shapes from 512 x 512 x 512 to 8192 x 4096 x
 // 14336, all three passes; 10% rms; the choice costs 3% against the best one
 // timed).  Per stage of K (128 bytes of a row):
-//   128 tiles  0.86 with one workgroup on a CU, 1.19 with two (forward 0.55,
-//              0.96): bound by issue and LDS, not by memory (a ring of four
+//   128 tiles  0.77 with one workgroup on a CU, 1.21 with two (forward 0.53,
+//              0.90): bound by issue and LDS, not by memory (a ring of four
 //              stages in LDS was no faster)
 //   256 tiles  1.71 converting the 8-bit operand, 1.32 on the expanded one (forward
 //              1.44) with all CUs at work, down to 0.84 (0.69) of it with few:
@@ -87,7 +87,7 @@ double linear8_cost(bool fwd, int tile, bool expanded, int64_t M, int64_t N, int
   const int64_t rounds = tiles / slots, rem = tiles % slots;
   auto round = [&](int64_t wgs, double stages) {
     if (tile == 128)
-      return stages * (wgs <= 256 ? (fwd ? 0.55 : 0.86) : (fwd ? 0.96 : 1.19)) + (fwd ? 6.1 : 4.9);
+      return stages * (wgs <= 256 ? (fwd ? 0.53 : 0.77) : (fwd ? 0.90 : 1.21)) + (fwd ? 5.0 : 4.7);
     const double low = fwd ? 0.69 : 0.84, fill = (double)std::min<int64_t>(wgs, 256) / 256.0;
     return stages * (fwd ? 1.44 : expanded ? 1.32 : 1.71) * (low + (1.0 - low) * fill) + (fwd ? 9.3 : 7.6);
   };
