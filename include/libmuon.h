@@ -396,8 +396,8 @@ muon_status muon_rows8_quantize(const void* x, int64_t rows, int64_t cols, int64
                                 int8_t* q, int64_t ldq, float* scale, void* stream);
 /* y[i][j] = q[i][j] * scale[i] (y may be bf16 or fp32; exact for the scales
  * muon_rows8_quantize writes, apart from bf16's range at its far ends).
- * Errors of both: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30,
- * a leading dimension below cols or above 2^40, ldq not a multiple of 16);
+ * Errors of both: MUON_E_DTYPE; MUON_E_SHAPE (a size negative, rows above
+ * 2^30, cols above 2^27, a leading dimension below cols or above 2^40, ldq not a multiple of 16);
  * MUON_E_ARG (a pointer null or not aligned: x and y to their element, q to
  * 16 bytes, scale to 4); MUON_E_HIP. */
 muon_status muon_rows8_dequantize(const int8_t* q, int64_t ldq, const float* scale, int64_t rows, int64_t cols,
@@ -455,7 +455,7 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
  * gradient is; with in == 0 y is the bias.
  * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, in above
  * 131071 for the forward product, a leading dimension below its column count
- * or above 2^21, ldq or ldw not a multiple of 16, a result of more than 2^24
+ * or above 2^21, ldq or ldw not a multiple of 16, a result of more than 2^22
  * 128 x 128 tiles); MUON_E_ARG (a pointer null
  * or misaligned: 8-bit rows to 16 bytes, others to their element);
  * MUON_E_WORKSPACE (workspace smaller than muon_linear8_workspace_bytes);

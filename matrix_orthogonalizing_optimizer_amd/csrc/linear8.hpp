@@ -83,24 +83,25 @@ __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
 
 // dy (rows x cols, any alignment) -> PIECES planes of bf16, rows ldo apart (a
 // multiple of 8), zero up to a multiple of 8 columns; 8 columns per thread, 4
-// rows of 64 pieces per workgroup.
+// rows of 64 pieces per workgroup at a time.
 template <typename T>
 __global__ __launch_bounds__(256) void linear8_planes_kernel(const PlanesArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int c = (int)(blockIdx.y * 64 + (threadIdx.x & 63)) * 8;
-  if (row >= a.rows || c >= a.cols) return;
-  RowRaw<T> x;
-  x.load(static_cast<const T*>(a.dy) + row * a.ld, c, a.cols);
-  bf16* o = static_cast<bf16*>(a.o) + row * a.ldo + c;
-  if constexpr (sizeof(T) == 2) {
-    *as_global(reinterpret_cast<u32x4*>(o)) = x.w[0];
-  } else {
+  if (c >= a.cols) return;
+  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * 4) {
+    RowRaw<T> x;
+    x.load(static_cast<const T*>(a.dy) + row * a.ld, c, a.cols);
+    bf16* o = static_cast<bf16*>(a.o) + row * a.ldo + c;
+    if constexpr (sizeof(T) == 2) {
+      *as_global(reinterpret_cast<u32x4*>(o)) = x.w[0];
+    } else {
 #pragma unroll
-    for (int pc = 0; pc < 3; ++pc) {
-      u32x4 w;
+      for (int pc = 0; pc < 3; ++pc) {
+        u32x4 w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = (bf16_piece(x.get(2 * j), pc) >> 16) | bf16_piece(x.get(2 * j + 1), pc);
-      *as_global(reinterpret_cast<u32x4*>(o + pc * a.plane)) = w;
+        for (int j = 0; j < 4; ++j) w[j] = (bf16_piece(x.get(2 * j), pc) >> 16) | bf16_piece(x.get(2 * j + 1), pc);
+        *as_global(reinterpret_cast<u32x4*>(o + pc * a.plane)) = w;
+      }
     }
   }
 }

@@ -18,7 +18,8 @@ hipError_t launch_linear8_few(int odt, const Linear8Args& a, hipStream_t s) {
 }
 
 hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)((a.rows + 3) / 4), (unsigned)((a.cols + 511) / 512));
+  const int64_t groups = (a.rows + 3) / 4;
+  const dim3 g((unsigned)(groups < (1 << 20) ? groups : (1 << 20)), (unsigned)((a.cols + 511) / 512));
   if (dt == DT_BF16) hipLaunchKernelGGL((linear8_planes_kernel<bf16>), g, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((linear8_planes_kernel<float>), g, dim3(256), 0, s, a);
   return hipGetLastError();

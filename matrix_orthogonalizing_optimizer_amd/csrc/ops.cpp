@@ -17,6 +17,7 @@ using namespace muon;
 namespace {
 
 constexpr int64_t MAX_SIDE = (int64_t)1 << 30;
+constexpr int64_t MAX_COLS = (int64_t)1 << 27;  // row operators: a launch per 64 columns stays within 2^32 threads
 constexpr int64_t MAX_LD = (int64_t)1 << 40;    // row operators: 64-bit offsets
 constexpr int64_t MAX_LD8 = (int64_t)1 << 21;   // linear layer: a tile's rows within 32-bit offsets
 constexpr int64_t MAX_IN = 131071;              // 128 * 128 * in stays below 2^31
@@ -24,6 +25,7 @@ constexpr int64_t MAX_IN = 131071;              // 128 * 128 * in stays below 2^
 bool dtype_ok(int32_t d) { return d == MUON_F32 || d == MUON_BF16; }
 size_t esize(int32_t d) { return d == MUON_F32 ? 4 : 2; }
 bool side_ok(int64_t v) { return v >= 0 && v <= MAX_SIDE; }
+bool cols_ok(int64_t v) { return v >= 0 && v <= MAX_COLS; }
 bool ld_ok(int64_t ld, int64_t cols, int64_t most) { return ld >= cols && ld <= most; }
 bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool at_or_null(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -161,7 +163,7 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
 // Fills the shared part of the arguments; false if the grid does not fit.
 bool linear8_args(const Linear8Plan& p, int64_t M, int64_t N, int64_t K, void* workspace, Linear8Args& a) {
   const int64_t tm = (M + p.tile - 1) / p.tile, tn = (N + p.tile - 1) / p.tile;
-  if (tm * tn > (1 << 24)) return false;  // tiles, their splits and join within 32 bits
+  if (tm * tn > (1 << 22)) return false;  // 512 threads each within 2^32
   a.M = (int32_t)M; a.N = (int32_t)N; a.K = (int32_t)K;
   a.tilesM = (int32_t)tm; a.tilesN = (int32_t)tn;
   a.splits = p.splits; a.per_split = p.per_split;
@@ -177,7 +179,7 @@ extern "C" {
 muon_status muon_rows8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t dtype, int8_t* q,
                                 int64_t ldq, float* scale, void* stream) {
   if (!dtype_ok(dtype)) return MUON_E_DTYPE;
-  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(ldx, cols, MAX_LD) || !ld_ok(ldq, cols, MAX_LD) || ldq % 16)
+  if (!side_ok(rows) || !cols_ok(cols) || !ld_ok(ldx, cols, MAX_LD) || !ld_ok(ldq, cols, MAX_LD) || ldq % 16)
     return MUON_E_SHAPE;
   if (rows == 0) return MUON_OK;
   if (!at(scale, 4) || (cols > 0 && (!at(x, esize(dtype)) || !at(q, 16)))) return MUON_E_ARG;
@@ -195,7 +197,7 @@ muon_status muon_rows8_quantize(const void* x, int64_t rows, int64_t cols, int64
 muon_status muon_rows8_dequantize(const int8_t* q, int64_t ldq, const float* scale, int64_t rows, int64_t cols,
                                   void* y, int64_t ldy, int32_t dtype, void* stream) {
   if (!dtype_ok(dtype)) return MUON_E_DTYPE;
-  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(ldy, cols, MAX_LD) || !ld_ok(ldq, cols, MAX_LD) || ldq % 16)
+  if (!side_ok(rows) || !cols_ok(cols) || !ld_ok(ldy, cols, MAX_LD) || !ld_ok(ldq, cols, MAX_LD) || ldq % 16)
     return MUON_E_SHAPE;
   if (rows == 0 || cols == 0) return MUON_OK;
   if (!at(scale, 4) || !at(q, 16) || !at(y, esize(dtype))) return MUON_E_ARG;
@@ -215,7 +217,7 @@ muon_status muon_norm_forward(int32_t kind, const void* x, int64_t rows, int64_t
                               int8_t* q, int64_t ldq, float* scale, float* mean, float* rstd, void* stream) {
   if (kind != MUON_NORM_LAYER && kind != MUON_NORM_RMS) return MUON_E_METHOD;
   if (!dtype_ok(dtype) || !dtype_ok(vec_dtype)) return MUON_E_DTYPE;
-  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(ldx, cols, MAX_LD) || (y && !ld_ok(ldy, cols, MAX_LD)) ||
+  if (!side_ok(rows) || !cols_ok(cols) || !ld_ok(ldx, cols, MAX_LD) || (y && !ld_ok(ldy, cols, MAX_LD)) ||
       (q && (!ld_ok(ldq, cols, MAX_LD) || ldq % 16)))
     return MUON_E_SHAPE;
   if (!std::isfinite(eps) || eps < 0.f) return MUON_E_ARG;
@@ -244,7 +246,7 @@ muon_status muon_norm_forward(int32_t kind, const void* x, int64_t rows, int64_t
 
 muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes) {
   if (!bytes) return MUON_E_ARG;
-  if (!side_ok(rows) || !side_ok(cols)) return MUON_E_SHAPE;
+  if (!side_ok(rows) || !cols_ok(cols)) return MUON_E_SHAPE;
   *bytes = norm_ws(rows, cols);
   return MUON_OK;
 }
@@ -255,7 +257,7 @@ muon_status muon_norm_backward(int32_t kind, const void* dy, int64_t lddy, const
                                int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
   if (kind != MUON_NORM_LAYER && kind != MUON_NORM_RMS) return MUON_E_METHOD;
   if (!dtype_ok(dtype) || !dtype_ok(vec_dtype)) return MUON_E_DTYPE;
-  if (!side_ok(rows) || !side_ok(cols) || !ld_ok(lddy, cols, MAX_LD) || !ld_ok(ldx, cols, MAX_LD) ||
+  if (!side_ok(rows) || !cols_ok(cols) || !ld_ok(lddy, cols, MAX_LD) || !ld_ok(ldx, cols, MAX_LD) ||
       !ld_ok(lddx, cols, MAX_LD))
     return MUON_E_SHAPE;
   const size_t es = esize(dtype), ve = esize(vec_dtype);

@@ -80,6 +80,10 @@ __device__ __forceinline__ void vec_load(const void* p, int dt, int c, int cols,
   else piece_load(static_cast<const bf16*>(p), c, cols, v);
 }
 
+// Workgroup number: grids of rows are two-dimensional, since a launch holds
+// fewer than 2^32 threads along x.
+__device__ __forceinline__ int64_t row_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Deterministic sums over a group of G threads (a part of a wave, or whole
 // waves): butterfly inside a wave, waves in order.  G > 64: all threads of the
 // workgroup take part and `red` is one of two alternating buffers, so one
@@ -182,8 +186,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_forward_kernel(const Ro
   constexpr int RPW = G < 256 ? 256 / G : 1;  // rows per workgroup
   __shared__ GroupRed<G, 1> red;
   const int t = threadIdx.x % G;
-  const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / G;
-  if (G < 256 && row >= a.rows) return;  // whole groups, and no barrier below when G < 256
+  const int64_t row = row_block() * RPW + threadIdx.x / G;
+  if (row >= a.rows) return;  // whole groups; no barrier below when G < 256
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   float v[NV][8];
 #pragma unroll
@@ -266,7 +270,8 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
   constexpr int G = 1024;
   __shared__ GroupRed<G, 1> red;
   const int t = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int64_t row = row_block();
+  if (row >= a.rows) return;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   float mean = 0.f, r = 1.f;
   if constexpr (KIND != ROW_COPY) {
@@ -351,7 +356,7 @@ template <typename T, int G, int NV>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void row_restore_kernel(const RestoreArgs a) {
   constexpr int RPW = G < 256 ? 256 / G : 1;
   const int t = threadIdx.x % G;
-  const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / G;
+  const int64_t row = row_block() * RPW + threadIdx.x / G;
   if (row >= a.rows) return;
   const int8_t* q = a.q + row * a.ldq;
   T* y = static_cast<T*>(a.y) + row * a.ldy;
@@ -517,7 +522,8 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
   constexpr int G = 1024;
   __shared__ GroupRed<G, 2> red;
   const int t = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int64_t row = row_block();
+  if (row >= a.rows) return;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
   T* dx = static_cast<T*>(a.dx) + row * a.lddx;

@@ -136,6 +136,22 @@ def test_rows8_past_32_bit_offsets():
     assert x[rows // 2].count_nonzero().item() == 0
 
 
+def test_rows8_more_rows_than_one_grid_dimension():
+    """2^24 rows of 256 threads are 2^32 threads: the last rows of a longer
+    matrix are reached all the same."""
+    d = dev()
+    rows, cols = (1 << 24) + 5, 1040
+    x = torch.zeros(rows, cols, dtype=BF, device=d)
+    ends = [0, (1 << 20) - 1, 1 << 20, (1 << 24) - 1, 1 << 24, rows - 1]
+    x[ends] = matrix(len(ends), cols, BF, 4)
+    q, s = mo.muon_rows8_quantize(x)
+    rq, rs = R.rows8(f64(x[ends]))
+    assert np.array_equal(q[ends].cpu().numpy(), rq) and np.array_equal(f64(s[ends]), rs)
+    x.zero_()
+    mo.muon_rows8_dequantize(q, s, out=x)
+    assert np.array_equal(f64(x[ends]), R.restore(rq, rs))
+
+
 # ------------------------------------------------------------------- norms
 
 # additions on the way of a term into a row sum: at most 24 of a thread (rows

@@ -112,7 +112,8 @@ LX = dict(dy=P, lddy=6, dy_dtype=1, wq=P, ldw=32, wscale=P, tokens=4, out=6, in_
 REFUSED = [
     ("muon_rows8_quantize", Q, E_DTYPE, [dict(dtype=2), dict(dtype=-1)]),
     ("muon_rows8_quantize", Q, E_SHAPE, [dict(rows=-1), dict(cols=-1), dict(ldx=19), dict(ldq=16), dict(ldq=24),
-                                         dict(rows=1 << 31), dict(cols=1 << 31), dict(ldx=1 << 41)]),
+                                         dict(rows=1 << 31), dict(cols=1 << 31, ldx=1 << 31, ldq=1 << 31),
+                                         dict(cols=(1 << 27) + 16, ldx=1 << 28, ldq=1 << 28), dict(ldx=1 << 41)]),
     ("muon_rows8_quantize", Q, E_ARG, [dict(x=None), dict(q=None), dict(scale=None), dict(x=P + 1), dict(q=P + 8),
                                        dict(scale=P + 2), dict(x=P + 2, dtype=0)]),
     ("muon_rows8_dequantize", D, E_DTYPE, [dict(dtype=7)]),
@@ -140,7 +141,9 @@ REFUSED = [
                                          dict(y=None), dict(q=P + 1), dict(wq=P + 8), dict(bias=P + 1)]),
     ("muon_linear8_weight_grad", LW, E_DTYPE, [dict(dy_dtype=2), dict(dw_dtype=2)]),
     ("muon_linear8_weight_grad", LW, E_SHAPE, [dict(tokens=-1), dict(out=-1), dict(in_=-1), dict(lddy=5),
-                                               dict(ldq=16), dict(ldq=33), dict(lddw=19)]),
+                                               dict(ldq=16), dict(ldq=33), dict(lddw=19),
+                                           dict(out=1 << 20, in_=1 << 20, lddy=1 << 20, ldq=1 << 20, lddw=1 << 20,
+                                                workspace_bytes=1 << 62)]),
     ("muon_linear8_weight_grad", LW, E_ARG, [dict(dy=None), dict(q=None), dict(scale=None), dict(dw=None),
                                              dict(dy=P + 1), dict(q=P + 2), dict(dw=P + 1)]),
     ("muon_linear8_input_grad", LX, E_DTYPE, [dict(dy_dtype=2), dict(dx_dtype=2)]),
