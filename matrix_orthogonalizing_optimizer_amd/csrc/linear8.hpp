@@ -23,8 +23,8 @@
 // Where many tile rows share the 8-bit operand it is turned into bf16 in the
 // workspace first (B_BF16; row_restore_kernel) and then copied to LDS like
 // dy: that takes 3 bytes of HBM traffic per element once, and saves every
-// workgroup the conversion and its register writes to LDS (1.8 -> 1.5 us per
-// 256 x 256 x 64 stage).  linear8_plan in ops.cpp chooses.
+// workgroup the conversion and its register writes to LDS (1.88 -> 1.62 us per
+// 256 x 256 x 64 stage of random data).  linear8_plan in ops.cpp chooses.
 // dy is copied to LDS directly as well, which takes bf16 rows in whole
 // 16-byte pieces.  Any other dy is laid out so in the workspace first
 // (linear8_planes_kernel): bf16 rows of odd widths or addresses as they are,
@@ -185,7 +185,8 @@ void linear8_kernel(const Linear8Args a) {
 
   // summation rows of K-stage ks.  The clamp compiles to a vector instruction:
   // back to a scalar register, or the buffer resources built from it count as
-  // divergent and each load runs in a waterfall loop (0.3 us of a stage)
+  // divergent and each load runs in a waterfall loop (0.2 us of a
+  // 1.06 us stage of a 128 tile)
   auto stage_rows = [&](int ks) { return __builtin_amdgcn_readfirstlane(max(0, min(BK, a.K - ks * BK))); };
   // ---- operand A (and B for L8_Y), row-major: rows of the tile
   const int rows_a = min(T, a.M - row0);
@@ -306,7 +307,7 @@ void linear8_kernel(const Linear8Args a) {
   // first to use: this step's later fragments and the next step's first p
   // ones (two instructions each; untransposed reads and register writes are
   // not counted, which only waits for more).  Waiting for all of them once
-  // per step cost 0.2 us of a 1.6 us stage.
+  // per step took 1.95 instead of 1.89 us for a stage of the weight gradient.
   auto wait_frag = [&](auto pc) {
     if constexpr (!INT) {
       constexpr int p = decltype(pc)::value;

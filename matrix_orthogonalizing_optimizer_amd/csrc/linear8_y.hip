@@ -5,16 +5,22 @@
 namespace muon {
 
 namespace {
-template <int T> hipError_t few(int odt, const Linear8Args& a, hipStream_t s) {
-  const dim3 g((unsigned)((a.N + 15) / 16));
-  if (odt == DT_BF16) hipLaunchKernelGGL((linear8_few_kernel<T, bf16>), g, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((linear8_few_kernel<T, float>), g, dim3(512), 0, s, a);
+template <int T, int CG> hipError_t few(int odt, const Linear8Args& a, hipStream_t s) {
+  const dim3 g((unsigned)((a.N + 16 * CG - 1) / (16 * CG)));
+  if (odt == DT_BF16) hipLaunchKernelGGL((linear8_few_kernel<T, CG, bf16>), g, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((linear8_few_kernel<T, CG, float>), g, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 }  // namespace
 
 hipError_t launch_linear8_few(int odt, const Linear8Args& a, hipStream_t s) {
-  return a.M <= 16 ? few<1>(odt, a, s) : a.M <= 32 ? few<2>(odt, a, s) : few<4>(odt, a, s);
+  if (a.M > 16) return a.M <= 32 ? few<2, 1>(odt, a, s) : few<4, 1>(odt, a, s);
+  // short rows leave 8 parts of K one or two steps each: 2 parts for 4 groups
+  // of channels, if the groups still fill the chip (us, 1 and 16 tokens:
+  // 50304 x 768 13.3 -> 11.0 and 15.2 -> 14.9, 16384 x 1024 6.1 -> 5.4 and 7.0
+  // -> 6.5, 50304 x 1024 14.7 -> 13.3 and 17.7 -> 18.7; but 8192 x 768 3.9 ->
+  // 4.3, 50304 x 2048 20.5 -> 24.2)
+  return a.K <= 1024 && a.N >= 16384 ? few<1, 4>(odt, a, s) : few<1, 1>(odt, a, s);
 }
 
 hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s) {

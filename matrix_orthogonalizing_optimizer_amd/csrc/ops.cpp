@@ -67,10 +67,10 @@ struct Linear8Plan {
   size_t bytes;
 };
 // Estimated time of a tiled product in us: what the choice between tiles,
-// splits and expansion rests on.  The constants are fitted to 1018 timings of
-// these kernels on one MI355X (21 shapes from 512 x 512 x 512 to 8192 x 4096 x
-// 14336, all three passes; 10% rms; the choice costs 3% against the best one
-// timed).  Per stage of K (128 bytes of a row):
+// splits and expansion rests on.  The constants come from a fit to 1018 timings
+// on one MI355X (21 shapes from 512 x 512 x 512 to 8192 x 4096 x 14336, all
+// three passes; 10% rms; the choice cost 3% against the best one timed); those
+// of the 128 tiles were lowered by what going from 4 to 8 waves gained since.  Per stage of K (128 bytes of a row):
 //   128 tiles  0.77 with one workgroup on a CU, 1.21 with two (forward 0.53,
 //              0.90): bound by issue and LDS, not by memory (a ring of four
 //              stages in LDS was no faster)
@@ -109,10 +109,16 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
   const int64_t nks = (K + (pass == MUON_LINEAR8_FORWARD ? 128 : 64) - 1) / (pass == MUON_LINEAR8_FORWARD ? 128 : 64);
   Linear8Plan p;
   // Few tokens: up to 16 the kernel bound by the weights is ahead at every size
-  // measured (14336 x 4096, 16 tokens: 20.9 against 24 us in tiles), up to 64
-  // it is while the weights are few (4096 x 4096, 64 tokens: 14.9 against 15.9
-  // us; 14336 x 4096, 32 tokens: 29.8 against 24).
-  p.few = pass == MUON_LINEAR8_FORWARD && (tokens <= 16 || (tokens <= 64 && out * in <= ((int64_t)1 << 24)));
+  // measured (14336 x 4096, 16 tokens: 20.5 against 25 us in tiles).  Up to 64
+  // it is while the weights are few, there are not so many channels that all
+  // workgroups reading all tokens counts, and a workgroup's own share of them
+  // stays short.  Against the tiles, us: 4096 x 4096, 64 tokens 13.0 / 14.8, 2048
+  // x 8192, 32 tokens 13.9 / 14.2; beyond each bound 5120 x 5120, 32 tokens 20.5 /
+  // 16.3, 16384 x 1024, 32 tokens 9.3 / 8.8, 2048 x 8192, 64 tokens 21.5 / 16.4,
+  // 1024 x 14336, 64 tokens 34.3 / 17.6.
+  p.few = pass == MUON_LINEAR8_FORWARD &&
+          (tokens <= 16 || (tokens <= 64 && out <= 8192 && out * in <= ((int64_t)1 << 24) &&
+                            tokens * in <= ((int64_t)1 << 18)));
   p.expanded = false;
   p.ldx = p.lddy = 0;
   p.dy_off = p.ws_off = 0;

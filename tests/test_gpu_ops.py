@@ -304,10 +304,13 @@ SIZES = [(1, 1, 1), (1, 16, 16), (1, 4096, 4096), (2, 70, 33), (3, 17, 129), (5,
          (17, 64, 1024), (33, 65, 47), (64, 256, 2304), (65, 129, 255), (100, 100, 100), (128, 128, 128),
          (129, 257, 64), (200, 513, 1001), (256, 256, 256), (300, 768, 512), (511, 300, 250), (1000, 264, 520),
          (1027, 333, 77), (2000, 48, 1040), (4100, 96, 40)]
+# few tokens with short rows of many channels; between the ways for few tokens and for many
+FEW_SIZES = [(1, 16384, 64), (9, 16390, 1000), (16, 16387, 1024), (16, 16385, 1040), (32, 100, 8192), (33, 100, 8000),
+             (64, 40, 4112), (17, 8208, 50)]
 
 
 @pytest.mark.parametrize("dtype,bias", [(BF, BF), (F32, None), (BF, None), (F32, F32), (BF, F32)])
-@pytest.mark.parametrize("t,n,k", SIZES)
+@pytest.mark.parametrize("t,n,k", SIZES + FEW_SIZES)
 def test_linear8_forward(t, n, k, dtype, bias):
     print("linear8_forward", t, n, k, dtype, bias, flush=True)
     d = dev()
