@@ -65,6 +65,25 @@ template <typename T> __device__ __forceinline__ void piece_load(const T* row, i
     for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? to_f32(as_global(row)[c + e]) : 0.f;
   }
 }
+// The same for the rows of a matrix.  A guarded 16-bit load is widened and so
+// waited for behind its own branch, up to seven in a row.  In a piece that
+// starts inside the row, elements past its end load the row's last one again
+// instead and are cleared afterwards; a piece past the end (a row may have no
+// columns and no address at all) loads nothing.  bf16 rows of 4095, 4096 of
+// them: norm 22.9 -> 20.8 us, its backward pass 53 -> 45.
+template <typename T> __device__ __forceinline__ void row_piece_load(const T* row, int c, int cols, float (&v)[8]) {
+  if (sizeof(T) == 4 || c + 8 <= cols) {
+    piece_load(row, c, cols, v);
+  } else if (c < cols) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(as_global(row)[min(c + e, cols - 1)]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? v[e] : 0.f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  }
+}
 template <typename T> __device__ __forceinline__ void piece_store(T* row, int c, int cols, const float (&v)[8]) {
   if (c + 8 <= cols) {
     row_store8(row + c, v);
@@ -191,7 +210,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_forward_kernel(const Ro
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   float v[NV][8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) piece_load(x, (i * G + t) * ROW_VE, a.cols, v[i]);
+  for (int i = 0; i < NV; ++i) row_piece_load(x, (i * G + t) * ROW_VE, a.cols, v[i]);
   if constexpr (KIND != ROW_COPY) {
     float mean = 0.f;
     if constexpr (KIND == 0) {
@@ -279,7 +298,7 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
       float s[1] = {0.f};
       for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
         float v[8];
-        piece_load(x, (int)c, a.cols, v);
+        row_piece_load(x, (int)c, a.cols, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[0] += v[e];
       }
@@ -289,7 +308,7 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
     float s[1] = {0.f};
     for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
       float v[8];
-      piece_load(x, (int)c, a.cols, v);
+      row_piece_load(x, (int)c, a.cols, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = c + e < a.cols ? v[e] - mean : 0.f;
@@ -305,7 +324,7 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
     if (!a.y && !a.scale) return;
   }
   auto value = [&](int64_t c, float (&v)[8]) {
-    piece_load(x, (int)c, a.cols, v);
+    row_piece_load(x, (int)c, a.cols, v);
     if constexpr (KIND != ROW_COPY) {
       float w[8];
       vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
@@ -388,17 +407,22 @@ template <typename T> struct RowRaw {
         w[0] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c))->v);
         w[1] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c + 4))->v);
       }
+    } else if (sizeof(T) == 2 && c < cols) {
+      uint32_t x[8];  // as in row_piece_load
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = as_global(reinterpret_cast<const uint16_t*>(row))[min(c + e, cols - 1)];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = c + e < cols ? x[e] : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[0][j] = x[2 * j] | (x[2 * j + 1] << 16);
     } else {
 #pragma unroll
       for (int h = 0; h < (int)(sizeof(T) / 2); ++h) w[h] = u32x4{0u, 0u, 0u, 0u};
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < cols) {
-          if constexpr (sizeof(T) == 2)
-            w[0][e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(row))[c + e] << (16 * (e & 1));
-          else
-            w[e >> 2][e & 3] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
-        }
+        for (int e = 0; e < 8; ++e)
+          if (c + e < cols) w[e >> 2][e & 3] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
+      }
     }
   }
   __device__ __forceinline__ float get(int e) const {
@@ -532,8 +556,8 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
   float s[2] = {0.f, 0.f};
   for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
     float h[8], g[8], w[8];
-    piece_load(x, (int)c, a.cols, h);
-    piece_load(dy, (int)c, a.cols, g);
+    row_piece_load(x, (int)c, a.cols, h);
+    row_piece_load(dy, (int)c, a.cols, g);
     vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -546,8 +570,8 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
   const float c2 = s[0] / (float)a.cols, c1 = KIND == 0 ? s[1] / (float)a.cols : 0.f;
   for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
     float h[8], g[8], w[8];
-    piece_load(x, (int)c, a.cols, h);
-    piece_load(dy, (int)c, a.cols, g);
+    row_piece_load(x, (int)c, a.cols, h);
+    row_piece_load(dy, (int)c, a.cols, g);
     vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = r * (g[e] * w[e] - c1 - (h[e] - mean) * r * c2);
@@ -564,8 +588,8 @@ __global__ __launch_bounds__(256) void norm_columns_long_kernel(const NormBwdArg
 #pragma unroll 2
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     float g[8], x[8];
-    piece_load(static_cast<const T*>(a.dy) + row * a.lddy, (int)c, a.cols, g);
-    piece_load(static_cast<const T*>(a.x) + row * a.ldx, (int)c, a.cols, x);
+    row_piece_load(static_cast<const T*>(a.dy) + row * a.lddy, (int)c, a.cols, g);
+    row_piece_load(static_cast<const T*>(a.x) + row * a.ldx, (int)c, a.cols, x);
     const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f, r = as_global(a.rstd)[row];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
