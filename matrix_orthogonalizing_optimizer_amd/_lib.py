@@ -527,19 +527,33 @@ def _vector(name, t, n, dtype=None):
 def _call_device(stream, names, *tensors):
     """Every tensor of a call lives on the GPU its kernels run on; returns
     that GPU's index.  names: the tensors' names, for the errors."""
+    di = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != di:
+            break
+    else:
+        if di >= 0 and di == (_current_device() if stream is None else _device_index(stream)):
+            return di
     di = None
-    for i, t in enumerate(tensors):
+    for name, t in zip(names.split(), tensors):
         if t is None:
             continue
-        d = t.get_device()
-        if d != di:
-            if not t.is_cuda:
-                raise ValueError(f"{names.split()[i]}: a {t.device} tensor; the library needs device memory")
-            if di is None:
-                di = _device_index(stream)
-            if d != di:
-                raise ValueError(f"{names.split()[i]}: on {t.device}, the kernels run on cuda:{di}")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a {t.device} tensor; the library needs device memory")
+        if di is None:
+            di = _device_index(stream)
+        if t.get_device() != di:
+            raise ValueError(f"{name}: on {t.device}, the kernels run on cuda:{di}")
     return di
+
+
+def _current_device():
+    """torch.cuda.current_device() for a process that has device tensors:
+    torch's direct query (0.1 of 0.3 us) where this torch has it."""
+    global _current_device
+    import torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
 
 
 def _empty(di, stream, *shape, dtype):
@@ -557,8 +571,9 @@ def _empty(di, stream, *shape, dtype):
 
 def _empty_rows8(di, stream, rows, cols):
     import torch
-    return (_empty(di, stream, rows, (cols + 15) // 16 * 16, dtype=torch.int8)[:, :cols],
-            _empty(di, stream, rows, dtype=torch.float32))
+    ld = (cols + 15) // 16 * 16
+    q = _empty(di, stream, rows, ld, dtype=torch.int8)
+    return q if ld == cols else q[:, :cols], _empty(di, stream, rows, dtype=torch.float32)
 
 
 def _scratch(di, stream, workspace, nbytes):
