@@ -89,11 +89,12 @@ __global__ __launch_bounds__(256) void linear8_planes_kernel(const PlanesArgs a)
   const int c = (int)(blockIdx.y * 64 + (threadIdx.x & 63)) * 8;
   if (c >= a.cols) return;
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * 4) {
-    RowRaw<T> x;
+    RowRaw<T, true> x;
     x.load(static_cast<const T*>(a.dy) + row * a.ld, c, a.cols);
+    x.settle(c, a.cols);
     bf16* o = static_cast<bf16*>(a.o) + row * a.ldo + c;
     if constexpr (sizeof(T) == 2) {
-      *as_global(reinterpret_cast<u32x4*>(o)) = x.w[0];
+      *as_global(reinterpret_cast<u32x4*>(o)) = u32x4{x.w[0], x.w[1], x.w[2], x.w[3]};
     } else {
 #pragma unroll
       for (int pc = 0; pc < 3; ++pc) {

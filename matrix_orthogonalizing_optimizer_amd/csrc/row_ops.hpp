@@ -65,24 +65,84 @@ template <typename T> __device__ __forceinline__ void piece_load(const T* row, i
     for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? to_f32(as_global(row)[c + e]) : 0.f;
   }
 }
-// The same for the rows of a matrix.  A guarded 16-bit load is widened and so
-// waited for behind its own branch, up to seven in a row.  In a piece that
-// starts inside the row, elements past its end load the row's last one again
-// instead and are cleared afterwards; a piece past the end (a row may have no
-// columns and no address at all) loads nothing.  bf16 rows of 4095, 4096 of
-// them: norm 22.9 -> 20.8 us, its backward pass 53 -> 45.
-template <typename T> __device__ __forceinline__ void row_piece_load(const T* row, int c, int cols, float (&v)[8]) {
-  if (sizeof(T) == 4 || c + 8 <= cols) {
-    piece_load(row, c, cols, v);
-  } else if (c < cols) {
+
+// 8 elements of a row as they lie in memory, loaded and settled apart: what is
+// under way takes a 16-bit row half the registers of its fp32 values, and no
+// branch stands behind the load.  (A branch that clears the registers of the
+// lanes past the row's end waits for the loads of the others: 8192 x 2040
+// bf16, whose last wave is partly past the end, norm backward 38 against 28 us
+// of 8192 x 2048.)  A piece that reaches past the end loads the row's last 8
+// elements, and settle() moves its own to the front and clears the others.
+// SHORT: rows may have less than 8 elements, which are loaded one by one.
+template <typename T, bool SHORT> struct RowRaw {
+  static constexpr int PER = 4 / sizeof(T), NW = 8 / PER;  // elements per register, registers
+  uint32_t w[NW];
+  __device__ __forceinline__ void load(const T* row, int c, int cols) {
+    if (!SHORT || cols >= 8) {
+      const T* p = row + min(c, cols - 8);
+      if constexpr (sizeof(T) == 2) {
+        const u32x4 a = as_global(reinterpret_cast<const u32x4_e2*>(p))->v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = to_f32(as_global(row)[min(c + e, cols - 1)]);
+        for (int j = 0; j < 4; ++j) w[j] = a[j];
+      } else {
+        const f32x4 a = as_global(reinterpret_cast<const f32x4_e4*>(p))->v;
+        const f32x4 b = as_global(reinterpret_cast<const f32x4_e4*>(p + 4))->v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? v[e] : 0.f;
-  } else {
+        for (int j = 0; j < 4; ++j) {
+          w[j] = __builtin_bit_cast(uint32_t, (float)a[j]);
+          w[j + 4] = __builtin_bit_cast(uint32_t, (float)b[j]);
+        }
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      for (int j = 0; j < NW; ++j) w[j] = 0u;
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (c + e < cols) {
+          if constexpr (sizeof(T) == 2)
+            w[e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(row))[c + e] << (16 * (e & 1));
+          else
+            w[e] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
+        }
+    }
   }
+  __device__ __forceinline__ void settle(int c, int cols) {
+    if ((SHORT && cols < 8) || c + 8 <= cols) return;
+    const int off = min(c + 8 - cols, 8);  // elements to drop at the front
+    const int regs = off / PER;
+    // registers by powers of two, then half a register
+#pragma unroll
+    for (int b = NW; b >= 1; b >>= 1) {
+      const bool take = (regs & b) != 0;
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        const uint32_t from = j + b < NW ? w[j + b] : 0u;
+        w[j] = take ? from : w[j];
+      }
+    }
+    if constexpr (PER == 2) {
+      const bool take = (off & 1) != 0;
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        const uint32_t from = (w[j] >> 16) | (j + 1 < NW ? w[j + 1] << 16 : 0u);
+        w[j] = take ? from : w[j];
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 2)
+      return __builtin_bit_cast(float, (e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+    else
+      return __builtin_bit_cast(float, w[e]);
+  }
+};
+// A piece of a row of more than 8 elements, widened.
+template <typename T> __device__ __forceinline__ void row_piece_load(const T* row, int c, int cols, float (&v)[8]) {
+  RowRaw<T, false> x;
+  x.load(row, c, cols);
+  x.settle(c, cols);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = x.get(e);
 }
 template <typename T> __device__ __forceinline__ void piece_store(T* row, int c, int cols, const float (&v)[8]) {
   if (c + 8 <= cols) {
@@ -209,8 +269,15 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_forward_kernel(const Ro
   if (row >= a.rows) return;  // whole groups; no barrier below when G < 256
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   float v[NV][8];
+  RowRaw<T, G == 8> raw[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) row_piece_load(x, (i * G + t) * ROW_VE, a.cols, v[i]);
+  for (int i = 0; i < NV; ++i) raw[i].load(x, (i * G + t) * ROW_VE, a.cols);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    raw[i].settle((i * G + t) * ROW_VE, a.cols);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = raw[i].get(e);
+  }
   if constexpr (KIND != ROW_COPY) {
     float mean = 0.f;
     if constexpr (KIND == 0) {
@@ -395,44 +462,6 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_restore_kernel(const Re
   }
 }
 
-// 8 raw elements of T, so that a 16-bit row takes half the registers of its
-// fp32 values while the next row is on its way.
-template <typename T> struct RowRaw {
-  u32x4 w[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* row, int c, int cols) {
-    if (c + 8 <= cols) {
-      if constexpr (sizeof(T) == 2) {
-        w[0] = as_global(reinterpret_cast<const u32x4_e2*>(row + c))->v;
-      } else {
-        w[0] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c))->v);
-        w[1] = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(row + c + 4))->v);
-      }
-    } else if (sizeof(T) == 2 && c < cols) {
-      uint32_t x[8];  // as in row_piece_load
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = as_global(reinterpret_cast<const uint16_t*>(row))[min(c + e, cols - 1)];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = c + e < cols ? x[e] : 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[0][j] = x[2 * j] | (x[2 * j + 1] << 16);
-    } else {
-#pragma unroll
-      for (int h = 0; h < (int)(sizeof(T) / 2); ++h) w[h] = u32x4{0u, 0u, 0u, 0u};
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < cols) w[e >> 2][e & 3] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
-      }
-    }
-  }
-  __device__ __forceinline__ float get(int e) const {
-    if constexpr (sizeof(T) == 2)
-      return __builtin_bit_cast(float, (e & 1) ? (w[0][e >> 1] & 0xffff0000u) : (w[0][e >> 1] << 16));
-    else
-      return __builtin_bit_cast(f32x4, w[e >> 2])[e & 3];
-  }
-};
-
 // Norm backward: workgroups loop over rows; a thread keeps its columns' gamma
 // and its sums of dy h and dy in registers over all of them, and the sums go
 // to workspace once per workgroup (partials[2][workgroups][cols]).  The next
@@ -454,7 +483,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
   }
   const int64_t stride = (int64_t)gridDim.x * RPW;
   int64_t row = (int64_t)blockIdx.x * RPW + sub;
-  RowRaw<T> x[NV], dy[NV];
+  RowRaw<T, G == 8> x[NV], dy[NV];
   float r = 0.f, mean = 0.f;
   auto fetch = [&](int64_t at) {
     const T* xp = static_cast<const T*>(a.x) + at * a.ldx;
@@ -471,7 +500,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
   int buf = 0;
   while (row < a.rows) {
     const int64_t next = row + stride;
-    RowRaw<T> cx[NV], cd[NV];
+    RowRaw<T, G == 8> cx[NV], cd[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       cx[i] = x[i];
@@ -479,6 +508,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
     }
     const float cr = r, cm = mean;
     if (next < a.rows) fetch(next);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      cx[i].settle((i * G + t) * ROW_VE, a.cols);
+      cd[i].settle((i * G + t) * ROW_VE, a.cols);
+    }
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
