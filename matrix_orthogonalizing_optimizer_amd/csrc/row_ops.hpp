@@ -136,13 +136,24 @@ template <typename T, bool SHORT> struct RowRaw {
       return __builtin_bit_cast(float, w[e]);
   }
 };
-// A piece of a row of more than 8 elements, widened.
+// A piece of a row of at least 8 elements, widened.
 template <typename T> __device__ __forceinline__ void row_piece_load(const T* row, int c, int cols, float (&v)[8]) {
   RowRaw<T, false> x;
   x.load(row, c, cols);
   x.settle(c, cols);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = x.get(e);
+}
+// Piece of a vector whose dtype is known at run time only.
+template <bool SHORT = true>
+__device__ __forceinline__ void vec_load(const void* p, int dt, int c, int cols, float (&v)[8]) {
+  if constexpr (SHORT) {
+    if (dt == DT_F32) piece_load(static_cast<const float*>(p), c, cols, v);
+    else piece_load(static_cast<const bf16*>(p), c, cols, v);
+  } else {
+    if (dt == DT_F32) row_piece_load(static_cast<const float*>(p), c, cols, v);
+    else row_piece_load(static_cast<const bf16*>(p), c, cols, v);
+  }
 }
 template <typename T> __device__ __forceinline__ void piece_store(T* row, int c, int cols, const float (&v)[8]) {
   if (c + 8 <= cols) {
@@ -152,11 +163,6 @@ template <typename T> __device__ __forceinline__ void piece_store(T* row, int c,
     for (int e = 0; e < 8; ++e)
       if (c + e < cols) as_global(row)[c + e] = from_f32<T>(v[e]);
   }
-}
-// The same for a vector whose dtype is known at run time only.
-__device__ __forceinline__ void vec_load(const void* p, int dt, int c, int cols, float (&v)[8]) {
-  if (dt == DT_F32) piece_load(static_cast<const float*>(p), c, cols, v);
-  else piece_load(static_cast<const bf16*>(p), c, cols, v);
 }
 
 // Workgroup number: grids of rows are two-dimensional, since a launch holds
@@ -309,11 +315,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_forward_kernel(const Ro
     for (int i = 0; i < NV; ++i) {
       const int c = (i * G + t) * ROW_VE;
       float w[8];
-      vec_load(a.gamma, a.vec_dtype, c, a.cols, w);
+      vec_load<G == 8>(a.gamma, a.vec_dtype, c, a.cols, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * w[e];
       if (a.beta) {
-        vec_load(a.beta, a.vec_dtype, c, a.cols, w);
+        vec_load<G == 8>(a.beta, a.vec_dtype, c, a.cols, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] += w[e];
       }
@@ -394,11 +400,11 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
     row_piece_load(x, (int)c, a.cols, v);
     if constexpr (KIND != ROW_COPY) {
       float w[8];
-      vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
+      vec_load<false>(a.gamma, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * r * w[e];
       if (a.beta) {
-        vec_load(a.beta, a.vec_dtype, (int)c, a.cols, w);
+        vec_load<false>(a.beta, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += w[e];
       }
@@ -477,7 +483,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
   float gam[NV][8], sg[NV][8], sb[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    vec_load(a.gamma, a.vec_dtype, (i * G + t) * ROW_VE, a.cols, gam[i]);
+    vec_load<G == 8>(a.gamma, a.vec_dtype, (i * G + t) * ROW_VE, a.cols, gam[i]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.f;
   }
@@ -592,7 +598,7 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
     float h[8], g[8], w[8];
     row_piece_load(x, (int)c, a.cols, h);
     row_piece_load(dy, (int)c, a.cols, g);
-    vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
+    vec_load<false>(a.gamma, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float ge = g[e] * w[e];
@@ -606,7 +612,7 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
     float h[8], g[8], w[8];
     row_piece_load(x, (int)c, a.cols, h);
     row_piece_load(dy, (int)c, a.cols, g);
-    vec_load(a.gamma, a.vec_dtype, (int)c, a.cols, w);
+    vec_load<false>(a.gamma, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = r * (g[e] * w[e] - c1 - (h[e] - mean) * r * c2);
     piece_store(dx, (int)c, a.cols, g);
