@@ -40,13 +40,14 @@ muon_status done(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_E_HIP; 
 int norm_parts(int64_t rows, int64_t cols) {
   // rows a workgroup takes at a time
   const int64_t per = cols <= 64 ? 32 : cols <= 256 ? 8 : cols <= 512 ? 4 : cols <= 768 ? 8 : cols <= 1024 ? 4 : 1;
-  // 8 waves per CU, or 4 where a workgroup takes 8 rows or more at a time: more
-  // workgroups hide more of a row's latency, and each adds a partial row that
-  // is written and read (us, 256 against 512: 8192 x 768 16.1 and 16.8, 30000 x
-  // 64 11.0 and 11.5, but 16384 x 512 19.0 and 16.2, 16384 x 1024 25.5 and 24.5,
-  // 16384 x 4096 86 and 81; 8192 x 8192 82 and 87, with 8 waves each)
-  const int64_t most = cols > 4096 || per >= 8 ? 256 : 512;
-  return (int)std::min<int64_t>(most, std::max<int64_t>(1, (rows + per - 1) / per));
+  // More workgroups hide more of a row's latency, and each adds a partial row
+  // that is written and read.  512 only where each takes at least two rounds
+  // of rows, of at most 4 rows of at most 4096 columns (us, 256 against 512
+  // workgroups: 16384 x 512 19.0 and 16.2, 8192 x 2048 34 and 27; but 8192 x 768
+  // in rounds of 8 16.1 and 16.8, 8192 x 8192 81 and 88, 1000 x 4096 15.6 and
+  // 19.1, 3000 x 1024 11.1 and 12.1, 1500 x 2048 13.0 and 14.0).
+  const int64_t rounds = std::max<int64_t>(1, (rows + per - 1) / per);
+  return (int)std::min<int64_t>(cols > 4096 || per >= 8 || rounds <= 1024 ? 256 : 512, rounds);
 }
 size_t norm_ws(int64_t rows, int64_t cols) {
   if (rows == 0 || cols == 0) return 0;
