@@ -71,8 +71,8 @@ template <> struct Acc8<false> {
 // all in the first piece (a NaN keeps a mantissa bit).
 __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  if ((u & 0x7f800000u) == 0x7f800000u) return p ? 0u : (u | ((u & 0x7fffffu) ? 0x400000u : 0u));
   uint32_t hi = u & 0xffff0000u;
+  if ((u & 0x7f800000u) == 0x7f800000u) return p ? 0u : (hi | ((u & 0x7fffffu) ? 0x400000u : 0u));
   if (p == 0) return hi;
   float r = x - __builtin_bit_cast(float, hi);
   hi = __builtin_bit_cast(uint32_t, r) & 0xffff0000u;

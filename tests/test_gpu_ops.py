@@ -454,6 +454,40 @@ def test_linear8_neighbours_of_dy_do_not_leak():
             assert torch.equal(dx, mo.muon_linear8_input_grad(c, wq, ws))
 
 
+@pytest.mark.parametrize("t,n,k", [(70, 37, 50), (130, 300, 129), (300, 2100, 2300), (2100, 300, 2300)])
+def test_linear8_fp32_dy_with_infinities(t, n, k):
+    """fp32 dy in three pieces, cut in the product or laid out first: numbers of
+    all sizes count fully; an infinity or a NaN (its payload in the low bits
+    only) spoils its own row and column and nothing else."""
+    d = dev()
+    q, s = rows8(t, k, 1)
+    wq, ws = rows8(n, k, 2)
+    dy = matrix(t, n, F32, 3)
+    dy[:, 2] *= 2.0 ** -60
+    dy[5] *= 2.0 ** 40
+    for name, pass_, args in (("dW", mo.muon_linear8_weight_grad, (q, s)),
+                              ("dX", mo.muon_linear8_input_grad, (wq, ws))):
+        left = f64(dy).T if name == "dW" else f64(dy)
+        right = R.restore(args[0].cpu().numpy(), f64(args[1]))
+        ref, terms = left @ right, np.abs(left) @ np.abs(right)
+        # a sum of three pieces of each value, as in grad_bounds
+        check(pass_(dy, *args, dtype=F32), ref, 2 * (3 * left.shape[1] + 16) * U * terms, name)
+    dy[5] *= 2.0 ** -40
+    bad = dy.clone()
+    bad[3, 4] = math.inf
+    bad.view(torch.int32)[6, 7] = 0x7f800001  # NaN
+    bad[t - 1, n - 1] = -math.inf
+    dw = mo.muon_linear8_weight_grad(bad, q, s)
+    dx = mo.muon_linear8_input_grad(bad, wq, ws)
+    cols, rows = [4, 7, n - 1], [3, 6, t - 1]
+    assert not torch.isfinite(dw[cols]).any() and not torch.isfinite(dx[rows]).any()
+    assert torch.isnan(dw[7]).all() and torch.isnan(dx[6]).all()
+    ok = [i for i in range(n) if i not in cols]
+    assert torch.equal(dw[ok], mo.muon_linear8_weight_grad(dy, q, s)[ok])
+    ok = [i for i in range(t) if i not in rows]
+    assert torch.equal(dx[ok], mo.muon_linear8_input_grad(dy, wq, ws)[ok])
+
+
 def test_linear8_past_32_bit_offsets():
     """Kept rows and gradients of more than 2^31 bytes; only the last rows
     are not zero, so a wrong offset shows."""
