@@ -39,7 +39,7 @@ hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s);
 hipError_t launch_linear8_forward(int tile, int odt, const Linear8Args& a, hipStream_t s);
 hipError_t launch_linear8_few(int odt, const Linear8Args& a, hipStream_t s);  // at most 64 tokens
 hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s);
-hipError_t launch_linear8_dw(int tile, bool expanded, int odt, const Linear8Args& a, hipStream_t s);
-hipError_t launch_linear8_dx(int tile, bool expanded, int odt, const Linear8Args& a, hipStream_t s);
+hipError_t launch_linear8_dw(int tile, bool expanded, bool dy_f32, int odt, const Linear8Args& a, hipStream_t s);
+hipError_t launch_linear8_dx(int tile, bool expanded, bool dy_f32, int odt, const Linear8Args& a, hipStream_t s);
 
 }  // namespace muon

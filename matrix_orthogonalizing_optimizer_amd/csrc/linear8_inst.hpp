@@ -20,7 +20,9 @@ template <int MODE, int BSRC, int T> hipError_t linear8_go(int odt, const Linear
   return hipGetLastError();
 }
 
-template <int MODE> hipError_t linear8_grad_any(int tile, bool expanded, int odt, const Linear8Args& a, hipStream_t s) {
+template <int MODE>
+hipError_t linear8_grad_any(int tile, bool expanded, bool dy_f32, int odt, const Linear8Args& a, hipStream_t s) {
+  if (dy_f32) return linear8_go<MODE, B_Q8_A_F32, 128>(odt, a, s);
   if (tile == 128) return linear8_go<MODE, B_Q8, 128>(odt, a, s);
   return expanded ? linear8_go<MODE, B_BF16, 256>(odt, a, s) : linear8_go<MODE, B_Q8, 256>(odt, a, s);
 }

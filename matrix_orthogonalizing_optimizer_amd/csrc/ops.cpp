@@ -65,6 +65,7 @@ int dy_planes(const void* dy, int64_t lddy, int64_t out, int32_t dtype) {
 struct Linear8Plan {
   bool few;       // few tokens: no tiles
   bool expanded;  // gradients: the 8-bit operand as bf16 in the workspace first
+  bool dy_f32;    // gradients: the product itself cuts fp32 dy into its pieces
   int tile, splits, per_split;
   int64_t whole;  // tiles that are not split
   int64_t ldx, lddy;
@@ -75,34 +76,45 @@ struct Linear8Plan {
 // splits and expansion rests on.  The constants come from a fit to 1018 timings
 // on one MI355X (21 shapes from 512 x 512 x 512 to 8192 x 4096 x 14336, all
 // three passes; 10% rms; the choice cost 3% against the best one timed); those
-// of the 128 tiles were lowered by what going from 4 to 8 waves gained since.  Per stage of K (128 bytes of a row):
+// of the 128 tiles were lowered by what going from 4 to 8 waves gained since.
+// Per stage of K (128 bytes of a row):
 //   128 tiles  0.77 with one workgroup on a CU, 1.21 with two (forward 0.53,
 //              0.90): bound by issue and LDS, not by memory (a ring of four
 //              stages in LDS was no faster)
 //   256 tiles  1.71 converting the 8-bit operand, 1.32 on the expanded one (forward
 //              1.44) with all CUs at work, down to 0.84 (0.69) of it with few:
 //              bound by power at full load
+//   128 tiles  1.0 and 1.6 cutting fp32 dy into its pieces (input gradient 1.1
+//              and 1.8)
 // and a constant per round of workgroups; a second launch and partial tiles for
-// a split; a launch and 3 bytes per element for the expansion.
+// a split; a launch and 3 bytes per element for the expansion; a launch and 4 or
+// 10 bytes per element where dy is laid out as planes.  Cutting fp32 dy in the
+// product saves those, and costs each stage (us against planes: 701 x 301 x
+// 1531 20.2 and 25.0, 5451 x 64 x 11904 98 and 228, 4096 x 256 x 8192 94 and
+// 147, but 1500 x 1500 x 1500 53.8 and 51.3).
 // z parts of the tiles that do not fill a round (the chip holds 256 workgroups of
 // 256 tiles, 512 of 128): 14336 x 4096 has 3.5 rounds of 256 tiles, and its last
 // half round takes as long as a whole one unless it is split.
-double linear8_cost(bool fwd, int tile, bool expanded, int64_t M, int64_t N, int64_t K, int64_t nks, int64_t z,
-                    int planes) {
+double linear8_cost(int pass, int tile, bool expanded, bool dy_f32, int64_t M, int64_t N, int64_t K, int64_t nks,
+                    int64_t z, int planes) {
+  const bool fwd = pass == MUON_LINEAR8_FORWARD, dw = pass == MUON_LINEAR8_WEIGHT_GRAD;
   const int64_t slots = tile == 128 ? 512 : 256;
   const int64_t tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
   const int64_t rounds = tiles / slots, rem = tiles % slots;
   auto round = [&](int64_t wgs, double stages) {
+    if (dy_f32) return stages * (wgs <= 256 ? (dw ? 1.0 : 1.1) : (dw ? 1.6 : 1.8)) + 5.0;
     if (tile == 128)
       return stages * (wgs <= 256 ? (fwd ? 0.53 : 0.77) : (fwd ? 0.90 : 1.21)) + (fwd ? 5.0 : 4.7);
     const double low = fwd ? 0.69 : 0.84, fill = (double)std::min<int64_t>(wgs, 256) / 256.0;
     return stages * (fwd ? 1.44 : expanded ? 1.32 : 1.71) * (low + (1.0 - low) * fill) + (fwd ? 9.3 : 7.6);
   };
-  const double all = (double)nks * planes, part = (double)((nks + z - 1) / z) * planes;
+  const double pieces = planes ? planes : 1;
+  const double all = (double)nks * pieces, part = (double)((nks + z - 1) / z) * pieces;
   double us = (double)rounds * round(slots, all);
   for (int64_t left = rem * z; left > 0; left -= slots) us += round(std::min(left, slots), part);
   if (z > 1 && rem > 0)
     us += (fwd ? 3.3 : 5.9) + 8.0 * (double)z * (double)rem * (double)(tile * tile) / (fwd ? 7.7e6 : 9.0e6);
+  if (planes && !dy_f32) us += 3.0 + (double)M * (double)K * (planes == 3 ? 10.0 : 4.0) / 5.0e6;
   if (expanded) us += 3.3 + 3.0 * (double)K * (double)N / 5.3e6;
   return us;
 }
@@ -124,7 +136,7 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
   p.few = pass == MUON_LINEAR8_FORWARD &&
           (tokens <= 16 || (tokens <= 64 && out <= 8192 && out * in <= ((int64_t)1 << 24) &&
                             tokens * in <= ((int64_t)1 << 18)));
-  p.expanded = false;
+  p.expanded = p.dy_f32 = false;
   p.ldx = p.lddy = 0;
   p.dy_off = p.ws_off = 0;
   if (p.few) {
@@ -138,15 +150,16 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
   const bool fwd = pass == MUON_LINEAR8_FORWARD;
   double best = 0.0;
   int64_t z = 0;
-  for (int option = 0; option < (fwd ? 2 : 3); ++option) {
-    const int tile = option == 0 ? 128 : 256;
-    const bool expanded = option == 2;
+  for (int option = 0; option < (fwd ? 2 : planes == 3 ? 4 : 3); ++option) {
+    const int tile = option == 0 || option == 3 ? 128 : 256;
+    const bool expanded = option == 2, dy_f32 = option == 3;
     for (int64_t t = 1; t <= std::max<int64_t>(1, std::min<int64_t>(nks, 32)); ++t) {
-      const double us = linear8_cost(fwd, tile, expanded, M, N, K, nks, t, planes ? planes : 1);
+      const double us = linear8_cost(pass, tile, expanded, dy_f32, M, N, K, nks, t, planes);
       if (z == 0 || us < best) {
         best = us;
         p.tile = tile;
         p.expanded = expanded;
+        p.dy_f32 = dy_f32;
         z = t;
       }
     }
@@ -162,7 +175,7 @@ Linear8Plan linear8_plan(int pass, int64_t tokens, int64_t out, int64_t in, int 
     p.dy_off = (size_t)K * (size_t)p.ldx * 2;
   }
   p.ws_off = p.dy_off;
-  if (planes) {
+  if (planes && !p.dy_f32) {
     p.lddy = (out + 63) / 64 * 64;
     p.ws_off += (size_t)planes * (size_t)tokens * (size_t)p.lddy * 2;
   }
@@ -381,7 +394,7 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
   a.planes = planes ? planes : 1;
   PlanesArgs d;
   std::memset(&d, 0, sizeof(d));
-  if (planes) {
+  if (planes && !p.dy_f32) {
     d.dy = dy; d.ld = lddy;
     d.o = ws_base(workspace) + p.dy_off; d.ldo = p.lddy;
     d.plane = tokens * p.lddy;
@@ -403,7 +416,7 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
   return done(timed(weight ? F_LINEAR8_DW : F_LINEAR8_DX, f, 0.0, s, [&] {
-    if (planes) {
+    if (planes && !p.dy_f32) {
       const hipError_t e = launch_linear8_planes(dev_dt(dy_dtype), d, s);
       if (e != hipSuccess) return e;
     }
@@ -411,8 +424,8 @@ static muon_status linear8_grad(bool weight, const void* dy, int64_t lddy, int32
       const hipError_t e = launch_row_restore(DT_BF16, x, s);
       if (e != hipSuccess) return e;
     }
-    return weight ? launch_linear8_dw(p.tile, p.expanded, dev_dt(o_dtype), a, s)
-                  : launch_linear8_dx(p.tile, p.expanded, dev_dt(o_dtype), a, s);
+    return weight ? launch_linear8_dw(p.tile, p.expanded, p.dy_f32, dev_dt(o_dtype), a, s)
+                  : launch_linear8_dx(p.tile, p.expanded, p.dy_f32, dev_dt(o_dtype), a, s);
   }));
 }
 
