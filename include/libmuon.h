@@ -478,10 +478,11 @@ muon_status muon_linear8_input_grad(const void* dy, int64_t lddy, int32_t dy_dty
                                     int64_t lddx, int32_t dx_dtype, void* workspace, size_t workspace_bytes,
                                     void* stream);
 /* Bytes of workspace of one pass (muon_linear8_pass), host only; 0 for many
- * sizes, among them the forward pass of up to 16 tokens.  dy, lddy, dy_dtype: those of the gradient call (the address is only
- * looked at for its alignment: fp32 dy, and bf16 dy whose rows are not whole
- * 16-byte pieces, are laid out in the workspace first); ignored for the
- * forward pass.  Errors: MUON_E_METHOD (unknown pass), MUON_E_DTYPE,
+ * sizes, among them the forward pass of up to 16 tokens.  dy, lddy, dy_dtype:
+ * those of the gradient call (the address is only looked at for its alignment:
+ * bf16 dy whose rows are not whole 16-byte pieces, and fp32 dy where many
+ * columns of the result share it, are laid out in the workspace first); ignored
+ * for the forward pass.  Errors: MUON_E_METHOD (unknown pass), MUON_E_DTYPE,
  * MUON_E_SHAPE, MUON_E_ARG. */
 muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t out, int64_t in, const void* dy,
                                          int64_t lddy, int32_t dy_dtype, size_t* bytes);

@@ -117,7 +117,7 @@ struct Linear8Args {
   int32_t per_split;  // K-stages (128 bytes of a row) per split
   int32_t bias_dtype;
   int32_t accumulate;
-  int32_t planes;     // gradients: bf16 planes of dy that sum to it
+  int32_t planes;     // gradients: bf16 planes (or pieces cut in the product) of dy that sum to it
   int64_t plane;      // elements between them
 };
 // dy as bf16 planes (see linear8_planes_kernel).

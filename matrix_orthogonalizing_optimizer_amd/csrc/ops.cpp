@@ -54,8 +54,8 @@ size_t norm_ws(int64_t rows, int64_t cols) {
   return (size_t)norm_parts(rows, cols) * (size_t)cols * 2 * sizeof(float) + WS_ALIGN;
 }
 
-// How dy enters a gradient product: as it lies (0 planes to make), or laid out
-// as bf16 planes in the workspace.
+// How dy enters a gradient product: as it lies (0 planes to make), or as bf16
+// planes, laid out in the workspace or, of fp32, cut in the product.
 int dy_planes(const void* dy, int64_t lddy, int64_t out, int32_t dtype) {
   if (dtype == MUON_F32) return 3;
   return at_or_null(dy, 16) && lddy % 8 == 0 && out % 8 == 0 ? 0 : 1;
