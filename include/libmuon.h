@@ -442,7 +442,8 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
 /* A linear layer y = x W^T + bias on 8-bit rows: x as tokens x in rows (q,
  * scale per token), W as out x in rows (wq, wscale per output channel).
  * The products of 8-bit values are summed exactly in 32-bit integers, hence
- * in <= 131071.  y: tokens x out of dtype; bias: out values of bias_dtype, or
+ * in <= 131071; with any scales that 8-bit rows have, a result in fp32's range
+ * comes out finite.  y: tokens x out of dtype; bias: out values of bias_dtype, or
  * NULL.  The gradients are those of this layer with the rounding to 8 bits
  * taken as the identity:
  *   dW[n][k] = sum_t dy[t][n] scale[t] q[t][k]     out x in, dw_dtype; written,

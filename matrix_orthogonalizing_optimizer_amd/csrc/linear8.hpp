@@ -524,9 +524,14 @@ void linear8_kernel(const Linear8Args a) {
         } else {
           TO* o = static_cast<TO*>(a.o) + (int64_t)r * a.ldo;
           if constexpr (INT) {
-            const float sr = as_global(a.sa)[r];
+            float sr, sr2;
+            split_scale(as_global(a.sa)[r], sr, sr2);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = (float)__builtin_bit_cast(int32_t, v[e]) * sr * cs[e];
+            if (sr2 != 1.f) {  // multiplied for every row: 8192 x 14336 x 4096 417 instead of 414 us
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] *= sr2;
+            }
             if (a.bias) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] += cb[e];
@@ -569,11 +574,11 @@ __global__ __launch_bounds__(256) void linear8_join_kernel(const Linear8Args a) 
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[4 * h + e] += x[e];
       }
-    const float sr = as_global(a.sa)[r];
-    float cs[8];
+    float sr, sr2, cs[8];
+    split_scale(as_global(a.sa)[r], sr, sr2);
     piece_load(a.sb, c, a.N, cs);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)s[e] * sr * cs[e];
+    for (int e = 0; e < 8; ++e) v[e] = (float)s[e] * sr * cs[e] * sr2;
     if (a.bias) {
       vec_load(a.bias, a.bias_dtype, c, a.N, cs);
 #pragma unroll

@@ -107,12 +107,13 @@ __global__ __launch_bounds__(512) void linear8_few_kernel(const Linear8Args a) {
   for (int t = 0; t < T; ++t) {
     const int64_t tok = 16 * t + l16;
     if (tok >= a.M) continue;
-    const float sx = as_global(a.sa)[tok];
+    float sx, sx2;
+    split_scale(as_global(a.sa)[tok], sx, sx2);
     TO* y = static_cast<TO*>(a.o) + tok * a.ldo + n;
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[e] = (float)acc[t][e] * sx * ws[e];
+      v[e] = (float)acc[t][e] * sx * ws[e] * sx2;
       if (a.bias) v[e] += b[e];
     }
     if (n + 4 <= a.N) {

@@ -247,6 +247,17 @@ __device__ __forceinline__ void row_scale(uint32_t m, float& s, float& inv, floa
     inv = 0.f;
   }
 }
+// A sum of products of 8-bit values times the scale s of its row and a second
+// scale c, v = sum * a * c * b with s = a b.  Left to right, sum * s leaves
+// fp32's range from s = 2^97 on (|sum| < 2^31) though a small c may bring the
+// result back: there s gives 2^32 to b.  Nothing is lost below: c is at least
+// 2^-126, so from s = 2^96 on sum * a * c is zero or at least 2^-62.  Below, a is s
+// and b is 1.
+__device__ __forceinline__ void split_scale(float s, float& a, float& b) {
+  const bool large = __builtin_fabsf(s) >= 0x1p96f;
+  a = large ? s * 0x1p-32f : s;
+  b = large ? 0x1p32f : 1.f;
+}
 // 8 values -> 8 bytes; x * inv is exact (a power of two) wherever it matters:
 // what falls below the normal range rounds to 0 either way.
 __device__ __forceinline__ u32x2 quant8(const float (&v)[8], float inv, float lim, bool fine) {
