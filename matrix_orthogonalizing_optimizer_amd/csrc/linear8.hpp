@@ -24,7 +24,7 @@
 // workspace first (B_BF16; row_restore_kernel) and then copied to LDS like
 // dy: that takes 3 bytes of HBM traffic per element once, and saves every
 // workgroup the conversion and its register writes to LDS (1.88 -> 1.62 us per
-// 256 x 256 x 64 stage of random data).  linear8_plan in ops.cpp chooses.
+// 256 x 256 x 64 stage of random data).  linear8_plan (linear8_plan.hpp) chooses.
 // dy is copied to LDS directly as well, which takes bf16 rows in whole
 // 16-byte pieces.  Any other dy is laid out so in the workspace first
 // (linear8_planes_kernel): bf16 rows of odd widths or addresses as they are,
