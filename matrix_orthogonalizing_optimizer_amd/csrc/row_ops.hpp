@@ -136,6 +136,18 @@ template <typename T, bool SHORT> struct RowRaw {
       return __builtin_bit_cast(float, w[e]);
   }
 };
+// Piece at column c of a row of at least 8 elements that may be overwritten
+// from here on: what reaches past the row's end is taken from `last`, the
+// thread's last piece as it was loaded and settled before.  A select in the
+// load's registers, so no branch stands behind the load.
+template <typename T>
+__device__ __forceinline__ void row_piece_reload(const T* row, int c, int cols, const RowRaw<T, false>& last,
+                                                 float (&v)[8]) {
+  RowRaw<T, false> x = last;
+  if (c + 8 <= cols) x.load(row, c, cols);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = x.get(e);
+}
 // A piece of a row of at least 8 elements, widened.
 template <typename T> __device__ __forceinline__ void row_piece_load(const T* row, int c, int cols, float (&v)[8]) {
   RowRaw<T, false> x;
@@ -366,8 +378,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_forward_kernel(const Ro
   }
 }
 
-// The same for rows of any length, which are read again for every pass.  A
-// thread rereads only pieces that it alone writes, so y may be x.
+// The same for rows of any length, which are read again for every pass.  y may
+// be x: in the pass that writes, a thread reads only what it alone writes.  Its
+// piece at the row's end, which is loaded with columns of its neighbour, is kept
+// from the pass before (loading it element by element behind that loop took
+// 2048 x 20001 bf16 from 51 to 56 us).
 template <typename T, int KIND>
 __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a) {
   constexpr int G = 1024;
@@ -377,6 +392,7 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
   if (row >= a.rows) return;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   float mean = 0.f, r = 1.f;
+  RowRaw<T, false> last;
   if constexpr (KIND != ROW_COPY) {
     if constexpr (KIND == 0) {
       float s[1] = {0.f};
@@ -391,11 +407,11 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
     }
     float s[1] = {0.f};
     for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
-      float v[8];
-      row_piece_load(x, (int)c, a.cols, v);
+      last.load(x, (int)c, a.cols);
+      last.settle((int)c, a.cols);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = c + e < a.cols ? v[e] - mean : 0.f;
+        const float d = c + e < a.cols ? last.get(e) - mean : 0.f;
         s[0] = fmaf(d, d, s[0]);
       }
     }
@@ -407,8 +423,7 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
     }
     if (!a.y && !a.scale) return;
   }
-  auto value = [&](int64_t c, float (&v)[8]) {
-    row_piece_load(x, (int)c, a.cols, v);
+  auto norm = [&](int64_t c, float (&v)[8]) {
     if constexpr (KIND != ROW_COPY) {
       float w[8];
       vec_load<false>(a.gamma, a.vec_dtype, (int)c, a.cols, w);
@@ -427,7 +442,8 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
     uint32_t m = 0;
     for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
       float v[8];
-      value(c, v);
+      row_piece_load(x, (int)c, a.cols, v);
+      norm(c, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t b = c + e < a.cols ? mag_bits(v[e]) : 0u;
@@ -441,8 +457,10 @@ __global__ __launch_bounds__(1024) void row_forward_long_kernel(const RowArgs a)
   }
   const int64_t cpad = ((int64_t)a.cols + 15) & ~(int64_t)15;
   for (int64_t c = (int64_t)t * ROW_VE; c < cpad; c += G * ROW_VE) {
-    float v[8];
-    value(c, v);
+    float v[8];  // past the row's end: anything, and not written
+    if constexpr (KIND == ROW_COPY) row_piece_load(x, (int)c, a.cols, v);
+    else row_piece_reload(x, (int)c, a.cols, last, v);
+    norm(c, v);
     if (a.scale) {  // 8-bit rows (q may be null when there are no columns)
       float z[8];
 #pragma unroll
@@ -605,14 +623,16 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
   const float r = as_global(a.rstd)[row];
   const float mean = KIND == 0 ? as_global(a.mean)[row] : 0.f;
   float s[2] = {0.f, 0.f};
+  RowRaw<T, false> last;  // dx may be dy (see row_forward_long_kernel)
   for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
-    float h[8], g[8], w[8];
+    float h[8], w[8];
     row_piece_load(x, (int)c, a.cols, h);
-    row_piece_load(dy, (int)c, a.cols, g);
+    last.load(dy, (int)c, a.cols);
+    last.settle((int)c, a.cols);
     vec_load<false>(a.gamma, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float ge = g[e] * w[e];
+      const float ge = last.get(e) * w[e];
       s[0] = fmaf(ge, (h[e] - mean) * r, s[0]);
       s[1] += ge;
     }
@@ -622,7 +642,7 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBwdA
   for (int64_t c = (int64_t)t * ROW_VE; c < a.cols; c += G * ROW_VE) {
     float h[8], g[8], w[8];
     row_piece_load(x, (int)c, a.cols, h);
-    row_piece_load(dy, (int)c, a.cols, g);
+    row_piece_reload(dy, (int)c, a.cols, last, g);
     vec_load<false>(a.gamma, a.vec_dtype, (int)c, a.cols, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = r * (g[e] * w[e] - c1 - (h[e] - mean) * r * c2);
