@@ -403,7 +403,7 @@ void linear8_kernel(const Linear8Args a) {
   };
 
   if (nst > 0) {
-    // ---- prologue: stage 0 in LDS, stage 1 on its way
+    // ---- prologue: stages 0 and 1 in LDS (of converted operands, stage 1's values in registers)
     auto copies = [&](int v) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
@@ -424,7 +424,10 @@ void linear8_kernel(const Linear8Args a) {
     advance();
     load_b(ksn);
     copies(1);
-    if constexpr (!AF32) wait_vmcnt<(CVT ? 3 : 2) * NQ>();  // what was issued for stage 1 may be under way
+    // All of it, stage 1 too: a wait for stage 0 alone would count on an order of
+    // issue that nothing holds the compiler to, and the barrier waits for every
+    // copy to LDS anyway.
+    if constexpr (!AF32) wait_vmcnt_lgkm0<0>();
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < NDR; ++r) read_one(ro(r), 0, 0, 0);

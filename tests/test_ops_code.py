@@ -11,6 +11,8 @@ hipcc cross-compiles for gfx950).
   s_waitcnt that covers it, counting LDS instructions in issue order; and no
   scalar load, which shares the counter and completes out of order, is under
   way together with one.
+- No copy to LDS is under way at a barrier: the waves behind it read what the
+  others copied.
 """
 import os
 import re
@@ -152,3 +154,29 @@ def test_transposed_reads_are_waited_for(src, compiled):
         loose = re.sub(r"lgkmcnt\(\d+\)", "lgkmcnt(15)", m.group(2))
         assert _untracked_uses(loose)
     assert found >= 6
+
+
+def _copies_at_barriers(text):
+    """Barriers with copies to LDS under way, in the order of the text (which a
+    loop of these kernels enters with its copies behind the barrier)."""
+    open_, bad, copies = False, 0, 0
+    for l in (l.split(";")[0].strip() for l in text.splitlines()):
+        if l.startswith("buffer_load") and l.endswith(" lds"):
+            open_, copies = True, copies + 1
+        elif l.startswith("s_waitcnt") and "vmcnt(0)" in l:
+            open_ = False
+        elif l.startswith("s_barrier") and open_:
+            bad += 1
+    return bad, copies
+
+
+@pytest.mark.parametrize("src", SOURCES[1:])
+def test_copies_to_lds_are_waited_for_at_barriers(src, compiled):
+    found = 0
+    for m in re.finditer(r"^(_ZN4muon14linear8_kernel\w*):(.*?)^\.Lfunc_end", compiled(src)[0], re.S | re.M):
+        bad, copies = _copies_at_barriers(m.group(2))
+        assert bad == 0, m.group(1)
+        if copies:
+            found += 1
+            assert _copies_at_barriers(m.group(2).replace("vmcnt(0)", "vmcnt(1)"))[0] > 0
+    assert found >= 4
