@@ -415,6 +415,9 @@ typedef enum { MUON_NORM_LAYER = 0, MUON_NORM_RMS = 1 } muon_norm_kind;
  *   q, ldq, scale: y, before any rounding to dtype, as 8-bit rows (both or neither)
  *   mean, rstd: rows fp32 values of mu and r, for the backward pass (mean must
  *     be NULL for MUON_NORM_RMS).
+ * With rows == 0 or cols == 0 nothing is read or written: a row without values
+ * has no statistics, and its 8-bit form needs no scale (see
+ * muon_linear8_forward; muon_rows8_quantize writes 2^-126).
  * Errors: MUON_E_METHOD (unknown kind), MUON_E_DTYPE, MUON_E_SHAPE (as for
  * muon_rows8_quantize), MUON_E_ARG (a required pointer null, any pointer
  * misaligned, eps negative or not finite, no output), MUON_E_HIP. */

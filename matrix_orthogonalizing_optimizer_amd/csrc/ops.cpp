@@ -123,9 +123,9 @@ muon_status muon_norm_forward(int32_t kind, const void* x, int64_t rows, int64_t
       (q && (!ld_ok(ldq, cols, MAX_LD) || ldq % 16)))
     return MUON_E_SHAPE;
   if (!std::isfinite(eps) || eps < 0.f) return MUON_E_ARG;
-  if ((q != nullptr) != (scale != nullptr) || (kind == MUON_NORM_RMS && mean)) return MUON_E_ARG;
-  if (rows == 0 || cols == 0) return MUON_OK;
-  if (!y && !q && !mean && !rstd) return MUON_E_ARG;
+  if (kind == MUON_NORM_RMS && mean) return MUON_E_ARG;
+  if (rows == 0 || cols == 0) return MUON_OK;  // the address of an empty q may be null
+  if ((q != nullptr) != (scale != nullptr) || (!y && !q && !mean && !rstd)) return MUON_E_ARG;
   if (!at(x, esize(dtype)) || !at(gamma, esize(vec_dtype)) || !at_or_null(beta, esize(vec_dtype)) ||
       !at_or_null(y, esize(dtype)) || !at_or_null(q, 16) || !at_or_null(scale, 4) || !at_or_null(mean, 4) ||
       !at_or_null(rstd, 4))

@@ -236,3 +236,11 @@ def test_binding_refuses(i):
     call, text = BINDING[i]
     with pytest.raises(ValueError, match=text):
         call()
+
+
+def test_norm_into_empty_rows8_is_accepted():
+    """An empty q has a null address; its scales may not."""
+    L = _lib()
+    for ch in (dict(cols=0, q=None), dict(rows=0, q=None), dict(cols=0, scale=None)):
+        assert L.muon_norm_forward(*dict(NF, **ch).values()) == 0, ch
+    assert L.muon_norm_forward(*dict(NF, cols=0, kind=1).values()) == E_ARG  # RMS norms have no mean
