@@ -456,7 +456,8 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
  * bf16: exact for powers of two, rounded once for other scales.  fp32 dy is
  * taken as three bf16 pieces that add up to it, so it loses nothing.
  * With tokens == 0 the weight gradient is zero; with out == 0 the input
- * gradient is; with in == 0 y is the bias.
+ * gradient is; with in == 0 y is the bias (zero without one), whatever the
+ * scales hold.
  * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, in above
  * 131071 for the forward product, a leading dimension below its column count
  * or above 2^21, ldq or ldw not a multiple of 16, a result of more than 2^22

@@ -38,6 +38,7 @@ hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s);
 // expanded: a.B is the 8-bit operand turned into bf16 (256 tiles only).
 hipError_t launch_linear8_forward(int tile, int odt, const Linear8Args& a, hipStream_t s);
 hipError_t launch_linear8_few(int odt, const Linear8Args& a, hipStream_t s);  // at most 64 tokens
+hipError_t launch_linear8_bias(int odt, const Linear8Args& a, hipStream_t s);  // no channels in
 hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s);
 hipError_t launch_linear8_dw(int tile, bool expanded, bool dy_f32, int odt, const Linear8Args& a, hipStream_t s);
 hipError_t launch_linear8_dx(int tile, bool expanded, bool dy_f32, int odt, const Linear8Args& a, hipStream_t s);

@@ -245,6 +245,7 @@ muon_status muon_linear8_forward(const int8_t* q, int64_t ldq, const float* scal
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)tokens * (double)out * (double)in;
   return done(timed(F_LINEAR8_Y, f, 0.0, s, [&] {
+    if (in == 0) return launch_linear8_bias(dev_dt(dtype), a, s);
     return p.few ? launch_linear8_few(dev_dt(dtype), a, s) : launch_linear8_forward(p.tile, dev_dt(dtype), a, s);
   }));
 }

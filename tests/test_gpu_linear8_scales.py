@@ -69,3 +69,21 @@ def test_true_overflow_and_nan(t, n, k):
     assert (y[0, cols] == math.inf).all() and (y[1, cols] == 0).all()
     assert torch.isnan(y[2]).all() and torch.isnan(y[:, 3]).all()
     assert not torch.isnan(y[[r for r in range(t) if r != 2]][:, cols]).any()
+
+
+@pytest.mark.parametrize("t", [1, 5, 40, 200, 5000])
+def test_no_channels_in_is_the_bias(t):
+    """A sum of nothing is zero whatever the scales hold; the norm of rows
+    without columns leaves them as they are."""
+    n = 300
+    x = torch.zeros(t, 16, dtype=BF, device=dev())[:, :0]
+    q = torch.empty(t, 16, dtype=torch.int8, device=dev())[:, :0]
+    s, ws = torch.full((t,), math.nan, device=dev()), torch.full((n,), math.inf, device=dev())
+    rstd = torch.full((t,), 5.0, device=dev())
+    mo.muon_norm_forward(x, torch.ones(0, dtype=BF, device=dev()), q=q, scale=s, rstd=rstd)
+    assert torch.isnan(s).all() and (rstd == 5).all()
+    wq = torch.empty(n, 16, dtype=torch.int8, device=dev())[:, :0]
+    b = torch.randn(n, generator=torch.Generator().manual_seed(5)).to(dev())
+    for dtype in (F32, BF):
+        assert torch.equal(mo.muon_linear8_forward(q, s, wq, ws, bias=b, dtype=dtype), b.to(dtype).expand(t, n))
+        assert (mo.muon_linear8_forward(q, s, wq, ws, dtype=dtype) == 0).all()
