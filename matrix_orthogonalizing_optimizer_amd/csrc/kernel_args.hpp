@@ -86,6 +86,7 @@ struct NormBwdArgs {
   int64_t lddy, ldx, lddx, rows;
   int32_t cols;
   int32_t vec_dtype;
+  int32_t sum_dy;   // the bias gradient is asked for
 };
 struct JoinArgs {
   const float* partials;

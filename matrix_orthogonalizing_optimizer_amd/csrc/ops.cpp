@@ -163,7 +163,7 @@ muon_status muon_norm_backward(int32_t kind, const void* dy, int64_t lddy, const
       !ld_ok(lddx, cols, MAX_LD))
     return MUON_E_SHAPE;
   const size_t es = esize(dtype), ve = esize(vec_dtype);
-  if (kind == MUON_NORM_RMS && (mean || dbeta)) return MUON_E_ARG;
+  if (kind == MUON_NORM_RMS && mean) return MUON_E_ARG;
   if (!at_or_null(dgamma, ve) || !at_or_null(dbeta, ve)) return MUON_E_ARG;
   if (cols == 0) return MUON_OK;
   if (rows > 0) {
@@ -186,6 +186,7 @@ muon_status muon_norm_backward(int32_t kind, const void* dy, int64_t lddy, const
     a.mean = mean; a.rstd = rstd;
     a.dx = dx; a.lddx = lddx;
     a.partials = part;
+    a.sum_dy = dbeta != nullptr;
     a.rows = rows; a.cols = (int32_t)cols;
     const double n = (double)rows * (double)cols;
     const hipError_t e = timed(F_NORM_BWD, 0.0, 3.0 * n * (double)es, s,

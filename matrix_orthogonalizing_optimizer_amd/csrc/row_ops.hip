@@ -57,7 +57,7 @@ template <typename T, int KIND> hipError_t backward(const NormBwdArgs& a, int pa
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((norm_backward_long_kernel<T, KIND>), row_grid(a.rows), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((norm_backward_long_kernel<T, KIND == 0 ? 0 : 1>), row_grid(a.rows), dim3(1024), 0, s, a);
     return hipGetLastError();
   }
   return by_width(a.cols, [&](auto g, auto nv) {
@@ -96,8 +96,14 @@ hipError_t launch_row_restore(int dt, const RestoreArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_norm_backward(int kind, int dt, const NormBwdArgs& a, int parts, hipStream_t s) {
-  if (dt == DT_BF16) return kind == 0 ? backward<bf16, 0>(a, parts, s) : backward<bf16, 1>(a, parts, s);
-  return kind == 0 ? backward<float, 0>(a, parts, s) : backward<float, 1>(a, parts, s);
+  const bool rms_beta = kind != 0 && a.sum_dy;
+  if (dt == DT_BF16)
+    return kind == 0 ? backward<bf16, 0>(a, parts, s)
+           : rms_beta ? backward<bf16, NORM_RMS_BETA>(a, parts, s)
+                      : backward<bf16, 1>(a, parts, s);
+  return kind == 0 ? backward<float, 0>(a, parts, s)
+         : rms_beta ? backward<float, NORM_RMS_BETA>(a, parts, s)
+                    : backward<float, 1>(a, parts, s);
 }
 
 hipError_t launch_norm_join(int vec_dtype, const JoinArgs& a, hipStream_t s) {

@@ -497,6 +497,12 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void row_restore_kernel(const Re
   }
 }
 
+// The backward kernels' KIND is that of the norm, and NORM_RMS_BETA for an RMS
+// norm whose bias gradient is asked for: the others keep no sum of dy that
+// nobody reads (a layer norm needs it for dx's mean in any case).
+enum : int { NORM_RMS_BETA = 3 };
+constexpr bool norm_sums_dy(int kind) { return kind != 1; }
+
 // Norm backward: workgroups loop over rows; a thread keeps its columns' gamma
 // and its sums of dy h and dy in registers over all of them, and the sums go
 // to workspace once per workgroup (partials[2][workgroups][cols]).  The next
@@ -555,7 +561,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
       for (int e = 0; e < 8; ++e) {
         const float h = (cx[i].get(e) - cm) * cr, d = cd[i].get(e);
         sg[i][e] = fmaf(d, h, sg[i][e]);
-        if (KIND == 0) sb[i][e] += d;
+        if (norm_sums_dy(KIND)) sb[i][e] += d;
         const float g = d * gam[i][e];
         s[0] = fmaf(g, h, s[0]);
         if (KIND == 0) s[1] += g;
@@ -605,7 +611,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_backward_kernel(const 
       if ((i * G + t) * ROW_VE < a.cols) piece_store(p, (i * G + t) * ROW_VE, a.cols, v[i]);
   };
   put(sg, 0);
-  if constexpr (KIND == 0) put(sb, 1);
+  if constexpr (norm_sums_dy(KIND)) put(sb, 1);
 }
 
 // Rows above NORM_BWD_MAX_COLS (a thread would hold too much of one): dx with
@@ -669,7 +675,7 @@ __global__ __launch_bounds__(256) void norm_columns_long_kernel(const NormBwdArg
     }
   }
   piece_store(a.partials + (int64_t)blockIdx.y * a.cols, (int)c, a.cols, sg);
-  if (KIND == 0) piece_store(a.partials + ((int64_t)gridDim.y + blockIdx.y) * a.cols, (int)c, a.cols, sb);
+  if (norm_sums_dy(KIND)) piece_store(a.partials + ((int64_t)gridDim.y + blockIdx.y) * a.cols, (int)c, a.cols, sb);
 }
 
 // Joins the workgroups' column sums in order: 64 columns per workgroup, 16
