@@ -583,6 +583,8 @@ def _scratch(di, stream, workspace, nbytes):
         if nbytes == 0:
             return None, None, 0
         workspace = _empty(di, stream, nbytes, dtype=torch.uint8)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

@@ -244,3 +244,14 @@ def test_norm_into_empty_rows8_is_accepted():
     for ch in (dict(cols=0, q=None), dict(rows=0, q=None), dict(cols=0, scale=None)):
         assert L.muon_norm_forward(*dict(NF, **ch).values()) == 0, ch
     assert L.muon_norm_forward(*dict(NF, cols=0, kind=1).values()) == E_ARG  # RMS norms have no mean
+
+
+def test_workspace_has_to_be_contiguous():
+    """The kernels write the workspace's bytes in a row: one whose elements lie
+    apart, or upon each other, holds less than it has elements."""
+    one = torch.zeros(1, dtype=torch.uint8)
+    for ws in (one.expand(4096), torch.zeros(8192, dtype=torch.uint8)[::2], torch.zeros(64, 64)[:, :32]):
+        with pytest.raises(ValueError, match="workspace"):
+            mo._lib._scratch(0, None, ws, 16)
+    ws = torch.zeros(64, 16)[8:24]
+    assert mo._lib._scratch(0, None, ws, 16) == (ws, ws.data_ptr(), 16 * 16 * 4)
