@@ -454,7 +454,8 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
  *   dX[t][k] = sum_n dy[t][n] wscale[n] wq[n][k]   tokens x in, dx_dtype
  * dy: tokens x out, bf16 or fp32.  q * scale enters the gradient products in
  * bf16: exact for powers of two, rounded once for other scales.  fp32 dy is
- * taken as three bf16 pieces that add up to it, so it loses nothing.
+ * taken as three bf16 pieces that add up to it: exactly from 2^-110 up, below
+ * that without its bits under 2^-133, the last that bf16 has.
  * With tokens == 0 the weight gradient is zero; with out == 0 the input
  * gradient is; with in == 0 y is the bias (zero without one), whatever the
  * scales hold.

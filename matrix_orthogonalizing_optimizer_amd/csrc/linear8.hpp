@@ -28,7 +28,7 @@
 // dy is copied to LDS directly as well, which takes bf16 rows in whole
 // 16-byte pieces.  Any other dy is laid out so in the workspace first
 // (linear8_planes_kernel): bf16 rows of odd widths or addresses as they are,
-// fp32 as three bf16 planes that sum to it exactly (8 significant bits each);
+// fp32 as three bf16 planes that sum to it (8 significant bits each; see bf16_piece);
 // K is then walked once per plane.  The planes are 6 bytes written and read
 // next to 4 of dy.  Where few tile columns share them, the 128 tiles cut fp32 dy
 // themselves (B_Q8_A_F32): it is loaded to registers once per K-stage, each of
@@ -71,8 +71,9 @@ template <> struct Acc8<false> {
 
 // Piece p (0, 1, 2) of fp32 x as bf16 bits in the high half of the result.
 // Cutting off mantissa bits leaves at most 24 - 8 - 8 = 8 significant bits
-// for the last piece, so the three add up to x exactly; an infinity or NaN is
-// all in the first piece (a NaN keeps a mantissa bit).
+// for the last piece, so the three add up to x exactly, except for bits under
+// 2^-133, which bf16 does not have (so from |x| = 2^-110 up nothing is lost); an
+// infinity or NaN is all in the first piece (a NaN keeps a mantissa bit).
 __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
   uint32_t hi = u & 0xffff0000u;
