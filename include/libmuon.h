@@ -406,7 +406,9 @@ muon_status muon_rows8_dequantize(const int8_t* q, int64_t ldq, const float* sca
 /* Row norms.  Per row x of cols values (all rows independent):
  *   mu = mean(x) (MUON_NORM_LAYER) or 0 (MUON_NORM_RMS)
  *   r  = 1 / sqrt(mean((x - mu)^2) + eps),  h = (x - mu) r
- *   y  = h gamma + beta */
+ *   y  = h gamma + beta
+ * The squares are summed in fp32: a row whose sum of (x - mu)^2 passes 2^128
+ * gets r = 0. */
 typedef enum { MUON_NORM_LAYER = 0, MUON_NORM_RMS = 1 } muon_norm_kind;
 
 /* x: rows x cols, dtype.  gamma, beta: cols values of vec_dtype; beta may be
@@ -462,7 +464,7 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
  * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, in above
  * 131071 for the forward product, a leading dimension below its column count
  * or above 2^21, ldq or ldw not a multiple of 16, a result of more than 2^22
- * 128 x 128 tiles); MUON_E_ARG (a pointer null
+ * tiles, which are 128 x 128 or, of some large products, 256 x 256); MUON_E_ARG (a pointer null
  * or misaligned: 8-bit rows to 16 bytes, others to their element);
  * MUON_E_WORKSPACE (workspace smaller than muon_linear8_workspace_bytes);
  * MUON_E_HIP. */

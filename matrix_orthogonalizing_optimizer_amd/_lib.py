@@ -613,7 +613,9 @@ def _launch(fn, di, stream, *args):
 def muon_rows8_quantize(x, q=None, scale=None, stream=None):
     """(q, scale): the 8-bit rows of x (2-D, fp32 or bf16, rows may be
     strided).  q: int8, x's shape, rows a multiple of 16 bytes apart (None:
-    allocated so); scale: fp32, one per row, a power of two."""
+    allocated so; the bytes of a row behind its columns up to the next multiple
+    of 16 are set to zero, which the products rely on); scale: fp32, one per
+    row, a power of two."""
     rows, cols, ldx, dt = _matrix("x", x)
     if (q is None) != (scale is None):
         raise ValueError("q and scale: give both or neither")

@@ -25,8 +25,9 @@ struct Linear8Plan {
 // Estimated time of a tiled product in us: what the choice between tiles,
 // splits and expansion rests on.  The constants come from a fit to 1018 timings
 // on one MI355X (21 shapes from 512 x 512 x 512 to 8192 x 4096 x 14336, all
-// three passes; 10% rms; the choice cost 3% against the best one timed); those
-// of the 128 tiles were lowered by what going from 4 to 8 waves gained since.
+// three passes; 10% rms; the choice cost 3% against the best one timed then);
+// those of the 128 tiles were lowered by hand by what going from 4 to 8 waves
+// gained afterwards, and the choice as a whole has not been timed since.
 // Per stage of K (128 bytes of a row):
 //   128 tiles  0.77 with one workgroup on a CU, 1.21 with two (forward 0.53,
 //              0.90): bound by issue and LDS, not by memory (a ring of four
@@ -45,8 +46,8 @@ struct Linear8Plan {
 // z parts of the tiles that do not fill a round (the chip holds 256 workgroups of
 // 256 tiles, 512 of 128): 14336 x 4096 has 3.5 rounds of 256 tiles, and its last
 // half round takes as long as a whole one unless it is split.
-inline double linear8_cost(int pass, int tile, bool expanded, bool dy_f32, int64_t M, int64_t N, int64_t K, int64_t nks,
-                    int64_t z, int planes) {
+inline double linear8_cost(int pass, int tile, bool expanded, bool dy_f32, int64_t M, int64_t N, int64_t K,
+                           int64_t nks, int64_t z, int planes) {
   const bool fwd = pass == MUON_LINEAR8_FORWARD, dw = pass == MUON_LINEAR8_WEIGHT_GRAD;
   const int64_t slots = tile == 128 ? 512 : 256;
   const int64_t tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
