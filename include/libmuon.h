@@ -448,8 +448,8 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
  * scale per token), W as out x in rows (wq, wscale per output channel).
  * The products of 8-bit values are summed exactly in 32-bit integers, hence
  * in <= 131071; with any scales that 8-bit rows have, a result in fp32's range
- * comes out finite.  y: tokens x out of dtype; bias: out values of bias_dtype, or
- * NULL.  The gradients are those of this layer with the rounding to 8 bits
+ * comes out finite.  y: tokens x out of dtype; bias: out values of bias_dtype,
+ * or NULL.  The gradients are those of this layer with the rounding to 8 bits
  * taken as the identity:
  *   dW[n][k] = sum_t dy[t][n] scale[t] q[t][k]     out x in, dw_dtype; written,
  *              or added to dw when accumulate is nonzero
@@ -464,8 +464,9 @@ muon_status muon_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_
  * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, in above
  * 131071 for the forward product, a leading dimension below its column count
  * or above 2^21, ldq or ldw not a multiple of 16, a result of more than 2^22
- * tiles, which are 128 x 128 or, of some large products, 256 x 256); MUON_E_ARG (a pointer null
- * or misaligned: 8-bit rows to 16 bytes, others to their element);
+ * tiles, which are 128 x 128 or, of some large products, 256 x 256);
+ * MUON_E_ARG (a pointer null or misaligned: 8-bit rows to 16 bytes, others to
+ * their element);
  * MUON_E_WORKSPACE (workspace smaller than muon_linear8_workspace_bytes);
  * MUON_E_HIP. */
 typedef enum {
