@@ -82,12 +82,14 @@ typedef enum {
 } muon_ns_method;
 
 /* Storage dtype of parameters and gradients.  Momentum and AdamW moments are
- * always fp32. */
+ * fp32, but for the moments of MUON_KIND_ADAMW8. */
 typedef enum { MUON_F32 = 0, MUON_BF16 = 1 } muon_dtype;
 
 /* [Moonlight] "代码": parameters tagged use_muon take the Muon rule, the rest
- * (embeddings, heads, norms, biases) take the AdamW backup. */
-typedef enum { MUON_KIND_MUON = 0, MUON_KIND_ADAMW = 1 } muon_kind;
+ * (embeddings, heads, norms, biases) take the AdamW backup.  An extension:
+ * MUON_KIND_ADAMW8 is the AdamW backup with its two moments kept in 8 bits
+ * (see muon_adamw8_state_bytes); 2 is not a kind. */
+typedef enum { MUON_KIND_MUON = 0, MUON_KIND_ADAMW = 1, MUON_KIND_ADAMW8 = 3 } muon_kind;
 
 /* One row of the shape table (plan time; no pointers).
  *   rows, cols  the 2-D view of the parameter (callers flatten ndim > 2 as
@@ -112,6 +114,8 @@ typedef struct {
  *   grad      rows x cols, dtype; read only.
  *   momentum  rows x cols fp32 (Muon kind); updated in place.
  *   exp_avg, exp_avg_sq  rows x cols fp32 (AdamW kind); updated in place.
+ *             MUON_KIND_ADAMW8: device buffers of muon_adamw8_state_bytes
+ *             bytes each, 4-byte aligned (cast to float*).
  *   update_out  optional (may be NULL), Muon kind: rows x cols fp32 receives
  *             the orthogonalized update O of every unit (before scaling).
  * Alignment: param/grad to their element size, fp32 buffers to 4 bytes. */
@@ -176,6 +180,50 @@ typedef struct {
   float extra_scale;
 } muon_hparams;
 
+/* The moments of a MUON_KIND_ADAMW8 parameter, in 8 bits each.  A step computes
+ * in fp32, each operation rounded by itself,
+ *   m <- m + (1-b1) (g - m);  v <- v + (1-b2) (g g - v);
+ *   W <- W (1 - lr wd) - lr sqrt(1-b2^t)/(1-b1^t) m / (eps + sqrt(v))
+ * with m and v as they are, and then rounds them to what is kept:
+ * Blocks of 256 elements in a row of the parameter's memory share an offset o.
+ * With u(x) the bits of the float x >= 0,
+ *   o = max(0, ceil(max u(x) / 2^20) - K),  K = 127 for |m|, 255 for v,
+ * an element's code k stands for the float of bits (k + o) 2^20, and for zero
+ * where k = 0; the code of m has its sign in bit 7.  That is 3 bits of
+ * mantissa and 15.9 (m) or 31.9 (v) powers of two below the block's largest.
+ *   k = floor((u(x) + 16 r) / 2^20) - o,  r uniform in 0 .. 65535:
+ * a value is rounded up or down with the probabilities that keep its mean
+ * (nearest rounding would hold v where it is: a step takes at most 1-b2 off
+ * it).  Under the smallest code lo (o + 1 as bits), m gets lo where
+ * |m| > lo (r + 1/2) / 65536 and else 0, and v > 0 gets lo.  NaN and infinity
+ * are kept, and lower the rest of their block to 0 or lo; finite values of at
+ * least 1.875 2^127 may become infinite.
+ * r comes from the step's number t and the element's index i: with
+ *   mix(x): x ^= x >> 16; x *= 0x6a09e667; x ^= x >> 15; x *= 0xbb67ae85;
+ *           x ^= x >> 16     (all modulo 2^32)
+ *   key = mix(lo32(t) ^ mix(hi32(t))),  q = i / 4,
+ *   h = mix(lo32(q) ^ (hi32(q) * 0x9e3779b1) ^ key) rotated right by 8 (i % 4),
+ * r is the low half of h for m and the high half for v.  So a step's result
+ * follows from its inputs, whatever else the step updates.
+ * Storage: the codes of ceil(numel / 256) whole blocks, then a 16-bit offset
+ * per block, then up to the next multiple of 16 bytes.  All zero bytes are
+ * zero moments (a new parameter's).  Codes behind the last element are left as
+ * they are.  Buffers of one parameter follow each other without gaps at
+ * 16-byte alignment.
+ * adam_beta1 and adam_beta2 are in [0, 1) for such parameters.
+ *
+ * muon_adamw8_state_bytes: bytes of one moment (host only).
+ * muon_adamw8_pack: fp32 values x to a moment's buffer, rounded as in step
+ *   `step` (codes behind the last element become 0, bytes behind the offsets
+ *   are left).  MUON_ADAMW8_SECOND takes |x|.
+ * muon_adamw8_unpack: the values that a buffer stands for.
+ * Errors: MUON_E_METHOD (unknown moment), MUON_E_SHAPE (numel negative or above
+ * 2^40), MUON_E_ARG (a pointer null or not 4-byte aligned), MUON_E_HIP. */
+typedef enum { MUON_ADAMW8_FIRST = 0, MUON_ADAMW8_SECOND = 1 } muon_adamw8_moment;
+muon_status muon_adamw8_state_bytes(int64_t numel, size_t* bytes);
+muon_status muon_adamw8_pack(const float* x, int64_t numel, int32_t moment, int64_t step, void* state, void* stream);
+muon_status muon_adamw8_unpack(const void* state, int64_t numel, int32_t moment, float* x, void* stream);
+
 /* Plan options.
  *   ns_method  muon_ns_method.
  *   ns_dtype   -1: Newton-Schulz computes in the parameter dtype (bf16 MFMA
@@ -204,7 +252,8 @@ typedef struct muon_plan muon_plan;
  * muon_plan_destroy.  Errors: MUON_E_ARG (null out, n < 0, unknown kind),
  * MUON_E_DTYPE, MUON_E_METHOD, MUON_E_SHAPE (negative size, side > 2^30,
  * split_rows not dividing rows or set on an AdamW row, a unit whose
- * working copy reaches 2^31 bytes); on error *out is NULL. */
+ * working copy reaches 2^31 bytes, a MUON_KIND_ADAMW8 row of more than 2^40
+ * elements); on error *out is NULL. */
 muon_status muon_plan_create(const muon_param_shape* table, int32_t n,
                              const muon_plan_options* opts, muon_plan** out);
 void muon_plan_destroy(muon_plan* plan);

@@ -435,11 +435,13 @@ muon_status muon_step(const muon_plan* plan, const muon_param_ptrs* ptrs, int32_
   if (hp->scale_mode != MUON_SCALE_MOONLIGHT && hp->scale_mode != MUON_SCALE_SPECTRAL &&
       hp->scale_mode != MUON_SCALE_UNIT_RMS)
     return MUON_E_ARG;
-  if (!P.adam.empty()) {
+  if (!P.adam.empty() || !P.adam8.empty()) {
     if (!finite(hp->adam_lr) || !finite(hp->adam_beta1) || !finite(hp->adam_beta2) ||
         !finite(hp->adam_eps) || !finite(hp->adam_weight_decay) || hp->adam_step < 1)
       return MUON_E_ARG;
     if (hp->adam_beta1 >= 1.f || hp->adam_beta2 >= 1.f) return MUON_E_ARG;
+    // a second moment has to stay nonnegative: its code has no sign
+    if (!P.adam8.empty() && (hp->adam_beta1 < 0.f || hp->adam_beta2 < 0.f)) return MUON_E_ARG;
   }
   // pointer checks
   for (int32_t p = 0; p < n; ++p) {
@@ -457,8 +459,9 @@ muon_status muon_step(const muon_plan* plan, const muon_param_ptrs* ptrs, int32_
     }
   }
   if (P.lay.total > 0 && (!workspace || workspace_bytes < P.lay.total)) return MUON_E_WORKSPACE;
-  if (P.lay.total == 0) return MUON_OK;
   hipStream_t st_ = reinterpret_cast<hipStream_t>(stream);
+  if (!P.adam8.empty()) HIP_TRY(launch_adamw8(P, ptrs, *hp, st_));
+  if (P.lay.total == 0) return MUON_OK;
   char* ws = align_base(workspace);
 
   // per-unit descriptors, uploaded once per step

@@ -1,6 +1,7 @@
 // Argument blocks of the libmuon kernels (shared by launchers and kernels).
 #pragma once
 
+#include "consts.hpp"
 #include "device_common.hpp"
 
 namespace muon {
@@ -51,6 +52,32 @@ struct AdamArgs {
   int64_t block_base;  // first global block of this launch
   int32_t nparams;
   float one_minus_b1, one_minus_b2, eps, keep, step;
+};
+
+// AdamW on 8-bit moments (see adamw8.hpp).
+struct Adamw8Desc {
+  void* w;
+  const void* g;
+  uint8_t* m;
+  uint8_t* v;
+  int64_t numel;
+  int32_t dtype;  // DT_F32 or DT_BF16, of w and g
+  int32_t pad;
+};
+struct Adamw8Args {
+  float one_minus_b1, one_minus_b2, eps, keep, step;
+  uint32_t key;      // of the step's random bits
+  int32_t tensors;
+  uint32_t wg_base;  // first workgroup of this launch
+  uint32_t first[ADAMW8_TENSORS];  // first workgroup of every tensor
+  Adamw8Desc desc[ADAMW8_TENSORS];
+};
+static_assert(sizeof(Adamw8Args) <= 4096, "kernel arguments");
+struct Adamw8PackArgs {
+  float* x;
+  uint8_t* state;
+  int64_t numel;
+  uint32_t key;
 };
 
 // Row operators (see row_ops.hpp).

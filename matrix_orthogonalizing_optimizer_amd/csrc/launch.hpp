@@ -4,8 +4,11 @@
 #include <hip/hip_runtime.h>
 
 #include "kernel_args.hpp"
+#include "libmuon.h"
 
 namespace muon {
+
+struct PlanImpl;
 
 // GEMM launch for input dtype ti / output dtype to (DT_*), tile edge 128 or
 // 256, symmetric-output flag, epilogue kind and operand layout (trans: both
@@ -21,6 +24,8 @@ hipError_t launch_momentum(int gdtype, int xdtype, bool tall, const MomArgs& a, 
 hipError_t launch_norm_finalize(const float* partials, int32_t per_unit, float4* aux, int32_t units,
                                 hipStream_t s);
 hipError_t launch_adamw(const AdamArgs& a, int64_t total_blocks, hipStream_t s);
+// The AdamW parameters of the plan with 8-bit moments.
+hipError_t launch_adamw8(const PlanImpl& P, const muon_param_ptrs* ptrs, const muon_hparams& hp, hipStream_t s);
 // Writes `bytes` (a multiple of 4) from host memory src to device memory dst
 // (4-byte aligned) through the arguments of ceil(bytes / 3 KiB) small kernel
 // launches on s; src may be reused as soon as the call returns.

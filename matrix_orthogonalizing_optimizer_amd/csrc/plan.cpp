@@ -127,13 +127,18 @@ muon_status build_plan(const muon_param_shape* table, int32_t n, const muon_plan
   std::vector<PlanUnit> order;  // table order
   for (int32_t p = 0; p < n; ++p) {
     const muon_param_shape& s = table[p];
-    if (s.kind != MUON_KIND_MUON && s.kind != MUON_KIND_ADAMW) return MUON_E_ARG;
+    if (s.kind != MUON_KIND_MUON && s.kind != MUON_KIND_ADAMW && s.kind != MUON_KIND_ADAMW8) return MUON_E_ARG;
     if (s.dtype != MUON_F32 && s.dtype != MUON_BF16) return MUON_E_DTYPE;
     if (s.rows < 0 || s.cols < 0 || s.split_rows < 0 || s.scale_dim < 0) return MUON_E_SHAPE;
     if (s.rows > kMaxDim || s.cols > kMaxDim) return MUON_E_SHAPE;
     if (s.kind == MUON_KIND_ADAMW) {
       if (s.split_rows != 0) return MUON_E_SHAPE;
       P.adam.push_back(p);
+      continue;
+    }
+    if (s.kind == MUON_KIND_ADAMW8) {
+      if (s.split_rows != 0 || s.rows * s.cols > ADAMW8_MAX_NUMEL) return MUON_E_SHAPE;
+      P.adam8.push_back(p);
       continue;
     }
     if (s.split_rows > 0 && s.rows % s.split_rows != 0) return MUON_E_SHAPE;

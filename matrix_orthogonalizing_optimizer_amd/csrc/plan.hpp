@@ -40,7 +40,8 @@ struct PlanImpl {
   muon_plan_options opts{};
   std::vector<PlanUnit> units;  // bucket order
   std::vector<PlanBucket> buckets;
-  std::vector<int32_t> adam;    // table indices of AdamW parameters
+  std::vector<int32_t> adam;    // table indices of AdamW parameters with fp32 moments
+  std::vector<int32_t> adam8;   // of those with 8-bit moments
   int32_t max_chunk = 0;
   int64_t max_partials = 0;
   size_t max_data = 0;

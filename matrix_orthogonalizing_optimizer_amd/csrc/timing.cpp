@@ -14,7 +14,7 @@ namespace {
 
 const char* kNames[F_COUNT] = {"momentum_norm", "norm_finalize", "ns_gram_A", "ns_poly_P",
                                "ns_update_PX", "ns_final_update", "gram_r0", "gram_p",
-                               "gram_q", "gram_t", "gram_r", "adamw", "rows8",
+                               "gram_q", "gram_t", "gram_r", "adamw", "adamw8", "rows8",
                                "norm_forward", "norm_backward", "linear8_forward", "linear8_weight_grad",
                                "linear8_input_grad"};
 

@@ -19,6 +19,7 @@ enum Family : int {
   F_GRAM_T,    // T = P R
   F_GRAM_R,    // R <- T P
   F_ADAMW,
+  F_ADAMW8,    // the step on 8-bit moments, and their conversions
   F_ROWS8,     // quantize / restore 8-bit rows
   F_NORM_FWD,  // layer / RMS norm forward
   F_NORM_BWD,  // its gradients, with the join of the vector gradients
