@@ -545,6 +545,56 @@ muon_status muon_linear8_input_grad(const void* dy, int64_t lddy, int32_t dy_dty
 muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t out, int64_t in, const void* dy,
                                          int64_t lddy, int32_t dy_dtype, size_t* bytes);
 
+/* Matrix products grouped by expert: rows offsets[e] .. offsets[e+1]-1 of x, y,
+ * dy and dx belong to expert e, whose weight W[e] is out x in at
+ * w + e * stride (elements), rows ldw apart:
+ *   muon_experts_forward      y[r]  = x[r] W[e]^T                  rows x out
+ *   muon_experts_input_grad   dx[r] = dy[r] W[e]                   rows x in
+ *   muon_experts_weight_grad  dW[e] = sum over e's rows r of dy[r]^T x[r]
+ * dW is laid out like W: with stride = out * lddw, lddw = in it is the gradient
+ * of a Muon parameter of experts * out rows, split_rows = out, as muon_step
+ * reads it.  dW is written, or added to when accumulate is nonzero; an expert
+ * without rows gets zero (or what it had).
+ * offsets: device memory, experts + 1 int32, 0 <= offsets[0] <= ... <=
+ * offsets[experts] <= rows; read when the work runs, so a router on the device
+ * may have written them just before on the same stream.  Rows before
+ * offsets[0] and from offsets[experts] on belong to nobody: they are not read, and
+ * y and dx are left as they were there.  Offsets outside 0 .. rows are taken as
+ * the nearest of these; where they decrease, the results are unspecified, but
+ * nothing outside the buffers is read or written.
+ * dtype: of both operands; the results have their own.  bf16 products are
+ * exact and summed in fp32; fp32 is multiplied and summed in fp32.
+ * With in == 0 y is zero, with out == 0 dx is zero, with rows == 0 dW is zero
+ * (or what it had).
+ * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, experts
+ * above 2^16, a leading dimension below its column count or above 2^21, a
+ * stride whose experts overlap or above 2^42, a result of more than 2^22
+ * tiles of 128 x 128 or 256 x 256); MUON_E_ARG (a pointer null or not aligned
+ * to its element); MUON_E_WORKSPACE (smaller than
+ * muon_experts_workspace_bytes); MUON_E_HIP. */
+typedef enum {
+  MUON_EXPERTS_FORWARD = 0,
+  MUON_EXPERTS_WEIGHT_GRAD = 1,
+  MUON_EXPERTS_INPUT_GRAD = 2
+} muon_experts_pass;
+muon_status muon_experts_forward(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t stride,
+                                 const int32_t* offsets, int64_t rows, int64_t experts, int64_t out, int64_t in,
+                                 int32_t dtype, void* y, int64_t ldy, int32_t y_dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+muon_status muon_experts_input_grad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t stride,
+                                    const int32_t* offsets, int64_t rows, int64_t experts, int64_t out, int64_t in,
+                                    int32_t dtype, void* dx, int64_t lddx, int32_t dx_dtype, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+muon_status muon_experts_weight_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, const int32_t* offsets,
+                                     int64_t rows, int64_t experts, int64_t out, int64_t in, int32_t dtype, void* dw,
+                                     int64_t lddw, int64_t stride, int32_t dw_dtype, int32_t accumulate,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace of one pass (muon_experts_pass), host only; 0 for products
+ * that fill the GPU by themselves.  Errors: MUON_E_METHOD (unknown pass),
+ * MUON_E_DTYPE, MUON_E_SHAPE, MUON_E_ARG. */
+muon_status muon_experts_workspace_bytes(int32_t pass, int64_t rows, int64_t experts, int64_t out, int64_t in,
+                                         int32_t dtype, size_t* bytes);
+
 /* Static text for a status code. */
 const char* muon_status_string(int32_t status);
 

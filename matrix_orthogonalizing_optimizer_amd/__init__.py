@@ -9,7 +9,8 @@ from ._lib import (EXPORTED, MUON_BF16, MUON_COEFF_HYBRID, MUON_COEFF_QUINTIC,  
                    muon_linear8_weight_grad, muon_linear8_workspace_bytes, muon_norm_backward,
                    muon_norm_backward_workspace_bytes, muon_norm_forward, muon_rows8_dequantize, muon_rows8_quantize,
                    MUON_SCALE_MOONLIGHT, MUON_SCALE_SPECTRAL, MUON_SCALE_UNIT_RMS, MuonError, Plan,
-                   lib, make_hparams, muon_adamw8_pack, muon_adamw8_state_bytes, muon_adamw8_unpack, muon_ns_coefficients, muon_probe_copy, muon_probe_copy_lds, muon_probe_mfma,
+                   lib, make_hparams, MUON_EXPERTS_FORWARD, MUON_EXPERTS_INPUT_GRAD, MUON_EXPERTS_WEIGHT_GRAD,
+                   muon_experts_forward, muon_experts_input_grad, muon_experts_weight_grad, muon_experts_workspace_bytes, muon_adamw8_pack, muon_adamw8_state_bytes, muon_adamw8_unpack, muon_ns_coefficients, muon_probe_copy, muon_probe_copy_lds, muon_probe_mfma,
                    muon_plan_buckets, muon_plan_create, muon_plan_units, muon_plan_workspace_bytes,
                    muon_status_string, muon_step, muon_timing_collect, muon_timing_enable,
                    muon_version, ns_orthogonalize, ns_orthogonalize_noalloc,

@@ -26,6 +26,7 @@ MUON_SCALE_MOONLIGHT, MUON_SCALE_SPECTRAL, MUON_SCALE_UNIT_RMS = 0, 1, 2
 MUON_COEFF_QUINTIC, MUON_COEFF_HYBRID = 0, 1
 MUON_NORM_LAYER, MUON_NORM_RMS = 0, 1
 MUON_LINEAR8_FORWARD, MUON_LINEAR8_WEIGHT_GRAD, MUON_LINEAR8_INPUT_GRAD = 0, 1, 2
+MUON_EXPERTS_FORWARD, MUON_EXPERTS_WEIGHT_GRAD, MUON_EXPERTS_INPUT_GRAD = 0, 1, 2
 
 EXPORTED = ["muon_plan_create", "muon_plan_destroy", "muon_plan_workspace_bytes",
             "muon_plan_buckets", "muon_plan_units", "muon_step", "ns_orthogonalize",
@@ -35,7 +36,9 @@ EXPORTED = ["muon_plan_create", "muon_plan_destroy", "muon_plan_workspace_bytes"
             "muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
             "muon_norm_backward_workspace_bytes", "muon_linear8_forward", "muon_linear8_weight_grad",
             "muon_linear8_input_grad", "muon_linear8_workspace_bytes",
-            "muon_adamw8_state_bytes", "muon_adamw8_pack", "muon_adamw8_unpack"]
+            "muon_adamw8_state_bytes", "muon_adamw8_pack", "muon_adamw8_unpack",
+            "muon_experts_forward", "muon_experts_weight_grad", "muon_experts_input_grad",
+            "muon_experts_workspace_bytes"]
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -134,7 +137,13 @@ def lib():
     L.muon_adamw8_state_bytes.argtypes = [i64, ctypes.POINTER(sz)]
     L.muon_adamw8_pack.argtypes = [vp, i64, i32, i64, vp, vp]
     L.muon_adamw8_unpack.argtypes = [vp, i64, i32, vp, vp]
-    for n in ("muon_adamw8_state_bytes", "muon_adamw8_pack", "muon_adamw8_unpack", "muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
+    L.muon_experts_forward.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp, sz, vp]
+    L.muon_experts_input_grad.argtypes = L.muon_experts_forward.argtypes
+    L.muon_experts_weight_grad.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp, i64, i64, i32, i32, vp, sz,
+                                           vp]
+    L.muon_experts_workspace_bytes.argtypes = [i32, i64, i64, i64, i64, i32, ctypes.POINTER(sz)]
+    for n in ("muon_experts_forward", "muon_experts_weight_grad", "muon_experts_input_grad",
+              "muon_experts_workspace_bytes", "muon_adamw8_state_bytes", "muon_adamw8_pack", "muon_adamw8_unpack", "muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
               "muon_norm_backward_workspace_bytes", "muon_linear8_forward", "muon_linear8_weight_grad",
               "muon_linear8_input_grad", "muon_linear8_workspace_bytes"):
         getattr(L, n).restype = i32
@@ -912,3 +921,118 @@ def muon_adamw8_unpack(state, out, moment=MUON_ADAMW8_FIRST, stream=None):
     _check_moment8("state", state, out.numel())
     _launch("muon_adamw8_unpack", di, stream, state.data_ptr(), out.numel(), moment, out.data_ptr())
     return out
+
+
+# ---------------------------------------------------------------------------
+# Matrix products grouped by expert
+
+def _expert_weights(name, t, experts):
+    """(out, in, ld, stride, dtype code) of the weights of all experts: experts x
+    out x in, or (experts * out) x in as a Muon parameter holds them."""
+    if t.dim() == 2:
+        rows, in_, ld, dt = _matrix(name, t)
+        if experts == 0 or rows % experts:
+            raise ValueError(f"{name}: {rows} rows for {experts} experts")
+        return rows // experts, in_, ld, rows // experts * ld, dt
+    if t.dim() != 3 or t.shape[0] != experts:
+        raise ValueError(f"{name}: expected {experts} x out x in, got {tuple(t.shape)}")
+    _, out, in_ = t.shape
+    stride, ld, unit = t.stride()
+    if unit != 1 and in_ > 1 and t.numel():
+        raise ValueError(f"{name}: columns must be contiguous")
+    if out <= 1:
+        ld = in_
+    elif ld < in_:
+        raise ValueError(f"{name}: rows overlap (stride {ld} for {in_} columns)")
+    if experts <= 1 or t.numel() == 0:
+        stride = out * ld
+    elif stride < (out - 1) * ld + in_:
+        raise ValueError(f"{name}: experts overlap (stride {stride} for {out} rows)")
+    return out, in_, ld, stride, _dtype_code(name, t)
+
+
+def _offsets(t):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() < 1 or not t.is_contiguous():
+        raise ValueError(f"offsets: expected a contiguous int32 vector of experts + 1, got {t.dtype} {tuple(t.shape)}")
+    return t.numel() - 1
+
+
+def muon_experts_workspace_bytes(kind: int, rows: int, experts: int, out: int, in_: int, dtype: int) -> int:
+    """Workspace of one pass (MUON_EXPERTS_FORWARD, _WEIGHT_GRAD, _INPUT_GRAD) on
+    operands of dtype MUON_BF16 or MUON_F32."""
+    b = ctypes.c_size_t()
+    _check("muon_experts_workspace_bytes",
+           lib().muon_experts_workspace_bytes(kind, rows, experts, out, in_, dtype, ctypes.byref(b)))
+    return b.value
+
+
+def muon_experts_forward(x, w, offsets, y=None, dtype=None, workspace=None, stream=None):
+    """y[r] = x[r] W[e]^T for the rows r = offsets[e] .. offsets[e + 1] - 1 of every
+    expert e.  x: rows x in; w: experts x out x in, or (experts * out) x in;
+    offsets: experts + 1 int32 on the device.  y: rows x out (None: allocated, of
+    ``dtype``, default x's); rows that belong to no expert are not written;
+    returned."""
+    experts = _offsets(offsets)
+    rows, in_, ldx, dt = _matrix("x", x)
+    out, win, ldw, stride, wdt = _expert_weights("w", w, experts)
+    if win != in_ or wdt != dt:
+        raise ValueError(f"w: expected {in_} columns of {x.dtype}, got {win} of {w.dtype}")
+    di = _call_device(stream, "x w offsets y workspace", x, w, offsets, y, workspace)
+    if y is None:
+        y = _empty(di, stream, rows, out, dtype=dtype or x.dtype)
+    r, c, ldy, ydt = _matrix("y", y)
+    if (r, c) != (rows, out):
+        raise ValueError(f"y: expected {(rows, out)}, got {(r, c)}")
+    nb = 0 if workspace is not None else muon_experts_workspace_bytes(MUON_EXPERTS_FORWARD, rows, experts, out, in_, dt)
+    workspace, wp, wsz = _scratch(di, stream, workspace, nb)
+    _launch("muon_experts_forward", di, stream, x.data_ptr(), ldx, w.data_ptr(), ldw, stride, offsets.data_ptr(), rows,
+            experts, out, in_, dt, y.data_ptr(), ldy, ydt, wp, wsz)
+    return y
+
+
+def muon_experts_input_grad(dy, w, offsets, dx=None, dtype=None, workspace=None, stream=None):
+    """dx[r] = dy[r] W[e]: the gradient of muon_experts_forward's x.  dx: rows x
+    in (None: allocated, of ``dtype``, default dy's); rows that belong to no
+    expert are not written; returned."""
+    experts = _offsets(offsets)
+    rows, out, lddy, dt = _matrix("dy", dy)
+    wout, in_, ldw, stride, wdt = _expert_weights("w", w, experts)
+    if wout != out or wdt != dt:
+        raise ValueError(f"w: expected {out} rows an expert of {dy.dtype}, got {wout} of {w.dtype}")
+    di = _call_device(stream, "dy w offsets dx workspace", dy, w, offsets, dx, workspace)
+    if dx is None:
+        dx = _empty(di, stream, rows, in_, dtype=dtype or dy.dtype)
+    r, c, lddx, xdt = _matrix("dx", dx)
+    if (r, c) != (rows, in_):
+        raise ValueError(f"dx: expected {(rows, in_)}, got {(r, c)}")
+    nb = 0 if workspace is not None else muon_experts_workspace_bytes(MUON_EXPERTS_INPUT_GRAD, rows, experts, out, in_, dt)
+    workspace, wp, wsz = _scratch(di, stream, workspace, nb)
+    _launch("muon_experts_input_grad", di, stream, dy.data_ptr(), lddy, w.data_ptr(), ldw, stride, offsets.data_ptr(),
+            rows, experts, out, in_, dt, dx.data_ptr(), lddx, xdt, wp, wsz)
+    return dx
+
+
+def muon_experts_weight_grad(dy, x, offsets, dw=None, dtype=None, accumulate=False, workspace=None, stream=None):
+    """dW[e] = sum over the rows r of expert e of dy[r]^T x[r]: the gradient that
+    muon_step reads for a parameter of experts * out rows with split_rows = out.
+    dw: experts x out x in, or (experts * out) x in, written, or added to with
+    accumulate (None: allocated, of ``dtype``, default dy's); returned."""
+    experts = _offsets(offsets)
+    rows, out, lddy, dt = _matrix("dy", dy)
+    xr, in_, ldx, xdt = _matrix("x", x)
+    if xr != rows or xdt != dt:
+        raise ValueError(f"x: expected {rows} rows of {dy.dtype}, got {xr} of {x.dtype}")
+    di = _call_device(stream, "dy x offsets dw workspace", dy, x, offsets, dw, workspace)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw")
+        dw = _empty(di, stream, experts, out, in_, dtype=dtype or dy.dtype)
+    wout, win, lddw, stride, wdt = _expert_weights("dw", dw, experts)
+    if (wout, win) != (out, in_):
+        raise ValueError(f"dw: expected {experts} x {out} x {in_}, got {tuple(dw.shape)}")
+    nb = 0 if workspace is not None else muon_experts_workspace_bytes(MUON_EXPERTS_WEIGHT_GRAD, rows, experts, out, in_, dt)
+    workspace, wp, wsz = _scratch(di, stream, workspace, nb)
+    _launch("muon_experts_weight_grad", di, stream, dy.data_ptr(), lddy, x.data_ptr(), ldx, offsets.data_ptr(), rows,
+            experts, out, in_, dt, dw.data_ptr(), lddw, stride, wdt, 1 if accumulate else 0, wp, wsz)
+    return dw

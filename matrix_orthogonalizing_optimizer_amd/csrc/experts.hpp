@@ -1,0 +1,541 @@
+// Matrix products grouped by expert, gfx950.  Rows offsets[e] .. offsets[e+1]-1
+// belong to expert e:
+//   EX_Y   y[r]  = x[r] W[e]^T
+//   EX_DX  dx[r] = dy[r] W[e]
+//   EX_DW  dW[e] = sum over the rows r of e of dy[r]^T x[r]
+// Written below as C (M x N) = sum over K of A B, sums in fp32.
+//
+// The offsets lie on the device, so the host does not know how many rows an
+// expert has.  EX_Y and EX_DX launch as many workgroups as any offsets can
+// need (rows / T + experts tile rows); each finds its tile from a prefix sum
+// over the experts' tile rows (experts_tile), and those past the last tile
+// end at once.  EX_DW has experts x tiles workgroups whose K is the expert's
+// number of rows.  Offsets are clamped to 0 .. rows, so no value of theirs
+// leads outside the operands.
+//
+// A workgroup of 8 waves owns a T x T tile of C (T = 256: 128 x 64 outputs per
+// wave, one workgroup per CU; T = 128: 64 x 32 per wave, two) and walks K in
+// stages of 128 bytes per row: 64 values of bf16, 32 of fp32.  Two stages live
+// in LDS.  v_mfma_f32_32x32x16_bf16, or v_mfma_f32_32x32x2_f32.
+//
+// An operand lies row-major (K contiguous: x and w of EX_Y, dy of EX_DX) or
+// K-major (w of EX_DX, both of EX_DW).  K-major bf16 fragments come out of LDS
+// transposed (ds_read_b64_tr_b16), fp32 ones element by element.
+//
+// DIRECT: bf16 rows of whole 16-byte pieces are copied global -> LDS without a
+// register round trip.  Otherwise (odd widths, any alignment, fp32) the pieces go
+// through registers, and what reaches past a row's end becomes zero there.
+//
+// splits > 1: the parts of a tile's K go to workgroups of their own, which leave
+// partial tiles in the workspace; experts_join_kernel adds those in order.
+#pragma once
+
+#include "device_common.hpp"
+#include "gemm.hpp"
+#include "kernel_args.hpp"
+#include "row_ops.hpp"
+
+namespace muon {
+
+enum : int { EX_Y = 0, EX_DW = 1, EX_DX = 2 };
+
+// First row of expert e and their number.
+struct ExpertRows {
+  int begin, count;
+};
+__device__ __forceinline__ ExpertRows experts_rows(const ExpertsArgs& a, int e) {
+  const auto* off = as_global(a.offsets);
+  const int b = min(max(off[e], 0), a.rows);
+  return {b, min(max(off[e + 1], b), a.rows) - b};
+}
+
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_prefix(int v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(v, d, 64);
+    if ((int)(threadIdx.x & 63) >= d) v += up;
+  }
+  return v;
+}
+
+// A tile of C: its expert and that one's rows, tile row and column within it.
+struct ExpertTile {
+  int expert, begin, count, bi, bj;
+  int index;  // number of the tile
+  int split;  // part of its K
+};
+
+// Workgroups are spread over the XCDs in chunks of S consecutive pieces of
+// work, as the optimizer's products are (gemm.hpp): a bijection of [0, tot).
+__device__ __forceinline__ int experts_deal(int b, int tot, int S) {
+  const int xcd = b & 7, loc = b >> 3;
+  const int full = tot / (8 * S);
+  if (loc < full * S) return (loc / S) * 8 * S + xcd * S + loc % S;
+  const int rest = tot - full * 8 * S, q = rest >> 3, r = rest & 7;
+  return full * 8 * S + xcd * q + (xcd < r ? xcd : r) + (loc - full * S);
+}
+
+// Tile number -> tile row and column: groups of 4 tile rows, column by column.
+__device__ __forceinline__ void experts_place(int w, int tilesM, int tilesN, int& bi, int& bj) {
+  constexpr int GROUP = 4;
+  const int g = w / (GROUP * tilesN);
+  const int first = g * GROUP;
+  const int gm = min(tilesM - first, GROUP);
+  const int in = w - g * GROUP * tilesN;
+  bi = first + in % gm;
+  bj = in / gm;
+}
+
+// The tile of workgroup b; false if there is none.  JOIN: workgroups count tiles
+// alone, in order.
+template <int MODE, int T, bool JOIN> __device__ __forceinline__ bool experts_tile(const ExpertsArgs& a, int b, ExpertTile& t) {
+  const int lane = threadIdx.x & 63;
+  const int splits = JOIN ? 1 : a.splits;
+  int tot, w, pre = 0, mine = 0, before = 0;
+  if constexpr (MODE == EX_DW) {
+    tot = a.experts * a.tilesM * a.tilesN;
+  } else {
+    int64_t sum = 0;
+    for (int c = 0; c < a.experts; c += 64) {
+      const int n = c + lane < a.experts ? experts_rows(a, c + lane).count : 0;
+      mine = (n + T - 1) / T;
+      pre = wave_prefix(mine);
+      sum += __builtin_amdgcn_readlane(pre, 63);
+    }
+    // more tile rows than the rows allow: the offsets go back, and the groups overlap
+    if (sum > a.rows / T + min(a.experts, a.rows)) return false;
+    tot = (int)sum * a.tilesN;
+  }
+  if (b >= tot * splits) return false;
+  w = JOIN ? b : experts_deal(b, tot * splits, 8 * a.tilesN);
+  t.split = __builtin_amdgcn_readfirstlane(w / tot);
+  w = __builtin_amdgcn_readfirstlane(w % tot);
+  t.index = w;
+  int tilesM;
+  if constexpr (MODE == EX_DW) {
+    const int per = a.tilesM * a.tilesN;
+    t.expert = w / per;
+    w -= t.expert * per;
+    tilesM = a.tilesM;
+  } else {
+    t.expert = 0;
+    const int at = w / a.tilesN;  // tile row, counted over all experts
+    for (int c = 0; c < a.experts; c += 64) {
+      if (a.experts > 64) {  // otherwise they are still there
+        const int n = c + lane < a.experts ? experts_rows(a, c + lane).count : 0;
+        mine = (n + T - 1) / T;
+        pre = wave_prefix(mine);
+      }
+      const uint64_t past = __ballot(before + pre > at);
+      if (past) {
+        const int l = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
+        t.expert = c + l;
+        tilesM = __builtin_amdgcn_readlane(mine, l);
+        before += __builtin_amdgcn_readlane(pre, l) - tilesM;
+        break;
+      }
+      before += __builtin_amdgcn_readlane(pre, 63);
+    }
+    w -= before * a.tilesN;
+  }
+  experts_place(w, tilesM, a.tilesN, t.bi, t.bj);
+  t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+  t.bi = __builtin_amdgcn_readfirstlane(t.bi);
+  t.bj = __builtin_amdgcn_readfirstlane(t.bj);
+  const ExpertRows r = experts_rows(a, t.expert);
+  t.begin = __builtin_amdgcn_readfirstlane(r.begin);
+  t.count = __builtin_amdgcn_readfirstlane(r.count);
+  return true;
+}
+
+// Stages of K of a part of a tile: [ks0, ks1).
+template <int MODE, int BK> __device__ __forceinline__ void experts_stages(const ExpertsArgs& a, const ExpertTile& t, int& ks0, int& ks1) {
+  const int K = MODE == EX_DW ? t.count : a.K;
+  const int nks = (K + BK - 1) / BK;
+  const int per = (nks + a.splits - 1) / a.splits;
+  ks0 = __builtin_amdgcn_readfirstlane(min(t.split * per, nks));
+  ks1 = __builtin_amdgcn_readfirstlane(min(ks0 + per, nks));
+}
+
+// A 16-byte piece of a row at column c, through registers.  load() takes the
+// row's last piece where c reaches past its end, settle() moves its own
+// elements to the front and clears the others (all of them where !ok), so no
+// branch stands behind the load.  Rows shorter than a piece are loaded element by
+// element.
+template <typename T> struct Piece {
+  static constexpr int PER = 16 / sizeof(T);
+  u32x4 w;
+  __device__ __forceinline__ void load(const T* row, int c, int cols) {
+    if (cols >= PER) {
+      const T* p = row + min(c, cols - PER);
+      if constexpr (sizeof(T) == 2) w = as_global(reinterpret_cast<const u32x4_e2*>(p))->v;
+      else w = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(p))->v);
+    } else {
+      w = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < PER - 1; ++e)
+        if (c + e < cols) {
+          if constexpr (sizeof(T) == 2) w[e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(row))[c + e] << (16 * (e & 1));
+          else w[e] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
+        }
+    }
+  }
+  __device__ __forceinline__ void settle(int c, int cols, bool ok) {
+    const int over = cols >= PER ? max(c + PER - cols, 0) : 0;
+    const int off = ok ? min(over, PER) : PER;  // elements to drop at the front
+    if (__ballot(off != 0) == 0) return;
+    const int regs = off * (int)sizeof(T) / 4;
+#pragma unroll
+    for (int b = 4; b >= 1; b >>= 1) {
+      const bool take = (regs & b) != 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t from = j + b < 4 ? w[j + b] : 0u;
+        w[j] = take ? from : w[j];
+      }
+    }
+    if constexpr (sizeof(T) == 2) {
+      const bool take = (off & 1) != 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t from = (w[j] >> 16) | (j + 1 < 4 ? w[j + 1] << 16 : 0u);
+        w[j] = take ? from : w[j];
+      }
+    }
+  }
+};
+
+template <int MODE, int T, bool DIRECT, typename TI, typename TO>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(T == 128 ? 4 : 2, T == 128 ? 4 : 2)))
+void experts_kernel(const ExpertsArgs a) {
+  constexpr int NW = 8;
+  constexpr bool AKM = MODE == EX_DW;      // A lies K-major
+  constexpr bool BKM = MODE != EX_Y;       // B lies K-major
+  constexpr int ES = (int)sizeof(TI);
+  constexpr int EPC = 16 / ES;             // elements per 16-byte chunk
+  constexpr int BK = 8 * EPC;              // K per stage
+  constexpr int WGN = NW / 2;              // waves: 2 along M, NW / 2 along N
+  constexpr int WTM = T / 64, WN = T / WGN, WTN = WN / 32;
+  constexpr int OPS = T * 8;               // chunks of one operand's stage
+  constexpr int STG = 2 * OPS;
+  constexpr int NQ = OPS / (64 * NW);      // 16-byte pieces of one operand a thread moves per stage
+  constexpr int NDR = WTM + WTN, NPAIR = WTM * WTN;
+  constexpr int RPP = (NDR + NPAIR - 1) / NPAIR;  // fragment reads issued per MFMA
+  constexpr int CR = T * ES / 16;          // chunks per K-row of a K-major stage
+  constexpr int RPC = 64 / CR;             // K-rows per wave-wide copy
+  static_assert(!DIRECT || ES == 2, "direct copies are bf16");
+  static_assert(RPC >= 1 && BK * CR == OPS, "K-major stage");
+  __shared__ u32x4 ring[2][STG];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wid / WGN, wn = wid % WGN;
+  const int half = lane >> 5, l32 = lane & 31;
+  ExpertTile t;
+  if (!experts_tile<MODE, T, false>(a, blockIdx.x, t)) return;
+  const int row0 = t.bi * T, col0 = t.bj * T;
+  int ks0, ks1;
+  experts_stages<MODE, BK>(a, t, ks0, ks1);
+  const int nst = ks1 - ks0;
+  const int M = MODE == EX_DW ? a.M : t.count;  // rows of C
+  const int K = MODE == EX_DW ? t.count : a.K;
+  const TI* A = static_cast<const TI*>(a.A) + (int64_t)t.begin * a.lda;
+  const TI* B = static_cast<const TI*>(a.B) + (MODE == EX_DW ? (int64_t)t.begin * a.ldb : (int64_t)t.expert * a.se);
+
+  // K-major chunk swizzle, see gemm.hpp
+  auto swz_t = [](int krow) {
+    return ES == 2 ? (((krow & 1) << 2) ^ (((krow >> 1) & 1) * 10)) : ((krow >> 2) & 1) << 3;
+  };
+  // the clamp compiles to a vector instruction: back to a scalar register, or
+  // the loads' buffer resources count as divergent
+  auto stage_rows = [&](int ks) { return __builtin_amdgcn_readfirstlane(max(0, min(BK, K - ks * BK))); };
+
+  // Chunk q of a thread: row-major, tile row crow + 8 q at k ck[q & 1] of the
+  // stage; K-major, K-row (wid NQ + q) RPC + lane / CR at column 8 ((lane % CR) ^ swz).
+  const int rows_a = min(T, M - row0), rows_b = min(T, a.N - col0);
+  const int crow = wid * (8 * NQ) + (lane >> 3);
+  const int ck[2] = {((lane & 7) ^ (lane >> 3)) * EPC, ((lane & 7) ^ (lane >> 3) ^ 1) * EPC};
+  auto km_row = [&](int q) { return (wid * NQ + q) * RPC + lane / CR; };
+  auto km_col = [&](int q) { return ((lane % CR) ^ swz_t(km_row(q))) * EPC; };
+
+  // ---- direct copies
+  auto km_offset = [&](int par, int64_t ld, int c0, int cols) {
+    const int col = c0 + km_col(par);
+    return col < cols ? (uint32_t)(((int64_t)km_row(par) * ld + col) * ES) : OOB;
+  };
+  const uint32_t ta[2] = {km_offset(0, a.lda, row0, M), km_offset(1, a.lda, row0, M)};
+  const uint32_t tb[2] = {km_offset(0, a.ldb, col0, a.N), km_offset(1, a.ldb, col0, a.N)};
+  const TI* Arow = A + (AKM ? 0 : (int64_t)row0 * a.lda);
+  const TI* Brow = B + (BKM ? 0 : (int64_t)col0 * a.ldb);
+  auto copy_row_major = [&](const TI* base, int64_t ld, int rows, int region, int q, int v, int ks) {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(base, (uint32_t)((((int64_t)rows - 1) * ld + K) * ES));
+    const int k = ks * BK + ck[q & 1];
+    const uint32_t off = k < K ? (uint32_t)(((crow + 8 * q) * ld + k) * ES) : OOB;
+    copy16_to_lds(r, &ring[v & 1][region + (wid * NQ + q) * 64], off);
+  };
+  auto copy_k_major = [&](const TI* base, int64_t ld, int cols, const uint32_t(&o)[2], int region, int q, int v, int ks) {
+    const int nk = stage_rows(ks);
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(base + (int64_t)ks * BK * ld, nk ? (uint32_t)((((int64_t)nk - 1) * ld + cols) * ES) : 0u);
+    copy16_to_lds(r, &ring[v & 1][region + (wid * NQ + q) * 64],
+                  o[q & 1] + (uint32_t)((int64_t)((q & ~1) * RPC) * ld * ES));
+  };
+  auto copy_a = [&](int q, int v, int ks) {
+    if constexpr (AKM) copy_k_major(A, a.lda, M, ta, 0, q, v, ks);
+    else copy_row_major(Arow, a.lda, rows_a, 0, q, v, ks);
+  };
+  auto copy_b = [&](int q, int v, int ks) {
+    if constexpr (BKM) copy_k_major(B, a.ldb, a.N, tb, OPS, q, v, ks);
+    else copy_row_major(Brow, a.ldb, rows_b, OPS, q, v, ks);
+  };
+
+  // ---- the same chunks through registers
+  Piece<TI> pa[DIRECT ? 1 : NQ], pb[DIRECT ? 1 : NQ];
+  auto load_pieces = [&](int ks) {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        // rows past the end: a row that is there, cleared by settle()
+        if constexpr (AKM) pa[q].load(A + (int64_t)min(ks * BK + km_row(q), K - 1) * a.lda, row0 + km_col(q), M);
+        else pa[q].load(Arow + (int64_t)min(crow + 8 * q, rows_a - 1) * a.lda, ks * BK + ck[q & 1], K);
+        if constexpr (BKM) pb[q].load(B + (int64_t)min(ks * BK + km_row(q), K - 1) * a.ldb, col0 + km_col(q), a.N);
+        else pb[q].load(Brow + (int64_t)min(crow + 8 * q, rows_b - 1) * a.ldb, ks * BK + ck[q & 1], K);
+      }
+    }
+  };
+  auto write_pieces = [&](int q, int v, int ks) {  // q < NQ: A, else B
+    if constexpr (!DIRECT) {
+      const int i = q < NQ ? q : q - NQ;
+      Piece<TI>& p = q < NQ ? pa[i] : pb[i];
+      if (q < NQ ? AKM : BKM)
+        p.settle((q < NQ ? row0 : col0) + km_col(i), q < NQ ? M : a.N, ks * BK + km_row(i) < K);
+      else
+        p.settle(ks * BK + ck[i & 1], K, crow + 8 * i < (q < NQ ? rows_a : rows_b));
+      ring[v & 1][(q < NQ ? 0 : OPS) + (wid * NQ + i) * 64 + lane] = p.w;
+    }
+  };
+
+  f32x16 acc[WTM][WTN];
+#pragma unroll
+  for (int i = 0; i < WTM; ++i)
+#pragma unroll
+    for (int j = 0; j < WTN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  // ---- fragments, double buffered by k-step
+  u32x4 fa[2][WTM], fb[2][WTN];
+  const int rswz = (l32 & 7) ^ ((l32 >> 3) & 1);
+  constexpr int ROWB = CR * 16;
+  uint32_t tbase[NDR];
+#pragma unroll
+  for (int r = 0; r < NDR; ++r) {
+    const int e = (lane >> 2) & 3, q = lane & 3;
+    const int region = r < WTM ? 0 : OPS;
+    const int rb = r < WTM ? wm * (T / 2) + r * 32 : wn * WN + (r - WTM) * 32;
+    const int col = rb + 16 * ((lane >> 4) & 1) + 4 * q;
+    tbase[r] = (uint32_t)(uintptr_t)(lds_ptr_t)&ring[0][0] +
+               (uint32_t)(region * 16 + (8 * half + e) * ROWB + ((col >> 3) ^ swz_t(e)) * 16 + (col & 7) * 2);
+  }
+  auto read_one = [&](int r, int v, int s, int slot) {
+    const bool isA = r < WTM;
+    const int rb = isA ? wm * (T / 2) + r * 32 : wn * WN + (r - WTM) * 32;
+    const u32x4* st = &ring[v & 1][isA ? 0 : OPS];
+    u32x4 f;
+    if (!(isA ? AKM : BKM)) {
+      f = st[(rb + l32) * 8 + ((2 * s + half) ^ rswz)];
+    } else if constexpr (ES == 2) {
+      const uint32_t p = tbase[r] + (uint32_t)((v & 1) * STG * 16);
+#pragma unroll
+      for (int kq = 0; kq < 2; ++kq) {
+        const uint2 w = lds_read_tr16_step<ROWB>(p, 2 * s + kq);
+        f[2 * kq] = w.x;
+        f[2 * kq + 1] = w.y;
+      }
+    } else {
+      // 4 consecutive k of one column
+      const int c = rb + l32;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 8 * s + 4 * half + e;
+        f[e] = reinterpret_cast<const uint32_t*>(st)[(k * CR + ((c >> 2) ^ swz_t(k))) * 4 + (c & 3)];
+      }
+    }
+    if (isA) fa[slot][r] = f;
+    else fb[slot][r - WTM] = f;
+  };
+  // reads in the order of first use: A0, B0 .. B(WTN-1), A1 .. A(WTM-1)
+  auto ro = [](int p) { return p == 0 ? 0 : (p <= WTN ? WTM + p - 1 : p - WTN); };
+  // The compiler does not track the transposed reads.  LDS instructions of a
+  // wave complete in order, so before MFMA p it is enough that at most as
+  // many are outstanding as were issued after the fragment that p is the
+  // first to use: this step's later fragments and the next step's first p
+  // ones (two instructions each; untransposed reads and register writes are
+  // not counted, which only waits for more).
+  auto wait_frag = [&](auto pc) {
+    if constexpr (ES == 2 && BKM) {
+      constexpr int p = decltype(pc)::value;
+      constexpr int i = p / WTN, j = p % WTN;
+      constexpr bool needA = j == 0 && AKM, needB = i == 0;  // first uses among the transposed
+      if constexpr (needA || needB) {
+        // position of that fragment in the reading order
+        constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : WTN + i);
+        constexpr int later_a = AKM ? (WTM - 1 - (at > WTN ? at - WTN : 0)) : 0;
+        constexpr int later_b = at <= WTN ? WTN - at : 0;
+        constexpr int now = p * RPP < NDR ? p * RPP : NDR;  // reads issued so far in this step
+        constexpr int now_a = AKM ? (now > 0 ? 1 : 0) + (now > WTN + 1 ? now - WTN - 1 : 0) : 0;
+        constexpr int now_b = now <= 1 ? 0 : (now - 1 < WTN ? now - 1 : WTN);
+        constexpr int n = 2 * (later_a + later_b + now_a + now_b);
+        __builtin_amdgcn_s_waitcnt(0xc07f | ((n < 15 ? n : 15) << 8));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  auto mfma_pair = [&](int p, int slot) { Mfma<TI>::run(acc[p / WTN][p % WTN], fa[slot][p / WTN], fb[slot][p % WTN]); };
+
+  if (nst > 0) {
+    // ---- prologue: stages 0 and 1 in LDS (through registers: stage 1 in those)
+    if constexpr (DIRECT) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) copy_a(q, s, ks0 + s);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) copy_b(q, s, ks0 + s);
+      }
+    } else {
+      load_pieces(ks0);
+#pragma unroll
+      for (int q = 0; q < 2 * NQ; ++q) write_pieces(q, 0, ks0);
+      load_pieces(ks0 + 1);
+    }
+    if constexpr (DIRECT) wait_vmcnt_lgkm0<0>();
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < NDR; ++r) read_one(ro(r), 0, 0, 0);
+
+    for (int v = 0; v < nst; ++v) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        static_for<0, NPAIR>([&](auto pc) __attribute__((always_inline)) {
+          constexpr int p = decltype(pc)::value;
+          wait_frag(pc);
+          mfma_pair(p, s & 1);
+          // the fragment reads of a step before its register writes: those wait
+#pragma unroll
+          for (int r = p * RPP; r < NDR && r < (p + 1) * RPP; ++r) read_one(ro(r), v, s + 1, (s + 1) & 1);
+          if constexpr (!DIRECT) {
+            // 2 NQ pieces over the last 2 of the 3 steps, after a head start for the loads
+            constexpr int SLOTS = 2 * NPAIR, PER = (2 * NQ + SLOTS - 1) / SLOTS;
+            const int at = (s - 1) * NPAIR + p;
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+              if (at >= 0 && at * PER + c < 2 * NQ) write_pieces(at * PER + c, v + 1, ks0 + v + 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      }
+      // stage v + 1 is whole and this wave is done reading stage v; after the
+      // barrier that holds for every wave
+      wait_vmcnt_lgkm0<0>();
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+      load_pieces(ks0 + v + 2);
+#pragma unroll
+      for (int p = 0; p < NPAIR; ++p) {
+        mfma_pair(p, 1);
+        if constexpr (DIRECT) {
+#pragma unroll
+          for (int c = p; c < 2 * NQ; c += NPAIR) {
+            if (c < NQ) copy_a(c, v + 2, ks0 + v + 2);
+            else copy_b(c - NQ, v + 2, ks0 + v + 2);
+          }
+        }
+#pragma unroll
+        for (int r = p * RPP; r < NDR && r < (p + 1) * RPP; ++r) read_one(ro(r), v + 1, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    wait_vmcnt_lgkm0<0>();  // trailing copies and reads
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __syncthreads();
+
+  // ---- epilogue: 32-row strips of a wave through its part of the ring, then
+  // rows of 8 values per lane
+  constexpr int SROW = WN + 8;
+  static_assert(NW * 32 * SROW * 4 <= 2 * STG * 16, "strips fit in the ring");
+  constexpr int CW = WN / 8, DRS = 64 / CW, NT = 32 / DRS;
+  float* strip = reinterpret_cast<float*>(&ring[0][0]) + wid * (32 * SROW);
+  const int dr0 = lane / CW, dc8 = (lane % CW) * 8;
+  const int gj = col0 + wn * WN + dc8;
+  TO* C = static_cast<TO*>(a.o) + (MODE == EX_DW ? (int64_t)t.expert * a.se : (int64_t)t.begin * a.ldo);
+  static_for<0, WTM>([&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    const int gr0 = row0 + wm * (T / 2) + i * 32;
+#pragma unroll
+    for (int j = 0; j < WTN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) strip[((e >> 2) * 8 + half * 4 + (e & 3)) * SROW + j * 32 + l32] = acc[i][j][e];
+    wave_lds_sync();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = gr0 + dr0 + DRS * n;
+      const float* sp = strip + (dr0 + DRS * n) * SROW + dc8;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(sp);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(sp + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (r < M && gj < a.N) {
+        if (a.splits > 1) {
+          float* o = a.ws + ((int64_t)t.index * a.splits + t.split) * (T * T) + (r - row0) * T + (gj - col0);
+          *as_global(reinterpret_cast<f32x4*>(o)) = lo;
+          *as_global(reinterpret_cast<f32x4*>(o + 4)) = hi;
+        } else {
+          TO* o = C + (int64_t)r * a.ldo;
+          if (MODE == EX_DW && a.accumulate) {
+            float old[8];
+            piece_load(o, gj, a.N, old);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += old[e];
+          }
+          piece_store(o, gj, a.N, v);
+        }
+      }
+    }
+    wave_lds_sync();
+  });
+}
+
+// Adds the partial tiles of a split product in order.  8 columns per thread,
+// T * T / 2048 workgroups per tile.  Parts without stages were written as zeros.
+template <int MODE, int T, typename TO> __global__ __launch_bounds__(256) void experts_join_kernel(const ExpertsArgs a) {
+  constexpr int WGS = T * T / 2048;
+  ExpertTile t;
+  if (!experts_tile<MODE, T, true>(a, (int)(blockIdx.x / WGS), t)) return;
+  const int in = (int)(blockIdx.x % WGS) * 2048 + threadIdx.x * 8;  // first value within the tile
+  const int r = t.bi * T + in / T, c = t.bj * T + in % T;
+  if (r >= (MODE == EX_DW ? a.M : t.count) || c >= a.N) return;
+  const float* w = a.ws + (int64_t)t.index * a.splits * (T * T) + in;
+  float v[8] = {};
+#pragma unroll 4
+  for (int z = 0; z < a.splits; ++z)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(w + (int64_t)z * (T * T) + 4 * h));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * h + e] += x[e];
+    }
+  TO* o = static_cast<TO*>(a.o) +
+          (MODE == EX_DW ? (int64_t)t.expert * a.se : (int64_t)t.begin * a.ldo) + (int64_t)r * a.ldo;
+  if (MODE == EX_DW && a.accumulate) {
+    float old[8];
+    piece_load(o, c, a.N, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += old[e];
+  }
+  piece_store(o, c, a.N, v);
+}
+
+}  // namespace muon

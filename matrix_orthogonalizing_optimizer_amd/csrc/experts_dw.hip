@@ -1,0 +1,8 @@
+// Weight gradient of the products grouped by expert.
+#include "experts_inst.hpp"
+
+namespace muon {
+hipError_t launch_experts_dw(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
+  return experts_any<EX_DW>(tile, direct, dt, odt, tiles, a, s);
+}
+}  // namespace muon

@@ -1,0 +1,29 @@
+// Launch of one pass of the tiled products grouped by expert.
+#pragma once
+
+#include "experts.hpp"
+#include "launch.hpp"
+
+namespace muon {
+
+template <int MODE, int T, bool DIRECT, typename TI, typename TO>
+hipError_t experts_go(int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((experts_kernel<MODE, T, DIRECT, TI, TO>), dim3((unsigned)(tiles * a.splits)), dim3(512), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((experts_join_kernel<MODE, T, TO>), dim3((unsigned)(tiles * (T * T / 2048))), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int MODE, typename TO> hipError_t experts_in(int tile, bool direct, int dt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
+  if (dt == DT_F32) return experts_go<MODE, 128, false, float, TO>(tiles, a, s);
+  if (!direct) return experts_go<MODE, 128, false, bf16, TO>(tiles, a, s);
+  return tile == 256 ? experts_go<MODE, 256, true, bf16, TO>(tiles, a, s) : experts_go<MODE, 128, true, bf16, TO>(tiles, a, s);
+}
+
+template <int MODE> hipError_t experts_any(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
+  return odt == DT_BF16 ? experts_in<MODE, bf16>(tile, direct, dt, tiles, a, s)
+                        : experts_in<MODE, float>(tile, direct, dt, tiles, a, s);
+}
+
+}  // namespace muon

@@ -1,0 +1,41 @@
+// Host side of the products grouped by expert: which kernel a product takes.
+// No HIP in here, so that a host program can ask for the choice.
+#pragma once
+
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+#include "libmuon.h"
+#include "plan.hpp"
+
+namespace muon {
+
+struct ExpertsPlan {
+  int tile, splits;
+  int64_t tiles;  // most that any offsets need
+  size_t bytes;   // workspace: partial tiles
+};
+
+// direct: all operands are bf16 rows of whole 16-byte pieces.
+inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t out, int64_t in, int32_t dtype,
+                                bool direct) {
+  const bool dw = pass == MUON_EXPERTS_WEIGHT_GRAD;
+  const int64_t N = pass == MUON_EXPERTS_FORWARD ? out : in;
+  const int64_t some = std::min(experts, rows);
+  ExpertsPlan p;
+  // tile rows that the offsets need at most, and those they need when every
+  // expert's last tile is half full
+  auto most = [&](int64_t t) { return dw ? experts * ((out + t - 1) / t) : rows / t + some; };
+  auto tiles = [&](int64_t t) { return (dw ? experts * ((out + t - 1) / t) : rows / t + (some + 1) / 2) * ((N + t - 1) / t); };
+  p.tile = direct && tiles(256) >= 192 ? 256 : 128;
+  const int64_t bk = dtype == MUON_F32 ? 32 : 64;
+  const int64_t K = pass == MUON_EXPERTS_FORWARD ? in : pass == MUON_EXPERTS_INPUT_GRAD ? out : (rows + some - 1) / std::max<int64_t>(some, 1);
+  const int64_t stages = (K + bk - 1) / bk, n = std::max<int64_t>(1, tiles(p.tile));
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / n, stages / 4, 32}));
+  p.tiles = most(p.tile) * ((N + p.tile - 1) / p.tile);
+  p.bytes = p.splits > 1 ? (size_t)p.tiles * (size_t)p.splits * (size_t)(p.tile * p.tile) * sizeof(float) + WS_ALIGN : 0;
+  return p;
+}
+
+}  // namespace muon

@@ -148,6 +148,28 @@ struct Linear8Args {
   int32_t planes;     // gradients: bf16 planes (or pieces cut in the product) of dy that sum to it
   int64_t plane;      // elements between them
 };
+// Products grouped by expert (see experts.hpp): C as a sum over K of A B, for
+// the rows offsets[e] .. offsets[e + 1] - 1 of expert e.
+//   forward          A = x (rows x in),  B = w (experts x out x in), C = y
+//   input gradient   A = dy (rows x out), B = w, C = dx
+//   weight gradient  A = dy, B = x, C = dw (experts x out x in)
+struct ExpertsArgs {
+  const void* A;
+  const void* B;
+  void* o;                 // C
+  const int32_t* offsets;  // experts + 1
+  float* ws;               // partial tiles
+  int64_t lda, ldb, ldo;
+  int64_t se;              // elements between experts of w or dw
+  int32_t rows, experts;
+  int32_t M;               // weight gradient: rows of an expert's C
+  int32_t N;               // columns of C
+  int32_t K;               // forward, input gradient
+  int32_t tilesM, tilesN;  // of an expert's C (tilesM: weight gradient)
+  int32_t splits;          // parts of every tile's K
+  int32_t accumulate;      // weight gradient: added to C
+};
+
 // dy as bf16 planes (see linear8_planes_kernel).
 struct PlanesArgs {
   const void* dy;

@@ -48,4 +48,11 @@ hipError_t launch_linear8_planes(int dt, const PlanesArgs& a, hipStream_t s);
 hipError_t launch_linear8_dw(int tile, bool expanded, bool dy_f32, int odt, const Linear8Args& a, hipStream_t s);
 hipError_t launch_linear8_dx(int tile, bool expanded, bool dy_f32, int odt, const Linear8Args& a, hipStream_t s);
 
+// Products grouped by expert.  dt, odt: dtypes of the operands and of the
+// result; direct: bf16 rows of whole 16-byte pieces; tiles: most that any
+// offsets need.
+hipError_t launch_experts_y(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
+hipError_t launch_experts_dw(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
+hipError_t launch_experts_dx(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
+
 }  // namespace muon

@@ -16,7 +16,7 @@ const char* kNames[F_COUNT] = {"momentum_norm", "norm_finalize", "ns_gram_A", "n
                                "ns_update_PX", "ns_final_update", "gram_r0", "gram_p",
                                "gram_q", "gram_t", "gram_r", "adamw", "adamw8", "rows8",
                                "norm_forward", "norm_backward", "linear8_forward", "linear8_weight_grad",
-                               "linear8_input_grad"};
+                               "linear8_input_grad", "experts_forward", "experts_weight_grad", "experts_input_grad"};
 
 struct Rec {
   int fam;

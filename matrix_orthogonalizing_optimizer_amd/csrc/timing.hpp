@@ -26,6 +26,9 @@ enum Family : int {
   F_LINEAR8_Y,
   F_LINEAR8_DW,
   F_LINEAR8_DX,
+  F_EXPERTS_Y,
+  F_EXPERTS_DW,
+  F_EXPERTS_DX,
   F_COUNT
 };
 
