@@ -189,7 +189,8 @@ __device__ __forceinline__ void adamw8_tile(const Adamw8Desc& d, int64_t first, 
   auto* mo = as_global(reinterpret_cast<uint16_t*>(d.m + codes)) + first;
   auto* vo = as_global(reinterpret_cast<uint16_t*>(d.v + codes)) + first;
   static_assert(WHOLE || NB == 1, "one block at the tensor's end");
-  const int left = WHOLE ? 4 : (int)max<int64_t>(0, min<int64_t>(4, d.numel - i0));  // of the lane's elements, those in the tensor
+  const int64_t rest = d.numel - i0;
+  const int left = WHOLE || rest >= 4 ? 4 : rest > 0 ? (int)rest : 0;  // of the lane's elements, those in the tensor
   Four<T, STREAM> w[NB], g[NB];
   uint32_t mc[NB], vc[NB], om[NB], ov[NB];
 #pragma unroll

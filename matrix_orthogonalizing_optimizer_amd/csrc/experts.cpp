@@ -80,6 +80,7 @@ muon_status experts_pass(int pass, const Matrix& r, const Matrix& s, int64_t str
   const double f = 2.0 * (double)rows * (double)out * (double)in;
   const int fam = pass == MUON_EXPERTS_FORWARD ? F_EXPERTS_Y : dw ? F_EXPERTS_DW : F_EXPERTS_DX;
   const hipError_t e = timed(fam, f, 0.0, st, [&] {
+    if (p.few) return launch_experts_few(dev_dt(dtype), dev_dt(odtype), a, st);
     const auto go = pass == MUON_EXPERTS_FORWARD ? launch_experts_y : dw ? launch_experts_dw : launch_experts_dx;
     return go(p.tile, direct, dev_dt(dtype), dev_dt(odtype), p.tiles, a, st);
   });

@@ -12,6 +12,7 @@
 namespace muon {
 
 struct ExpertsPlan {
+  bool few;       // forward, few rows an expert: no tiles
   int tile, splits;
   int64_t tiles;  // most that any offsets need
   size_t bytes;   // workspace: partial tiles
@@ -24,6 +25,19 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   const int64_t N = pass == MUON_EXPERTS_FORWARD ? out : in;
   const int64_t some = std::min(experts, rows);
   ExpertsPlan p;
+  // Few rows: the kernel that streams the weights is ahead of the tiles up to 24
+  // rows an expert, or 64 rows at all (us, against the tiles: 64 experts of 1408 x
+  // 2048, 384 rows 76 and 122, 1536 rows 116 and 116; 8 of 14336 x 4096, 128 rows
+  // 227 and 253, 256 rows 380 and 212; one of 768 x 768, 64 rows 7.9 and 11.2, 128
+  // rows 14.4 and 11.9).
+  p.few = pass == MUON_EXPERTS_FORWARD && some <= 65535 && (rows <= 24 * some || rows <= 64);
+  if (p.few) {
+    p.tile = 128;
+    p.splits = 1;
+    p.tiles = (out + 15) / 16 * some;
+    p.bytes = 0;
+    return p;
+  }
   // tile rows that the offsets need at most, and those they need when every
   // expert's last tile is half full
   auto most = [&](int64_t t) { return dw ? experts * ((out + t - 1) / t) : rows / t + some; };

@@ -52,6 +52,7 @@ hipError_t launch_linear8_dx(int tile, bool expanded, bool dy_f32, int odt, cons
 // result; direct: bf16 rows of whole 16-byte pieces; tiles: most that any
 // offsets need.
 hipError_t launch_experts_y(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
+hipError_t launch_experts_few(int dt, int odt, const ExpertsArgs& a, hipStream_t s);  // forward, few rows an expert
 hipError_t launch_experts_dw(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
 hipError_t launch_experts_dx(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
 
