@@ -206,9 +206,10 @@ template <typename T> struct Piece {
   }
 };
 
-template <int MODE, int T, bool DIRECT, typename TI, typename TO>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(T == 128 ? 4 : 2, T == 128 ? 4 : 2)))
-void experts_kernel(const ExpertsArgs a) {
+// One tile, of which the first 64 MA rows and 128 NA columns are computed (the
+// others lie outside C): MA, NA are the 32 x 32 blocks of a wave along M and N.
+template <int MODE, int T, int MA, int NA, bool DIRECT, typename TI, typename TO>
+__device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const ExpertTile& t, u32x4 (*ring)[2 * T * 8]) {
   constexpr int NW = 8;
   constexpr bool AKM = MODE == EX_DW;      // A lies K-major
   constexpr bool BKM = MODE != EX_Y;       // B lies K-major
@@ -216,24 +217,20 @@ void experts_kernel(const ExpertsArgs a) {
   constexpr int EPC = 16 / ES;             // elements per 16-byte chunk
   constexpr int BK = 8 * EPC;              // K per stage
   constexpr int WGN = NW / 2;              // waves: 2 along M, NW / 2 along N
-  constexpr int WTM = T / 64, WN = T / WGN, WTN = WN / 32;
+  constexpr int WN = 32 * NA;              // columns of a wave
   constexpr int OPS = T * 8;               // chunks of one operand's stage
   constexpr int STG = 2 * OPS;
   constexpr int NQ = OPS / (64 * NW);      // 16-byte pieces of one operand a thread moves per stage
-  constexpr int NDR = WTM + WTN, NPAIR = WTM * WTN;
+  constexpr int NDR = MA + NA, NPAIR = MA * NA;
   constexpr int RPP = (NDR + NPAIR - 1) / NPAIR;  // fragment reads issued per MFMA
   constexpr int CR = T * ES / 16;          // chunks per K-row of a K-major stage
   constexpr int RPC = 64 / CR;             // K-rows per wave-wide copy
   static_assert(!DIRECT || ES == 2, "direct copies are bf16");
   static_assert(RPC >= 1 && BK * CR == OPS, "K-major stage");
-  __shared__ u32x4 ring[2][STG];
-
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wid / WGN, wn = wid % WGN;
   const int half = lane >> 5, l32 = lane & 31;
-  ExpertTile t;
-  if (!experts_tile<MODE, T, false>(a, blockIdx.x, t)) return;
   const int row0 = t.bi * T, col0 = t.bj * T;
   int ks0, ks1;
   experts_stages<MODE, BK>(a, t, ks0, ks1);
@@ -283,11 +280,11 @@ void experts_kernel(const ExpertsArgs a) {
   };
   auto copy_a = [&](int q, int v, int ks) {
     if constexpr (AKM) copy_k_major(A, a.lda, M, ta, 0, q, v, ks);
-    else copy_row_major(Arow, a.lda, rows_a, 0, q, v, ks);
+    else if (MA == T / 64 || wid * (8 * NQ) < 64 * MA) copy_row_major(Arow, a.lda, rows_a, 0, q, v, ks);
   };
   auto copy_b = [&](int q, int v, int ks) {
     if constexpr (BKM) copy_k_major(B, a.ldb, a.N, tb, OPS, q, v, ks);
-    else copy_row_major(Brow, a.ldb, rows_b, OPS, q, v, ks);
+    else if (128 * NA >= T || wid * (8 * NQ) < 128 * NA) copy_row_major(Brow, a.ldb, rows_b, OPS, q, v, ks);
   };
 
   // ---- the same chunks through registers
@@ -316,31 +313,31 @@ void experts_kernel(const ExpertsArgs a) {
     }
   };
 
-  f32x16 acc[WTM][WTN];
+  f32x16 acc[MA][NA];
 #pragma unroll
-  for (int i = 0; i < WTM; ++i)
+  for (int i = 0; i < MA; ++i)
 #pragma unroll
-    for (int j = 0; j < WTN; ++j)
+    for (int j = 0; j < NA; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
   // ---- fragments, double buffered by k-step
-  u32x4 fa[2][WTM], fb[2][WTN];
+  u32x4 fa[2][MA], fb[2][NA];
   const int rswz = (l32 & 7) ^ ((l32 >> 3) & 1);
   constexpr int ROWB = CR * 16;
   uint32_t tbase[NDR];
 #pragma unroll
   for (int r = 0; r < NDR; ++r) {
     const int e = (lane >> 2) & 3, q = lane & 3;
-    const int region = r < WTM ? 0 : OPS;
-    const int rb = r < WTM ? wm * (T / 2) + r * 32 : wn * WN + (r - WTM) * 32;
+    const int region = r < MA ? 0 : OPS;
+    const int rb = r < MA ? wm * (32 * MA) + r * 32 : wn * WN + (r - MA) * 32;
     const int col = rb + 16 * ((lane >> 4) & 1) + 4 * q;
     tbase[r] = (uint32_t)(uintptr_t)(lds_ptr_t)&ring[0][0] +
                (uint32_t)(region * 16 + (8 * half + e) * ROWB + ((col >> 3) ^ swz_t(e)) * 16 + (col & 7) * 2);
   }
   auto read_one = [&](int r, int v, int s, int slot) {
-    const bool isA = r < WTM;
-    const int rb = isA ? wm * (T / 2) + r * 32 : wn * WN + (r - WTM) * 32;
+    const bool isA = r < MA;
+    const int rb = isA ? wm * (32 * MA) + r * 32 : wn * WN + (r - MA) * 32;
     const u32x4* st = &ring[v & 1][isA ? 0 : OPS];
     u32x4 f;
     if (!(isA ? AKM : BKM)) {
@@ -363,10 +360,10 @@ void experts_kernel(const ExpertsArgs a) {
       }
     }
     if (isA) fa[slot][r] = f;
-    else fb[slot][r - WTM] = f;
+    else fb[slot][r - MA] = f;
   };
-  // reads in the order of first use: A0, B0 .. B(WTN-1), A1 .. A(WTM-1)
-  auto ro = [](int p) { return p == 0 ? 0 : (p <= WTN ? WTM + p - 1 : p - WTN); };
+  // reads in the order of first use: A0, B0 .. B(NA-1), A1 .. A(MA-1)
+  auto ro = [](int p) { return p == 0 ? 0 : (p <= NA ? MA + p - 1 : p - NA); };
   // The compiler does not track the transposed reads.  LDS instructions of a
   // wave complete in order, so before MFMA p it is enough that at most as
   // many are outstanding as were issued after the fragment that p is the
@@ -376,23 +373,23 @@ void experts_kernel(const ExpertsArgs a) {
   auto wait_frag = [&](auto pc) {
     if constexpr (ES == 2 && BKM) {
       constexpr int p = decltype(pc)::value;
-      constexpr int i = p / WTN, j = p % WTN;
+      constexpr int i = p / NA, j = p % NA;
       constexpr bool needA = j == 0 && AKM, needB = i == 0;  // first uses among the transposed
       if constexpr (needA || needB) {
         // position of that fragment in the reading order
-        constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : WTN + i);
-        constexpr int later_a = AKM ? (WTM - 1 - (at > WTN ? at - WTN : 0)) : 0;
-        constexpr int later_b = at <= WTN ? WTN - at : 0;
+        constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : NA + i);
+        constexpr int later_a = AKM ? (MA - 1 - (at > NA ? at - NA : 0)) : 0;
+        constexpr int later_b = at <= NA ? NA - at : 0;
         constexpr int now = p * RPP < NDR ? p * RPP : NDR;  // reads issued so far in this step
-        constexpr int now_a = AKM ? (now > 0 ? 1 : 0) + (now > WTN + 1 ? now - WTN - 1 : 0) : 0;
-        constexpr int now_b = now <= 1 ? 0 : (now - 1 < WTN ? now - 1 : WTN);
+        constexpr int now_a = AKM ? (now > 0 ? 1 : 0) + (now > NA + 1 ? now - NA - 1 : 0) : 0;
+        constexpr int now_b = now <= 1 ? 0 : (now - 1 < NA ? now - 1 : NA);
         constexpr int n = 2 * (later_a + later_b + now_a + now_b);
         __builtin_amdgcn_s_waitcnt(0xc07f | ((n < 15 ? n : 15) << 8));
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
-  auto mfma_pair = [&](int p, int slot) { Mfma<TI>::run(acc[p / WTN][p % WTN], fa[slot][p / WTN], fb[slot][p % WTN]); };
+  auto mfma_pair = [&](int p, int slot) { Mfma<TI>::run(acc[p / NA][p % NA], fa[slot][p / NA], fb[slot][p % NA]); };
 
   if (nst > 0) {
     // ---- prologue: stages 0 and 1 in LDS (through registers: stage 1 in those)
@@ -472,11 +469,11 @@ void experts_kernel(const ExpertsArgs a) {
   const int dr0 = lane / CW, dc8 = (lane % CW) * 8;
   const int gj = col0 + wn * WN + dc8;
   TO* C = static_cast<TO*>(a.o) + (MODE == EX_DW ? (int64_t)t.expert * a.se : (int64_t)t.begin * a.ldo);
-  static_for<0, WTM>([&](auto ic) __attribute__((always_inline)) {
+  static_for<0, MA>([&](auto ic) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value;
-    const int gr0 = row0 + wm * (T / 2) + i * 32;
+    const int gr0 = row0 + wm * (32 * MA) + i * 32;
 #pragma unroll
-    for (int j = 0; j < WTN; ++j)
+    for (int j = 0; j < NA; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) strip[((e >> 2) * 8 + half * 4 + (e & 3)) * SROW + j * 32 + l32] = acc[i][j][e];
     wave_lds_sync();
@@ -506,6 +503,28 @@ void experts_kernel(const ExpertsArgs a) {
     }
     wave_lds_sync();
   });
+}
+
+template <int MODE, int T, bool DIRECT, typename TI, typename TO>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(T == 128 ? 4 : 2, T == 128 ? 4 : 2)))
+void experts_kernel(const ExpertsArgs a) {
+  __shared__ u32x4 ring[2][2 * T * 8];
+  ExpertTile t;
+  if (!experts_tile<MODE, T, false>(a, blockIdx.x, t)) return;
+  // a tile at C's edge of which half or less is inside computes that half: 64
+  // experts of 1408 x 2048, 49152 rows lose a tenth of their work to edges
+  // instead of a quarter
+  const bool low = (MODE == EX_DW ? a.M : t.count) - t.bi * T <= T / 2;
+  if constexpr (T == 256) {
+    const bool narrow = a.N - t.bj * T <= T / 2;
+    if (low && narrow) experts_compute<MODE, T, 2, 1, DIRECT, TI, TO>(a, t, ring);
+    else if (low) experts_compute<MODE, T, 2, 2, DIRECT, TI, TO>(a, t, ring);
+    else if (narrow) experts_compute<MODE, T, 4, 1, DIRECT, TI, TO>(a, t, ring);
+    else experts_compute<MODE, T, 4, 2, DIRECT, TI, TO>(a, t, ring);
+  } else {
+    if (low) experts_compute<MODE, T, 1, 1, DIRECT, TI, TO>(a, t, ring);
+    else experts_compute<MODE, T, 2, 1, DIRECT, TI, TO>(a, t, ring);
+  }
 }
 
 // Adds the partial tiles of a split product in order.  8 columns per thread,
