@@ -17,7 +17,8 @@ LIB = os.path.join(PKG, "libmuon.so")
 HIP_SOURCES = ["api.cpp", "timing.cpp", "kernels_elem.hip", "gemm_bf16.hip", "gemm_f16.hip",
                "gemm_f32.hip", "probes.hip", "noalloc.hip", "ops.cpp", "row_ops.hip",
                "linear8_y.hip", "linear8_dw.hip", "linear8_dx.hip", "adamw8.hip",
-               "experts.cpp", "experts_y.hip", "experts_dw.hip", "experts_dx.hip", "experts_few.hip"]
+               "experts.cpp", "experts_y.hip", "experts_dw.hip", "experts_dx.hip", "experts_few.hip",
+               "experts_big_y.hip", "experts_big_dw.hip", "experts_big_dx.hip"]
 HOST_SOURCES = ["plan.cpp"]
 ARCH = "gfx950"
 

@@ -12,6 +12,8 @@
 
 using namespace muon;
 
+static_assert(sizeof(ExpertsItem) == 32 && sizeof(ExpertsHead) <= 8192, "workspace layout");
+
 namespace {
 
 constexpr int64_t MAX_SIDE = (int64_t)1 << 30;
@@ -72,17 +74,26 @@ muon_status experts_pass(int pass, const Matrix& r, const Matrix& s, int64_t str
   a.tilesN = (int32_t)((ocols + p.tile - 1) / p.tile);
   a.splits = p.splits;
   a.accumulate = accumulate;
-  if (p.splits > 1) {
+  if (p.bytes) {
     const uintptr_t u = reinterpret_cast<uintptr_t>(workspace);
-    a.ws = reinterpret_cast<float*>((u + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN);
+    char* ws = reinterpret_cast<char*>((u + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN);
+    a.ws = reinterpret_cast<float*>(ws + p.ws_off);
+    a.head = reinterpret_cast<ExpertsHead*>(ws);
+    a.items = reinterpret_cast<ExpertsItem*>(ws + p.items_off);
+    a.chunk = (int32_t)p.chunk;
+    a.cap = (int32_t)p.cap;
   }
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)rows * (double)out * (double)in;
   const int fam = pass == MUON_EXPERTS_FORWARD ? F_EXPERTS_Y : dw ? F_EXPERTS_DW : F_EXPERTS_DX;
   const hipError_t e = timed(fam, f, 0.0, st, [&] {
     if (p.few) return launch_experts_few(dev_dt(dtype), dev_dt(odtype), a, st);
+    if (p.big) {
+      const auto go = pass == MUON_EXPERTS_FORWARD ? launch_experts_big_y : dw ? launch_experts_big_dw : launch_experts_big_dx;
+      return go(dev_dt(odtype), a, st);
+    }
     const auto go = pass == MUON_EXPERTS_FORWARD ? launch_experts_y : dw ? launch_experts_dw : launch_experts_dx;
-    return go(p.tile, direct, dev_dt(dtype), dev_dt(odtype), p.tiles, a, st);
+    return go(direct, dev_dt(dtype), dev_dt(odtype), p.tiles, a, st);
   });
   return e == hipSuccess ? MUON_OK : MUON_E_HIP;
 }

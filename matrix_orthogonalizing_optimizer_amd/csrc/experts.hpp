@@ -206,6 +206,52 @@ template <typename T> struct Piece {
   }
 };
 
+// 16 bytes from LDS at a constant offset from addr, in inline assembly: for a
+// read that the compiler sees it waits for all copies to LDS under way, as
+// they might write what is read (the last quarter of every stage then took the
+// time of its copies).
+template <int OFF> __device__ __forceinline__ u32x4 lds_read_b128(uint32_t addr) {
+  static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
+  u32x4 r;
+  asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(r) : "v"(addr), "i"(OFF) : "memory");
+  return r;
+}
+
+// Row block r (0 .. 3) of 32 rows of 128 bytes.
+__device__ __forceinline__ u32x4 lds_read_b128_block(uint32_t addr, int r) {
+  switch (r) {
+    case 0: return lds_read_b128<0>(addr);
+    case 1: return lds_read_b128<4096>(addr);
+    case 2: return lds_read_b128<8192>(addr);
+    default: return lds_read_b128<12288>(addr);
+  }
+}
+
+// Waits for the fragments that MFMA p of a step is the first to use.  The
+// compiler does not track reads in inline assembly.  LDS instructions of a wave
+// complete in order, so it is enough that at most as many are outstanding as were
+// issued after that fragment: this step's later fragments and the next step's
+// first ones, IA or IB instructions each (0: reads that the compiler tracks; those
+// and register writes are not counted, which only waits for more).  Reads come in
+// the order A0, B0 .. B(NB-1), A1 .. A(NA-1).
+template <int NA, int NB, int IA, int IB, typename P> __device__ __forceinline__ void experts_wait_frag(P) {
+  constexpr int NDR = NA + NB, NPAIR = NA * NB, RPP = (NDR + NPAIR - 1) / NPAIR;
+  constexpr int p = P::value, i = p / NB, j = p % NB;
+  constexpr bool needA = j == 0 && IA > 0, needB = i == 0 && IB > 0;  // first uses
+  if constexpr (needA || needB) {
+    // position of that fragment in the reading order
+    constexpr int at = needB ? j + 1 : (i == 0 ? 0 : NB + i);
+    constexpr int later_a = NA - 1 - (at > NB ? at - NB : 0);
+    constexpr int later_b = at <= NB ? NB - at : 0;
+    constexpr int now = p * RPP < NDR ? p * RPP : NDR;  // reads issued so far in this step
+    constexpr int now_a = (now > 0 ? 1 : 0) + (now > NB + 1 ? now - NB - 1 : 0);
+    constexpr int now_b = now <= 1 ? 0 : (now - 1 < NB ? now - 1 : NB);
+    constexpr int n = IA * (later_a + now_a) + IB * (later_b + now_b);
+    __builtin_amdgcn_s_waitcnt(0xc07f | ((n < 15 ? n : 15) << 8));
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // One tile, of which the first 64 MA rows and 128 NA columns are computed (the
 // others lie outside C): MA, NA are the 32 x 32 blocks of a wave along M and N.
 template <int MODE, int T, int MA, int NA, bool DIRECT, typename TI, typename TO>
@@ -325,6 +371,9 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   u32x4 fa[2][MA], fb[2][NA];
   const int rswz = (l32 & 7) ^ ((l32 >> 3) & 1);
   constexpr int ROWB = CR * 16;
+  const uint32_t rd[2] = {
+      (uint32_t)(uintptr_t)(lds_ptr_t)&ring[0][(wm * (32 * MA) + l32) * 8 + (half ^ rswz)],
+      (uint32_t)(uintptr_t)(lds_ptr_t)&ring[0][OPS + (wn * WN + l32) * 8 + (half ^ rswz)]};
   uint32_t tbase[NDR];
 #pragma unroll
   for (int r = 0; r < NDR; ++r) {
@@ -341,7 +390,8 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
     const u32x4* st = &ring[v & 1][isA ? 0 : OPS];
     u32x4 f;
     if (!(isA ? AKM : BKM)) {
-      f = st[(rb + l32) * 8 + ((2 * s + half) ^ rswz)];
+      // chunk 2 s + half of the row, swizzled
+      f = lds_read_b128_block((rd[isA ? 0 : 1] ^ (uint32_t)(32 * s)) + (uint32_t)((v & 1) * STG * 16), isA ? r : r - MA);
     } else if constexpr (ES == 2) {
       const uint32_t p = tbase[r] + (uint32_t)((v & 1) * STG * 16);
 #pragma unroll
@@ -364,30 +414,8 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   };
   // reads in the order of first use: A0, B0 .. B(NA-1), A1 .. A(MA-1)
   auto ro = [](int p) { return p == 0 ? 0 : (p <= NA ? MA + p - 1 : p - NA); };
-  // The compiler does not track the transposed reads.  LDS instructions of a
-  // wave complete in order, so before MFMA p it is enough that at most as
-  // many are outstanding as were issued after the fragment that p is the
-  // first to use: this step's later fragments and the next step's first p
-  // ones (two instructions each; untransposed reads and register writes are
-  // not counted, which only waits for more).
   auto wait_frag = [&](auto pc) {
-    if constexpr (ES == 2 && BKM) {
-      constexpr int p = decltype(pc)::value;
-      constexpr int i = p / NA, j = p % NA;
-      constexpr bool needA = j == 0 && AKM, needB = i == 0;  // first uses among the transposed
-      if constexpr (needA || needB) {
-        // position of that fragment in the reading order
-        constexpr int at = needB ? (j + 1) : (i == 0 ? 0 : NA + i);
-        constexpr int later_a = AKM ? (MA - 1 - (at > NA ? at - NA : 0)) : 0;
-        constexpr int later_b = at <= NA ? NA - at : 0;
-        constexpr int now = p * RPP < NDR ? p * RPP : NDR;  // reads issued so far in this step
-        constexpr int now_a = AKM ? (now > 0 ? 1 : 0) + (now > NA + 1 ? now - NA - 1 : 0) : 0;
-        constexpr int now_b = now <= 1 ? 0 : (now - 1 < NA ? now - 1 : NA);
-        constexpr int n = 2 * (later_a + later_b + now_a + now_b);
-        __builtin_amdgcn_s_waitcnt(0xc07f | ((n < 15 ? n : 15) << 8));
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
+    experts_wait_frag<MA, NA, AKM ? (ES == 2 ? 2 : 0) : 1, BKM ? (ES == 2 ? 2 : 0) : 1>(pc);
   };
   auto mfma_pair = [&](int p, int slot) { Mfma<TI>::run(acc[p / NA][p % NA], fa[slot][p / NA], fb[slot][p % NA]); };
 

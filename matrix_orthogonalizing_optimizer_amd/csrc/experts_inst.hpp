@@ -15,15 +15,15 @@ hipError_t experts_go(int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MODE, typename TO> hipError_t experts_in(int tile, bool direct, int dt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
+template <int MODE, typename TO> hipError_t experts_in(bool direct, int dt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
   if (dt == DT_F32) return experts_go<MODE, 128, false, float, TO>(tiles, a, s);
   if (!direct) return experts_go<MODE, 128, false, bf16, TO>(tiles, a, s);
-  return tile == 256 ? experts_go<MODE, 256, true, bf16, TO>(tiles, a, s) : experts_go<MODE, 128, true, bf16, TO>(tiles, a, s);
+  return experts_go<MODE, 128, true, bf16, TO>(tiles, a, s);
 }
 
-template <int MODE> hipError_t experts_any(int tile, bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
-  return odt == DT_BF16 ? experts_in<MODE, bf16>(tile, direct, dt, tiles, a, s)
-                        : experts_in<MODE, float>(tile, direct, dt, tiles, a, s);
+template <int MODE> hipError_t experts_any(bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
+  return odt == DT_BF16 ? experts_in<MODE, bf16>(direct, dt, tiles, a, s)
+                        : experts_in<MODE, float>(direct, dt, tiles, a, s);
 }
 
 }  // namespace muon

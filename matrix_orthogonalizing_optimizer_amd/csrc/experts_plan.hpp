@@ -13,9 +13,13 @@ namespace muon {
 
 struct ExpertsPlan {
   bool few;       // forward, few rows an expert: no tiles
+  bool big;       // 256 x 256 tiles from lists
   int tile, splits;
   int64_t tiles;  // most that any offsets need
-  size_t bytes;   // workspace: partial tiles
+  int64_t chunk;  // big, weight gradient: rows of an expert summed at once
+  int64_t cap;    // big: room of a list
+  size_t items_off, ws_off;  // workspace: lists, partial tiles
+  size_t bytes;
 };
 
 // direct: all operands are bf16 rows of whole 16-byte pieces.
@@ -24,7 +28,9 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   const bool dw = pass == MUON_EXPERTS_WEIGHT_GRAD;
   const int64_t N = pass == MUON_EXPERTS_FORWARD ? out : in;
   const int64_t some = std::min(experts, rows);
-  ExpertsPlan p;
+  ExpertsPlan p{};
+  p.tile = 128;
+  p.splits = 1;
   // Few rows: the kernel that streams the weights is ahead of the tiles up to 24
   // rows an expert, or 64 rows at all (us, against the tiles: 64 experts of 1408 x
   // 2048, 384 rows 76 and 122, 1536 rows 116 and 116; 8 of 14336 x 4096, 128 rows
@@ -32,17 +38,27 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   // rows 14.4 and 11.9).
   p.few = pass == MUON_EXPERTS_FORWARD && some <= 65535 && (rows <= 24 * some || rows <= 64);
   if (p.few) {
-    p.tile = 128;
-    p.splits = 1;
     p.tiles = (out + 15) / 16 * some;
-    p.bytes = 0;
     return p;
   }
   // tile rows that the offsets need at most, and those they need when every
   // expert's last tile is half full
   auto most = [&](int64_t t) { return dw ? experts * ((out + t - 1) / t) : rows / t + some; };
   auto tiles = [&](int64_t t) { return (dw ? experts * ((out + t - 1) / t) : rows / t + (some + 1) / 2) * ((N + t - 1) / t); };
-  p.tile = direct && tiles(256) >= 192 ? 256 : 128;
+  const int64_t per = ((out + 255) / 256) * ((N + 255) / 256);  // weight gradient: tiles of an expert
+  // an expert with more rows than a CU sums over all is cut
+  const int64_t share = (rows + 63) / 64 * per / 256;
+  p.chunk = 64 * std::max<int64_t>(8, share);
+  p.big = direct && tiles(256) >= 192 && experts + (dw ? rows / p.chunk : 0) <= 2048;
+  if (p.big) {
+    p.tile = 256;
+    p.tiles = dw ? (experts + rows / p.chunk) * per : most(256) * ((N + 255) / 256);
+    p.cap = p.tiles / 8 + 32;  // 8 equal lists, the last tiles in up to 24 more parts
+    p.items_off = 8192;  // behind the head
+    p.ws_off = p.items_off + (size_t)p.cap * 8 * 32;
+    p.bytes = p.ws_off + (dw ? (size_t)(2 * (rows / p.chunk) * per) * 256 * 256 * sizeof(float) : 0) + WS_ALIGN;
+    return p;
+  }
   const int64_t bk = dtype == MUON_F32 ? 32 : 64;
   const int64_t K = pass == MUON_EXPERTS_FORWARD ? in : pass == MUON_EXPERTS_INPUT_GRAD ? out : (rows + some - 1) / std::max<int64_t>(some, 1);
   const int64_t stages = (K + bk - 1) / bk, n = std::max<int64_t>(1, tiles(p.tile));

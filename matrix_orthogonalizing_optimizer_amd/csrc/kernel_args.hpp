@@ -168,6 +168,31 @@ struct ExpertsArgs {
   int32_t tilesM, tilesN;  // of an expert's C (tilesM: weight gradient)
   int32_t splits;          // parts of every tile's K
   int32_t accumulate;      // weight gradient: added to C
+  // large products: lists of the tiles (see experts_big.hpp)
+  int32_t chunk;           // weight gradient: rows of an expert that a tile sums at once
+  int32_t cap;             // tiles that a list has room for
+  struct ExpertsHead* head;
+  struct ExpertsItem* items;
+};
+// What one workgroup does of a large product: `size` rows (low half) and columns
+// (high half) of an expert's C from row0, col0 on, over `count` rows from `begin` on.
+struct __attribute__((aligned(32))) ExpertsItem {
+  int32_t begin, count;
+  int32_t row0, col0;
+  int32_t size;
+  int32_t expert;
+  int32_t slot;  // partial tile it leaves in the workspace; -1: C itself
+  int32_t pad;
+};
+constexpr int EXPERTS_SPLIT = 512;  // experts whose rows take several chunks, at most
+struct ExpertsHead {
+  int32_t count[8];  // items of each list
+  int32_t splits;    // experts summed in chunks
+  int32_t pad[7];
+  int32_t taken[8][16];  // items that the list's workgroups have taken, a cache line each
+  struct {
+    int32_t expert, slot, chunks;  // partial tiles from slot on: [chunk][tile]
+  } split[EXPERTS_SPLIT];
 };
 
 // dy as bf16 planes (see linear8_planes_kernel).

@@ -188,6 +188,42 @@ def test_large_and_long(shape, dtype):
         run_all(rows, experts, out - 1, in_ - 3, dtype, split_rows(rows, experts, experts), what="odd")
 
 
+@pytest.mark.parametrize("shape", [(3000, 60, 1152, 1032), (9000, 12, 5128, 1288), (700, 1000, 264, 264), (2600, 2048, 264, 136),
+                                   (40000, 30, 2560, 520)])
+def test_many_tiles(shape):
+    """Each workgroup computes many tiles one after the other, of experts with no
+    row, of one stage of K, and of many; every value against products in fp64 on
+    the device (whole numbers: exact)."""
+    rows, experts, out, in_ = shape
+    print("experts many tiles", shape, flush=True)
+    d = dev()
+    off = split_rows(rows, experts, 3, empty=0.3, lead=1, tail=2)
+    gen = torch.Generator(device=d).manual_seed(1)
+    whole = lambda *s: torch.randint(-3, 4, s, generator=gen, device=d).to(BF)
+    x, w, dy = whole(rows, in_), whole(experts, out, in_), whole(rows, out)
+    nan = float("nan")
+    for odt in (F32, BF):
+        y = torch.full((rows, out), nan, dtype=odt, device=d)
+        dx = torch.full((rows, in_), nan, dtype=odt, device=d)
+        dw = torch.full((experts, out, in_), nan, dtype=odt, device=d)
+        mo.muon_experts_forward(x, w, off, y=y)
+        mo.muon_experts_input_grad(dy, w, off, dx=dx)
+        mo.muon_experts_weight_grad(dy, x, off, dw=dw)
+        for e, a, b in R.groups(off.tolist(), rows):
+            ref = dy[a:b].double().t().contiguous() @ x[a:b].double()
+            assert torch.equal(dw[e], ref.to(odt)), ("weight grad", e, odt)
+            if b > a:
+                assert torch.equal(y[a:b], (x[a:b].double() @ w[e].double().t().contiguous()).to(odt)), ("forward", e, odt)
+                assert torch.equal(dx[a:b], (dy[a:b].double() @ w[e].double()).to(odt)), ("input grad", e, odt)
+        for t in (y, dx):
+            assert t[0].isnan().all() and t[rows - 2:].isnan().all()
+    before = dw.clone()
+    mo.muon_experts_weight_grad(dy, x, off, dw=dw, accumulate=True)
+    for e, a, b in R.groups(off.tolist(), rows):
+        ref = dy[a:b].double().t().contiguous() @ x[a:b].double() + before[e].double()
+        assert torch.equal(dw[e], ref.to(BF)), ("weight grad added", e)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("shape", [(777, 5, 301, 129), (600, 4, 512, 1024), (64, 8, 128, 4096), (3000, 2, 136, 72)])
 def test_any_values(shape, dtype):
