@@ -98,7 +98,7 @@ template <int MODE> __global__ __launch_bounds__(256) void experts_list_kernel(c
     }
     if (tid == 0) first[0] = 0;
     __syncthreads();
-    const int S = 8 * a.tilesN, n = big_count(x, sum * a.tilesN, S);
+    const int S = 4 * a.tilesN, n = big_count(x, sum * a.tilesN, S);
     // what is left over full rounds of 32 workgroups
     const int rest = n % 32, parts = rest == 0 || rest > 16 ? 1 : rest > 8 ? 2 : 4, cut = parts > 1 ? rest : 0;
     for (int p = tid; p < n; p += 256) {
@@ -329,6 +329,12 @@ void experts_big_kernel(const ExpertsArgs a) {
   const uint32_t ring0 = (uint32_t)(uintptr_t)(lds_ptr_t)&ring[0][0];
 
   int g = 0;  // ring slot of the stage that is computed next
+  // C in whole 16-byte pieces, written and not added to: a strip is ST stores,
+  // whichever of its lanes lie inside C
+  constexpr int ST = sizeof(TO) / 2;
+  const bool pieces = !(MODE == EX_DW && a.accumulate) && a.N % 8 == 0 && a.ldo % 8 == 0 &&
+                      (MODE != EX_DW || a.se % 8 == 0) && (uintptr_t)a.o % 16 == 0;
+  int stores = 0;  // of the tile before, if their number is known
   ExpertsItem now = item(k0);
   auto tile = [&](const ExpertsItem& t, int nst, auto mc, auto nc) __attribute__((always_inline)) {
     constexpr int MA = decltype(mc)::value, NA = decltype(nc)::value;  // 32 x 32 blocks of a wave along M and N
@@ -399,7 +405,11 @@ void experts_big_kernel(const ExpertsArgs a) {
         }
         // the next stage is whole and this wave is done reading this one; after
         // the barrier that holds for every wave
-        wait_vmcnt_lgkm0<0>();
+        // The stores of the tile before were issued after this stage's copies: they
+        // may still be under way.
+        if (v == 0 && stores == 8 * ST) wait_vmcnt_lgkm0<8 * ST>();
+        else if (v == 0 && stores == 16 * ST) wait_vmcnt_lgkm0<16 * ST>();
+        else wait_vmcnt_lgkm0<0>();
         post();
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
@@ -422,46 +432,69 @@ void experts_big_kernel(const ExpertsArgs a) {
     g += nst;
     now = item(q0);  // the next one, on its way during the epilogue
 
-    // ---- epilogue: strips of 16 rows of a wave, then 8 values of a row per lane
+    // ---- epilogue: strips of 8 rows of a wave, then 8 values of a row per lane
     constexpr int CW = WN / 8, DRS = 64 / CW;
     static_assert(DRS >= SROWS, "a lane takes one piece of a strip");
     float* strip = strips[wid];
     const int dr0 = lane / CW, dc8 = (lane % CW) * 8;
-    const int row0 = t.row0, col0 = t.col0;
-    const int gj = col0 + wn * WN + dc8;
+    const int gj = t.col0 + wn * WN + dc8;
     const int M = MODE == EX_DW ? a.M : t.count;
-    TO* C = static_cast<TO*>(a.o) + (MODE == EX_DW ? (int64_t)t.expert * a.se : (int64_t)t.begin * a.ldo);
-    float* W = a.ws + (int64_t)t.slot * (T * T);
-    static_for<0, 4 * MA>([&](auto ic) __attribute__((always_inline)) {
-      constexpr int i = decltype(ic)::value / 4, h = decltype(ic)::value % 4;
-      const int r = row0 + wm * (32 * MA) + i * 32 + h * SROWS + dr0;
+    const bool mine = dr0 < SROWS && gj < a.N;
+    TO* C = static_cast<TO*>(a.o) + (MODE == EX_DW ? (int64_t)t.expert * a.se : (int64_t)t.begin * a.ldo) +
+            (int64_t)t.row0 * a.ldo;
+    // put(lo, hi): the lane's values of a strip; strips come in the order of their rows
+    auto each_strip = [&](auto put) __attribute__((always_inline)) {
+      static_for<0, 4 * MA>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value / 4, h = decltype(ic)::value % 4;
 #pragma unroll
-      for (int j = 0; j < NA; ++j)
+        for (int j = 0; j < NA; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) strip[(half * 4 + e) * WN + j * 32 + l32] = acc[i][j][4 * h + e];
-      wave_lds_sync();
-      if (dr0 < SROWS && r < M && gj < a.N) {
-        const float* sp = strip + dr0 * WN + dc8;
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(sp);
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(sp + 4);
-        if (MODE == EX_DW && t.slot >= 0) {
-          float* o = W + (r - row0) * T + (gj - col0);
-          *as_global(reinterpret_cast<f32x4*>(o)) = lo;
-          *as_global(reinterpret_cast<f32x4*>(o + 4)) = hi;
-        } else {
-          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          TO* o = C + (int64_t)r * a.ldo;
-          if (MODE == EX_DW && a.accumulate) {
-            float old[8];
-            piece_load(o, gj, a.N, old);
+          for (int e = 0; e < 4; ++e) strip[(half * 4 + e) * WN + j * 32 + l32] = acc[i][j][4 * h + e];
+        wave_lds_sync();
+        const float* sp = strip + (dr0 % SROWS) * WN + dc8;
+        put(*reinterpret_cast<const f32x4*>(sp), *reinterpret_cast<const f32x4*>(sp + 4));
+        wave_lds_sync();
+      });
+    };
+    if (pieces && (MODE != EX_DW || t.slot < 0)) {
+      // through a resource that drops what lies outside C
+      const int rows = min(T, M - t.row0);
+      const __amdgpu_buffer_rsrc_t rc =
+          make_rsrc(C, rows > 0 ? (uint32_t)((((int64_t)rows - 1) * a.ldo + a.N) * (int)sizeof(TO)) : 0u);
+      const uint32_t step = (uint32_t)(SROWS * a.ldo * (int)sizeof(TO));
+      uint32_t off = mine ? (uint32_t)(((int64_t)(wm * (32 * MA) + dr0) * a.ldo + gj) * (int)sizeof(TO)) : OOB;
+      each_strip([&](const f32x4& lo, const f32x4& hi) __attribute__((always_inline)) {
+        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        buffer_store8<TO>(rc, off, v);
+        off += step;
+        asm volatile("" : "+v"(off));  // one register, not one per strip
+      });
+      stores = 4 * MA * ST;
+    } else {
+      int r = wm * (32 * MA) + dr0;
+      each_strip([&](const f32x4& lo, const f32x4& hi) __attribute__((always_inline)) {
+        if (mine && t.row0 + r < M) {
+          if (MODE == EX_DW && t.slot >= 0) {
+            float* o = a.ws + (int64_t)t.slot * (T * T) + r * T + (gj - t.col0);
+            *as_global(reinterpret_cast<f32x4*>(o)) = lo;
+            *as_global(reinterpret_cast<f32x4*>(o + 4)) = hi;
+          } else {
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            TO* o = C + (int64_t)r * a.ldo;
+            if (MODE == EX_DW && a.accumulate) {
+              float old[8];
+              piece_load(o, gj, a.N, old);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += old[e];
+              for (int e = 0; e < 8; ++e) v[e] += old[e];
+            }
+            piece_store(o, gj, a.N, v);
           }
-          piece_store(o, gj, a.N, v);
         }
-      }
-      wave_lds_sync();
-    });
+        r += SROWS;
+        asm volatile("" : "+v"(r));
+      });
+      stores = 0;
+    }
   };
 
   // ---- the first two stages, then item by item
