@@ -58,7 +58,7 @@ muon_status experts_pass(int pass, const Matrix& r, const Matrix& s, int64_t str
                       (dw || stride % 8 == 0);
   const ExpertsPlan p = experts_plan(pass, rows, experts, out, in, dtype, direct);
   if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MUON_E_WORKSPACE;
-  if (p.tiles * std::max(p.splits, p.splits > 1 ? p.tile * p.tile / 2048 : 1) > MAX_WORKGROUPS) return MUON_E_SHAPE;
+  if (std::max(p.tiles * p.splits, p.joined * (p.tile * p.tile / 2048)) > MAX_WORKGROUPS) return MUON_E_SHAPE;
   ExpertsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.A = r.p; a.lda = r.ld;
@@ -78,11 +78,11 @@ muon_status experts_pass(int pass, const Matrix& r, const Matrix& s, int64_t str
     const uintptr_t u = reinterpret_cast<uintptr_t>(workspace);
     char* ws = reinterpret_cast<char*>((u + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN);
     a.ws = reinterpret_cast<float*>(ws + p.ws_off);
-    a.head = reinterpret_cast<ExpertsHead*>(ws);
-    a.items = reinterpret_cast<ExpertsItem*>(ws + p.items_off);
-    a.chunk = (int32_t)p.chunk;
+    if (p.big) a.head = reinterpret_cast<ExpertsHead*>(ws);
+    if (p.big) a.items = reinterpret_cast<ExpertsItem*>(ws + p.items_off);
     a.cap = (int32_t)p.cap;
   }
+  a.chunk = (int32_t)p.chunk;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const double f = 2.0 * (double)rows * (double)out * (double)in;
   const int fam = pass == MUON_EXPERTS_FORWARD ? F_EXPERTS_Y : dw ? F_EXPERTS_DW : F_EXPERTS_DX;
@@ -93,7 +93,7 @@ muon_status experts_pass(int pass, const Matrix& r, const Matrix& s, int64_t str
       return go(dev_dt(odtype), a, st);
     }
     const auto go = pass == MUON_EXPERTS_FORWARD ? launch_experts_y : dw ? launch_experts_dw : launch_experts_dx;
-    return go(direct, dev_dt(dtype), dev_dt(odtype), p.tiles, a, st);
+    return go(direct, dev_dt(dtype), dev_dt(odtype), p.tiles, p.joined, a, st);
   });
   return e == hipSuccess ? MUON_OK : MUON_E_HIP;
 }

@@ -9,8 +9,8 @@
 // expert has.  EX_Y and EX_DX launch as many workgroups as any offsets can
 // need (rows / T + experts tile rows); each finds its tile from a prefix sum
 // over the experts' tile rows (experts_tile), and those past the last tile
-// end at once.  EX_DW has experts x tiles workgroups whose K is the expert's
-// number of rows.  Offsets are clamped to 0 .. rows, so no value of theirs
+// end at once.  EX_DW has a workgroup per tile and unit of at most `chunk` rows
+// of an expert (one unit for an expert without rows).  Offsets are clamped to 0 .. rows, so no value of theirs
 // leads outside the operands.
 //
 // A workgroup of 8 waves owns a T x T tile of C (T = 256: 128 x 64 outputs per
@@ -26,8 +26,9 @@
 // register round trip.  Otherwise (odd widths, any alignment, fp32) the pieces go
 // through registers, and what reaches past a row's end becomes zero there.
 //
-// splits > 1: the parts of a tile's K go to workgroups of their own, which leave
-// partial tiles in the workspace; experts_join_kernel adds those in order.
+// Parts of a tile's K (`splits` of them, or chunks of an expert's rows in the
+// weight gradient) go to workgroups of their own, which leave partial tiles in
+// the workspace; experts_join_kernel adds those in order.
 #pragma once
 
 #include "device_common.hpp"
@@ -59,11 +60,14 @@ __device__ __forceinline__ int wave_prefix(int v) {
   return v;
 }
 
-// A tile of C: its expert and that one's rows, tile row and column within it.
+// A tile of C: its expert and that one's rows (or a chunk of them), tile row and
+// column within it.
 struct ExpertTile {
   int expert, begin, count, bi, bj;
-  int index;  // number of the tile
-  int split;  // part of its K
+  int64_t slot;  // partial tile that it leaves in the workspace; -1: C itself
+  int split;     // forward, input gradient: part of its K
+  int parts;     // joining: partial tiles, from slot on `stride` apart
+  int64_t stride;
 };
 
 // Workgroups are spread over the XCDs in chunks of S consecutive pieces of
@@ -87,65 +91,98 @@ __device__ __forceinline__ void experts_place(int w, int tilesM, int tilesN, int
   bj = in / gm;
 }
 
-// The tile of workgroup b; false if there is none.  JOIN: workgroups count tiles
-// alone, in order.
+// The tile of workgroup b; false if there is none.  JOIN: the b-th tile that was
+// left in parts.
+//   forward, input gradient: tiles of T rows of the experts; all in `splits` parts
+//   weight gradient: units of at most `chunk` rows of an expert; experts of
+//   several units leave parts
 template <int MODE, int T, bool JOIN> __device__ __forceinline__ bool experts_tile(const ExpertsArgs& a, int b, ExpertTile& t) {
+  constexpr bool DW = MODE == EX_DW;
   const int lane = threadIdx.x & 63;
-  const int splits = JOIN ? 1 : a.splits;
-  int tot, w, pre = 0, mine = 0, before = 0;
-  if constexpr (MODE == EX_DW) {
-    tot = a.experts * a.tilesM * a.tilesN;
-  } else {
-    int64_t sum = 0;
-    for (int c = 0; c < a.experts; c += 64) {
-      const int n = c + lane < a.experts ? experts_rows(a, c + lane).count : 0;
-      mine = (n + T - 1) / T;
-      pre = wave_prefix(mine);
-      sum += __builtin_amdgcn_readlane(pre, 63);
+  const int tiles = DW ? a.tilesM * a.tilesN : a.tilesN;  // of a unit, or of a tile row
+  // units or tile rows of the wave's 64 experts, and those in parts (joining: experts in parts)
+  ExpertRows r = {0, 0};
+  int mine = 0, pre = 0, cut = 0, cutpre = 0;
+  auto look = [&](int c) {
+    r = {0, 0};
+    if (c + lane < a.experts) r = experts_rows(a, c + lane);
+    mine = c + lane >= a.experts ? 0 : DW ? max(1, (r.count + a.chunk - 1) / a.chunk) : (r.count + T - 1) / T;
+    pre = wave_prefix(mine);
+    if constexpr (DW) {
+      cut = mine > 1 ? mine : 0;
+      cutpre = wave_prefix(cut);
     }
-    // more tile rows than the rows allow: the offsets go back, and the groups overlap
-    if (sum > a.rows / T + min(a.experts, a.rows)) return false;
-    tot = (int)sum * a.tilesN;
+  };
+  int64_t sum = 0;
+  for (int c = 0; c < a.experts; c += 64) {
+    look(c);
+    sum += __builtin_amdgcn_readlane(pre, 63);
   }
+  // more than the rows allow: the offsets go back, and the groups overlap
+  if (sum > (DW ? a.experts + a.rows / a.chunk : a.rows / T + min(a.experts, a.rows))) return false;
+  const int tot = (int)sum * tiles;
+  t.split = 0;
+  t.slot = -1;
+  int before = 0, cutbefore = 0;
+  if constexpr (DW && JOIN) {
+    int left = b / tiles;
+    for (int c = 0; c < a.experts; c += 64) {
+      if (a.experts > 64) look(c);
+      const uint64_t some = __ballot(cut > 0);
+      const int n = __popcll(some);
+      if (left < n) {
+        const int below = __popcll(some & ((1ull << lane) - 1));
+        const int l = __builtin_ctzll(__ballot((some >> lane & 1) && below == left));
+        t.expert = c + l;
+        t.parts = __builtin_amdgcn_readlane(cut, l);
+        const int in = b % tiles;
+        t.slot = (int64_t)(cutbefore + __builtin_amdgcn_readlane(cutpre, l) - t.parts) * tiles + in;
+        t.stride = tiles;
+        t.begin = t.count = 0;
+        experts_place(in, a.tilesM, a.tilesN, t.bi, t.bj);
+        return true;
+      }
+      left -= n;
+      cutbefore += __builtin_amdgcn_readlane(cutpre, 63);
+    }
+    return false;
+  }
+  const int splits = DW || JOIN ? 1 : a.splits;
   if (b >= tot * splits) return false;
-  w = JOIN ? b : experts_deal(b, tot * splits, 8 * a.tilesN);
+  int w = JOIN ? b : experts_deal(b, tot * splits, 8 * a.tilesN);
   t.split = __builtin_amdgcn_readfirstlane(w / tot);
   w = __builtin_amdgcn_readfirstlane(w % tot);
-  t.index = w;
-  int tilesM;
-  if constexpr (MODE == EX_DW) {
-    const int per = a.tilesM * a.tilesN;
-    t.expert = w / per;
-    w -= t.expert * per;
-    tilesM = a.tilesM;
-  } else {
-    t.expert = 0;
-    const int at = w / a.tilesN;  // tile row, counted over all experts
-    for (int c = 0; c < a.experts; c += 64) {
-      if (a.experts > 64) {  // otherwise they are still there
-        const int n = c + lane < a.experts ? experts_rows(a, c + lane).count : 0;
-        mine = (n + T - 1) / T;
-        pre = wave_prefix(mine);
-      }
-      const uint64_t past = __ballot(before + pre > at);
-      if (past) {
-        const int l = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
-        t.expert = c + l;
-        tilesM = __builtin_amdgcn_readlane(mine, l);
-        before += __builtin_amdgcn_readlane(pre, l) - tilesM;
-        break;
-      }
-      before += __builtin_amdgcn_readlane(pre, 63);
+  const int at = __builtin_amdgcn_readfirstlane(w / tiles);  // unit or tile row, counted over all experts
+  int unit = 0, units = 0, cuts = 0;
+  for (int c = 0; c < a.experts; c += 64) {
+    if (a.experts > 64) look(c);  // otherwise they are still there
+    const uint64_t past = __ballot(before + pre > at);
+    if (past) {
+      const int l = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
+      t.expert = c + l;
+      t.begin = __builtin_amdgcn_readlane(r.begin, l);
+      t.count = __builtin_amdgcn_readlane(r.count, l);
+      units = __builtin_amdgcn_readlane(mine, l);
+      unit = at - (before + __builtin_amdgcn_readlane(pre, l) - units);
+      if constexpr (DW) cuts = cutbefore + __builtin_amdgcn_readlane(cutpre, l) - units;
+      break;
     }
-    w -= before * a.tilesN;
+    before += __builtin_amdgcn_readlane(pre, 63);
+    if constexpr (DW) cutbefore += __builtin_amdgcn_readlane(cutpre, 63);
   }
-  experts_place(w, tilesM, a.tilesN, t.bi, t.bj);
-  t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+  if constexpr (DW) {
+    experts_place(w % tiles, a.tilesM, a.tilesN, t.bi, t.bj);
+    t.begin += unit * a.chunk;
+    t.count = min(a.chunk, t.count - unit * a.chunk);
+    if (units > 1) t.slot = (int64_t)(cuts + unit) * tiles + w % tiles;
+  } else {
+    experts_place(w - (at - unit) * tiles, units, a.tilesN, t.bi, t.bj);
+    if (a.splits > 1) t.slot = JOIN ? (int64_t)w * a.splits : (int64_t)w * a.splits + t.split;
+    t.parts = a.splits;
+    t.stride = 1;
+  }
   t.bi = __builtin_amdgcn_readfirstlane(t.bi);
   t.bj = __builtin_amdgcn_readfirstlane(t.bj);
-  const ExpertRows r = experts_rows(a, t.expert);
-  t.begin = __builtin_amdgcn_readfirstlane(r.begin);
-  t.count = __builtin_amdgcn_readfirstlane(r.count);
   return true;
 }
 
@@ -513,8 +550,8 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
       const f32x4 hi = *reinterpret_cast<const f32x4*>(sp + 4);
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       if (r < M && gj < a.N) {
-        if (a.splits > 1) {
-          float* o = a.ws + ((int64_t)t.index * a.splits + t.split) * (T * T) + (r - row0) * T + (gj - col0);
+        if (t.slot >= 0) {
+          float* o = a.ws + t.slot * (T * T) + (r - row0) * T + (gj - col0);
           *as_global(reinterpret_cast<f32x4*>(o)) = lo;
           *as_global(reinterpret_cast<f32x4*>(o + 4)) = hi;
         } else {
@@ -543,20 +580,12 @@ void experts_kernel(const ExpertsArgs a) {
   // experts of 1408 x 2048, 49152 rows lose a tenth of their work to edges
   // instead of a quarter
   const bool low = (MODE == EX_DW ? a.M : t.count) - t.bi * T <= T / 2;
-  if constexpr (T == 256) {
-    const bool narrow = a.N - t.bj * T <= T / 2;
-    if (low && narrow) experts_compute<MODE, T, 2, 1, DIRECT, TI, TO>(a, t, ring);
-    else if (low) experts_compute<MODE, T, 2, 2, DIRECT, TI, TO>(a, t, ring);
-    else if (narrow) experts_compute<MODE, T, 4, 1, DIRECT, TI, TO>(a, t, ring);
-    else experts_compute<MODE, T, 4, 2, DIRECT, TI, TO>(a, t, ring);
-  } else {
-    if (low) experts_compute<MODE, T, 1, 1, DIRECT, TI, TO>(a, t, ring);
-    else experts_compute<MODE, T, 2, 1, DIRECT, TI, TO>(a, t, ring);
-  }
+  if (low) experts_compute<MODE, T, 1, 1, DIRECT, TI, TO>(a, t, ring);
+  else experts_compute<MODE, T, 2, 1, DIRECT, TI, TO>(a, t, ring);
 }
 
-// Adds the partial tiles of a split product in order.  8 columns per thread,
-// T * T / 2048 workgroups per tile.  Parts without stages were written as zeros.
+// Adds the partial tiles of a tile in order.  8 columns per thread, T * T / 2048
+// workgroups per tile.  Parts without stages were written as zeros.
 template <int MODE, int T, typename TO> __global__ __launch_bounds__(256) void experts_join_kernel(const ExpertsArgs a) {
   constexpr int WGS = T * T / 2048;
   ExpertTile t;
@@ -564,13 +593,13 @@ template <int MODE, int T, typename TO> __global__ __launch_bounds__(256) void e
   const int in = (int)(blockIdx.x % WGS) * 2048 + threadIdx.x * 8;  // first value within the tile
   const int r = t.bi * T + in / T, c = t.bj * T + in % T;
   if (r >= (MODE == EX_DW ? a.M : t.count) || c >= a.N) return;
-  const float* w = a.ws + (int64_t)t.index * a.splits * (T * T) + in;
+  const float* w = a.ws + t.slot * (T * T) + in;
   float v[8] = {};
 #pragma unroll 4
-  for (int z = 0; z < a.splits; ++z)
+  for (int z = 0; z < t.parts; ++z)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(w + (int64_t)z * (T * T) + 4 * h));
+      const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(w + z * t.stride * (T * T) + 4 * h));
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * h + e] += x[e];
     }

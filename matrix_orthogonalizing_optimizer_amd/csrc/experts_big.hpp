@@ -205,6 +205,17 @@ __device__ __forceinline__ int lds_read_uniform(const int* p) {
   return __builtin_amdgcn_readfirstlane(r);
 }
 
+// The workgroup's barrier without the waits of __syncthreads(), which are for all
+// memory instructions under way, the stores of the tile before among them.
+// What has to be complete has been waited for in front of it.
+__device__ __forceinline__ void big_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
 template <int MODE, typename TO>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void experts_big_kernel(const ExpertsArgs a) {
@@ -334,7 +345,7 @@ void experts_big_kernel(const ExpertsArgs a) {
   constexpr int ST = sizeof(TO) / 2;
   const bool pieces = !(MODE == EX_DW && a.accumulate) && a.N % 8 == 0 && a.ldo % 8 == 0 &&
                       (MODE != EX_DW || a.se % 8 == 0) && (uintptr_t)a.o % 16 == 0;
-  int stores = 0;  // of the tile before, if their number is known
+  bool stored = false;  // the tile before was written so
   ExpertsItem now = item(k0);
   auto tile = [&](const ExpertsItem& t, int nst, auto mc, auto nc) __attribute__((always_inline)) {
     constexpr int MA = decltype(mc)::value, NA = decltype(nc)::value;  // 32 x 32 blocks of a wave along M and N
@@ -405,14 +416,13 @@ void experts_big_kernel(const ExpertsArgs a) {
         }
         // the next stage is whole and this wave is done reading this one; after
         // the barrier that holds for every wave
-        // The stores of the tile before were issued after this stage's copies: they
-        // may still be under way.
-        if (v == 0 && stores == 8 * ST) wait_vmcnt_lgkm0<8 * ST>();
-        else if (v == 0 && stores == 16 * ST) wait_vmcnt_lgkm0<16 * ST>();
-        else wait_vmcnt_lgkm0<0>();
+        // The stores of the tile before, 8 ST of a wave or more, were issued after the
+        // copies of the next stage: as many may still be under way.
+        wait_vmcnt<8 * ST>();
+        if (v > 0 || !stored) wait_vmcnt<0>();
+        wait_lgkm0();
         post();
-        __syncthreads();
-        __builtin_amdgcn_sched_barrier(0);
+        big_barrier();
 #pragma unroll
         for (int p = 0; p < NPAIR; ++p) {
           mfma_pair(p, 1);
@@ -469,7 +479,8 @@ void experts_big_kernel(const ExpertsArgs a) {
         off += step;
         asm volatile("" : "+v"(off));  // one register, not one per strip
       });
-      stores = 4 * MA * ST;
+      static_assert(4 * MA >= 8, "strips of a tile");
+      stored = true;
     } else {
       int r = wm * (32 * MA) + dr0;
       each_strip([&](const f32x4& lo, const f32x4& hi) __attribute__((always_inline)) {
@@ -493,7 +504,7 @@ void experts_big_kernel(const ExpertsArgs a) {
         r += SROWS;
         asm volatile("" : "+v"(r));
       });
-      stores = 0;
+      stored = false;
     }
   };
 
@@ -508,7 +519,7 @@ void experts_big_kernel(const ExpertsArgs a) {
   }
   wait_vmcnt_lgkm0<0>();
   post();
-  __syncthreads();
+  big_barrier();
   while (queued > 0) {
     const ExpertsItem t = now;
     q0 = q1;

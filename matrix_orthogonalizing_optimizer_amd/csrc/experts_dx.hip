@@ -2,7 +2,7 @@
 #include "experts_inst.hpp"
 
 namespace muon {
-hipError_t launch_experts_dx(bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s) {
-  return experts_any<EX_DX>(direct, dt, odt, tiles, a, s);
+hipError_t launch_experts_dx(bool direct, int dt, int odt, int64_t tiles, int64_t joined, const ExpertsArgs& a, hipStream_t s) {
+  return experts_any<EX_DX>(direct, dt, odt, tiles, joined, a, s);
 }
 }  // namespace muon

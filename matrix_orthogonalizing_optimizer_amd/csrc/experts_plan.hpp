@@ -16,7 +16,8 @@ struct ExpertsPlan {
   bool big;       // 256 x 256 tiles from lists
   int tile, splits;
   int64_t tiles;  // most that any offsets need
-  int64_t chunk;  // big, weight gradient: rows of an expert summed at once
+  int64_t joined; // of them, those that are left in parts
+  int64_t chunk;  // weight gradient: rows of an expert summed at once
   int64_t cap;    // big: room of a list
   size_t items_off, ws_off;  // workspace: lists, partial tiles
   size_t bytes;
@@ -60,11 +61,21 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
     return p;
   }
   const int64_t bk = dtype == MUON_F32 ? 32 : 64;
-  const int64_t K = pass == MUON_EXPERTS_FORWARD ? in : pass == MUON_EXPERTS_INPUT_GRAD ? out : (rows + some - 1) / std::max<int64_t>(some, 1);
+  if (dw) {
+    // the same for tiles of 128, two workgroups on a CU
+    const int64_t mine = ((out + 127) / 128) * ((N + 127) / 128);
+    p.chunk = bk * std::max<int64_t>(8, ((rows + bk - 1) / bk) * mine / 512);
+    p.tiles = (experts + rows / p.chunk) * mine;
+    p.joined = rows / p.chunk * mine;
+    p.bytes = p.joined ? (size_t)(2 * p.joined) * 128 * 128 * sizeof(float) + WS_ALIGN : 0;
+    return p;
+  }
+  const int64_t K = pass == MUON_EXPERTS_FORWARD ? in : out;
   const int64_t stages = (K + bk - 1) / bk, n = std::max<int64_t>(1, tiles(p.tile));
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / n, stages / 4, 32}));
   p.tiles = most(p.tile) * ((N + p.tile - 1) / p.tile);
-  p.bytes = p.splits > 1 ? (size_t)p.tiles * (size_t)p.splits * (size_t)(p.tile * p.tile) * sizeof(float) + WS_ALIGN : 0;
+  p.joined = p.splits > 1 ? p.tiles : 0;
+  p.bytes = p.joined ? (size_t)p.joined * (size_t)p.splits * 128 * 128 * sizeof(float) + WS_ALIGN : 0;
   return p;
 }
 

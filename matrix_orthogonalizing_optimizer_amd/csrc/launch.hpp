@@ -50,13 +50,13 @@ hipError_t launch_linear8_dx(int tile, bool expanded, bool dy_f32, int odt, cons
 
 // Products grouped by expert.  dt, odt: dtypes of the operands and of the
 // result; direct: bf16 rows of whole 16-byte pieces; tiles: most that any
-// offsets need.
-hipError_t launch_experts_y(bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
+// offsets need (before they are split); joined: of them, those left in parts.
+hipError_t launch_experts_y(bool direct, int dt, int odt, int64_t tiles, int64_t joined, const ExpertsArgs& a, hipStream_t s);
 hipError_t launch_experts_big_y(int odt, const ExpertsArgs& a, hipStream_t s);  // tiles from lists (experts_big.hpp)
 hipError_t launch_experts_big_dw(int odt, const ExpertsArgs& a, hipStream_t s);
 hipError_t launch_experts_big_dx(int odt, const ExpertsArgs& a, hipStream_t s);
 hipError_t launch_experts_few(int dt, int odt, const ExpertsArgs& a, hipStream_t s);  // forward, few rows an expert
-hipError_t launch_experts_dw(bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
-hipError_t launch_experts_dx(bool direct, int dt, int odt, int64_t tiles, const ExpertsArgs& a, hipStream_t s);
+hipError_t launch_experts_dw(bool direct, int dt, int odt, int64_t tiles, int64_t joined, const ExpertsArgs& a, hipStream_t s);
+hipError_t launch_experts_dx(bool direct, int dt, int odt, int64_t tiles, int64_t joined, const ExpertsArgs& a, hipStream_t s);
 
 }  // namespace muon
