@@ -13,9 +13,8 @@
 // of an expert (one unit for an expert without rows).  Offsets are clamped to 0 .. rows, so no value of theirs
 // leads outside the operands.
 //
-// A workgroup of 8 waves owns a T x T tile of C (T = 256: 128 x 64 outputs per
-// wave, one workgroup per CU; T = 128: 64 x 32 per wave, two) and walks K in
-// stages of 128 bytes per row: 64 values of bf16, 32 of fp32.  Two stages live
+// A workgroup of 8 waves owns a T x T tile of C (T = 128: 64 x 32 outputs per wave,
+// two workgroups per CU) and walks K in stages of 128 bytes per row: 64 values of bf16, 32 of fp32.  Two stages live
 // in LDS.  v_mfma_f32_32x32x16_bf16, or v_mfma_f32_32x32x2_f32.
 //
 // An operand lies row-major (K contiguous: x and w of EX_Y, dy of EX_DX) or
@@ -198,20 +197,20 @@ template <int MODE, int BK> __device__ __forceinline__ void experts_stages(const
 // A 16-byte piece of a row at column c, through registers.  load() takes the
 // row's last piece where c reaches past its end, settle() moves its own
 // elements to the front and clears the others (all of them where !ok), so no
-// branch stands behind the load.  Rows shorter than a piece are loaded element by
-// element.
-template <typename T> struct Piece {
+// branch stands behind the load.  SHORT: rows shorter than a piece, element by
+// element (with both in one loop the loads of a stage cost 3 - 15% more).
+template <typename T, bool SHORT> struct Piece {
   static constexpr int PER = 16 / sizeof(T);
   u32x4 w;
   __device__ __forceinline__ void load(const T* row, int c, int cols) {
-    if (cols >= PER) {
+    if constexpr (!SHORT) {
       const T* p = row + min(c, cols - PER);
       if constexpr (sizeof(T) == 2) w = as_global(reinterpret_cast<const u32x4_e2*>(p))->v;
       else w = __builtin_bit_cast(u32x4, as_global(reinterpret_cast<const f32x4_e4*>(p))->v);
     } else {
       w = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int e = 0; e < PER - 1; ++e)
+      for (int e = 0; e < PER; ++e)
         if (c + e < cols) {
           if constexpr (sizeof(T) == 2) w[e >> 1] |= (uint32_t)as_global(reinterpret_cast<const uint16_t*>(row))[c + e] << (16 * (e & 1));
           else w[e] = as_global(reinterpret_cast<const uint32_t*>(row))[c + e];
@@ -219,7 +218,7 @@ template <typename T> struct Piece {
     }
   }
   __device__ __forceinline__ void settle(int c, int cols, bool ok) {
-    const int over = cols >= PER ? max(c + PER - cols, 0) : 0;
+    const int over = SHORT ? 0 : max(c + PER - cols, 0);
     const int off = ok ? min(over, PER) : PER;  // elements to drop at the front
     if (__ballot(off != 0) == 0) return;
     const int regs = off * (int)sizeof(T) / 4;
@@ -291,7 +290,7 @@ template <int NA, int NB, int IA, int IB, typename P> __device__ __forceinline__
 
 // One tile, of which the first 64 MA rows and 128 NA columns are computed (the
 // others lie outside C): MA, NA are the 32 x 32 blocks of a wave along M and N.
-template <int MODE, int T, int MA, int NA, bool DIRECT, typename TI, typename TO>
+template <int MODE, int T, int MA, int NA, bool DIRECT, bool SHORT, typename TI, typename TO>
 __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const ExpertTile& t, u32x4 (*ring)[2 * T * 8]) {
   constexpr int NW = 8;
   constexpr bool AKM = MODE == EX_DW;      // A lies K-major
@@ -371,7 +370,7 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   };
 
   // ---- the same chunks through registers
-  Piece<TI> pa[DIRECT ? 1 : NQ], pb[DIRECT ? 1 : NQ];
+  Piece<TI, SHORT> pa[DIRECT ? 1 : NQ], pb[DIRECT ? 1 : NQ];
   auto load_pieces = [&](int ks) {
     if constexpr (!DIRECT) {
 #pragma unroll
@@ -387,7 +386,7 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   auto write_pieces = [&](int q, int v, int ks) {  // q < NQ: A, else B
     if constexpr (!DIRECT) {
       const int i = q < NQ ? q : q - NQ;
-      Piece<TI>& p = q < NQ ? pa[i] : pb[i];
+      Piece<TI, SHORT>& p = q < NQ ? pa[i] : pb[i];
       if (q < NQ ? AKM : BKM)
         p.settle((q < NQ ? row0 : col0) + km_col(i), q < NQ ? M : a.N, ks * BK + km_row(i) < K);
       else
@@ -580,8 +579,16 @@ void experts_kernel(const ExpertsArgs a) {
   // experts of 1408 x 2048, 49152 rows lose a tenth of their work to edges
   // instead of a quarter
   const bool low = (MODE == EX_DW ? a.M : t.count) - t.bi * T <= T / 2;
-  if (low) experts_compute<MODE, T, 1, 1, DIRECT, TI, TO>(a, t, ring);
-  else experts_compute<MODE, T, 2, 1, DIRECT, TI, TO>(a, t, ring);
+  if constexpr (!DIRECT) {
+    // one operand's rows are shorter than a 16-byte piece
+    constexpr int PER = 16 / (int)sizeof(TI);
+    if ((MODE != EX_Y && a.N < PER) || (MODE == EX_DW ? a.M : a.K) < PER) {
+      experts_compute<MODE, T, 2, 1, false, true, TI, TO>(a, t, ring);
+      return;
+    }
+  }
+  if (low) experts_compute<MODE, T, 1, 1, DIRECT, false, TI, TO>(a, t, ring);
+  else experts_compute<MODE, T, 2, 1, DIRECT, false, TI, TO>(a, t, ring);
 }
 
 // Adds the partial tiles of a tile in order.  8 columns per thread, T * T / 2048

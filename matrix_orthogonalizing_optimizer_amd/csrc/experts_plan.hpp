@@ -50,7 +50,13 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   // an expert with more rows than a CU sums over all is cut
   const int64_t share = (rows + 63) / 64 * per / 256;
   p.chunk = 64 * std::max<int64_t>(8, share);
-  p.big = direct && tiles(256) >= 192 && experts + (dw ? rows / p.chunk : 0) <= 2048;
+  // 256 x 256 tiles where there is about one for every CU.  us, against tiles of 128:
+  // forward 4096 rows of 8 experts of 1408 x 2048, 120 tiles 43 and 34; weight
+  // gradient 4096 rows of 8 of 512 x 1024, 64 tiles 34 and 25; from about 260 on
+  // ahead: forward 16384 rows of 8 of 4096 x 4096 497 and 587, weight gradient 1024
+  // rows of 2 of 4096 x 4096, 512 tiles 46 and 61, 4096 rows of 64 of 1408 x 2048 103
+  // and 176 (but the forward product of the latter 120 and 102).
+  p.big = direct && tiles(256) >= 240 && experts + (dw ? rows / p.chunk : 0) <= 2048;
   if (p.big) {
     p.tile = 256;
     p.tiles = dw ? (experts + rows / p.chunk) * per : most(256) * ((N + 255) / 256);
@@ -60,11 +66,12 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
     p.bytes = p.ws_off + (dw ? (size_t)(2 * (rows / p.chunk) * per) * 256 * 256 * sizeof(float) : 0) + WS_ALIGN;
     return p;
   }
-  const int64_t bk = dtype == MUON_F32 ? 32 : 64;
+  // tiles of 128: two workgroups on a CU
+  const int64_t bk = dtype == MUON_F32 ? 32 : 64, slots = 512;
   if (dw) {
-    // the same for tiles of 128, two workgroups on a CU
+    // units as above
     const int64_t mine = ((out + 127) / 128) * ((N + 127) / 128);
-    p.chunk = bk * std::max<int64_t>(8, ((rows + bk - 1) / bk) * mine / 512);
+    p.chunk = bk * std::max<int64_t>(8, ((rows + bk - 1) / bk) * mine / slots);
     p.tiles = (experts + rows / p.chunk) * mine;
     p.joined = rows / p.chunk * mine;
     p.bytes = p.joined ? (size_t)(2 * p.joined) * 128 * 128 * sizeof(float) + WS_ALIGN : 0;
@@ -72,7 +79,7 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   }
   const int64_t K = pass == MUON_EXPERTS_FORWARD ? in : out;
   const int64_t stages = (K + bk - 1) / bk, n = std::max<int64_t>(1, tiles(p.tile));
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / n, stages / 4, 32}));
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({slots / n, stages / 4, 32}));
   p.tiles = most(p.tile) * ((N + p.tile - 1) / p.tile);
   p.joined = p.splits > 1 ? p.tiles : 0;
   p.bytes = p.joined ? (size_t)p.joined * (size_t)p.splits * 128 * 128 * sizeof(float) + WS_ALIGN : 0;

@@ -311,3 +311,13 @@ def test_same_result_every_time():
     first = mo.muon_experts_weight_grad(dy, x, off)
     for _ in range(3):
         assert torch.equal(first, mo.muon_experts_weight_grad(dy, x, off))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(300, 3, 3, 129), (300, 3, 129, 3), (500, 2, 1, 300), (500, 2, 300, 5), (400, 2, 8, 7),
+                                   (400, 2, 7, 8), (5000, 3, 2, 2)])
+def test_one_width_shorter_than_a_piece(shape, dtype):
+    """One operand's rows are shorter than 16 bytes, the other's are not."""
+    print("experts short rows", shape, dtype, flush=True)
+    run_all(*shape, dtype, split_rows(shape[0], shape[1], 2, lead=1), 5, (1, 2, 3), (3, 2, 1), what=shape)
+    run_all(*shape, dtype, split_rows(shape[0], shape[1], 2), 5, what=shape)
