@@ -16,7 +16,7 @@ template <int T, int CG, int U, bool WHOLE, typename TI> hipError_t go(int odt, 
 // Two tiles of rows and two groups of channels read the rows half as often, and
 // leave enough workgroups where the channels of all experts make 512 (us, one
 // of each against two: 64 experts of 1408 x 2048, 384 rows 82 and 76, 1024 rows
-// 131 and 103; but 64 rows, one an expert, 38 and 39, 16 rows of one expert of
+// 131 and 103, before experts of at most 16 rows left the second tile out; but 64 rows, one an expert, 38 and 39, 16 rows of one expert of
 // 768 x 768 6.0 and 7.5).  Where they do not, 4 tiles of rows from 8 rows an
 // expert up (256 rows over 16 experts of 512 x 513: 25 and 14 us).
 template <bool WHOLE, typename TI> hipError_t few(int odt, const ExpertsArgs& a, hipStream_t s) {
