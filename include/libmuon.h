@@ -566,10 +566,12 @@ muon_status muon_linear8_workspace_bytes(int32_t pass, int64_t tokens, int64_t o
  * exact and summed in fp32; fp32 is multiplied and summed in fp32.
  * With in == 0 y is zero, with out == 0 dx is zero, with rows == 0 dW is zero
  * (or what it had).
- * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative or above 2^30, experts
+ * The results overlap no operand, and calls that may run at the same time (two
+ * streams, two graphs) have workspaces of their own.
+ * Errors: MUON_E_DTYPE; MUON_E_SHAPE (a size negative, rows above 2^30, experts
  * above 2^16, a leading dimension below its column count or above 2^21, a
- * stride whose experts overlap or above 2^42, a result of more than 2^22
- * tiles of 128 x 128 or 256 x 256); MUON_E_ARG (a pointer null or not aligned
+ * stride whose experts overlap or above 2^42, a result that may take more than
+ * 2^22 tiles of 128 x 128); MUON_E_ARG (a pointer null or not aligned
  * to its element); MUON_E_WORKSPACE (smaller than
  * muon_experts_workspace_bytes); MUON_E_HIP. */
 typedef enum {
@@ -589,8 +591,10 @@ muon_status muon_experts_weight_grad(const void* dy, int64_t lddy, const void* x
                                      int64_t rows, int64_t experts, int64_t out, int64_t in, int32_t dtype, void* dw,
                                      int64_t lddw, int64_t stride, int32_t dw_dtype, int32_t accumulate,
                                      void* workspace, size_t workspace_bytes, void* stream);
-/* Bytes of workspace of one pass (muon_experts_pass), host only; 0 for products
- * that fill the GPU by themselves.  Errors: MUON_E_METHOD (unknown pass),
+/* Bytes of workspace of one pass (muon_experts_pass), host only, whatever the
+ * operands' alignment: partial sums of products whose tiles are too few or too
+ * unequal to fill the GPU, lists of the tiles of large ones, or 0.  Not an error
+ * where out, in or rows is 0.  Errors: MUON_E_METHOD (unknown pass),
  * MUON_E_DTYPE, MUON_E_SHAPE, MUON_E_ARG. */
 muon_status muon_experts_workspace_bytes(int32_t pass, int64_t rows, int64_t experts, int64_t out, int64_t in,
                                          int32_t dtype, size_t* bytes);

@@ -143,7 +143,8 @@ def lib():
                                            vp]
     L.muon_experts_workspace_bytes.argtypes = [i32, i64, i64, i64, i64, i32, ctypes.POINTER(sz)]
     for n in ("muon_experts_forward", "muon_experts_weight_grad", "muon_experts_input_grad",
-              "muon_experts_workspace_bytes", "muon_adamw8_state_bytes", "muon_adamw8_pack", "muon_adamw8_unpack", "muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
+              "muon_experts_workspace_bytes", "muon_adamw8_state_bytes", "muon_adamw8_pack", "muon_adamw8_unpack",
+              "muon_rows8_quantize", "muon_rows8_dequantize", "muon_norm_forward", "muon_norm_backward",
               "muon_norm_backward_workspace_bytes", "muon_linear8_forward", "muon_linear8_weight_grad",
               "muon_linear8_input_grad", "muon_linear8_workspace_bytes"):
         getattr(L, n).restype = i32

@@ -45,7 +45,8 @@ muon_status experts_pass(int pass, const Matrix& r, const Matrix& s, int64_t str
   const bool dw = pass == MUON_EXPERTS_WEIGHT_GRAD;
   if (!dtype_ok(dtype) || !dtype_ok(odtype)) return MUON_E_DTYPE;
   const int64_t ocols = pass == MUON_EXPERTS_FORWARD ? out : in;
-  if (!side_ok(rows) || !side_ok(out) || !side_ok(in) || experts < 0 || experts > MAX_EXPERTS || !ld_ok(r.ld, r.cols) ||
+  if (!side_ok(rows) || out < 0 || out > MAX_LD || in < 0 || in > MAX_LD || experts < 0 || experts > MAX_EXPERTS ||
+      !ld_ok(r.ld, r.cols) ||
       !ld_ok(s.ld, s.cols) || !ld_ok(ldo, ocols) || stride > MAX_STRIDE)
     return MUON_E_SHAPE;
   // experts of w may not overlap in dw, and their rows lie in order
@@ -54,7 +55,7 @@ muon_status experts_pass(int pass, const Matrix& r, const Matrix& s, int64_t str
   const bool empty = dw ? rows == 0 : (pass == MUON_EXPERTS_FORWARD ? in : out) == 0;  // sums over nothing
   if (!at(offsets, 4) || !at(o, esize(odtype)) || (!empty && (!at(r.p, esize(dtype)) || !at(s.p, esize(dtype)))))
     return MUON_E_ARG;
-  const bool direct = dtype == MUON_BF16 && pieces(r.p, r.cols, r.ld) && pieces(s.p, s.cols, s.ld) &&
+  const bool direct = !empty && dtype == MUON_BF16 && pieces(r.p, r.cols, r.ld) && pieces(s.p, s.cols, s.ld) &&
                       (dw || stride % 8 == 0);
   const ExpertsPlan p = experts_plan(pass, rows, experts, out, in, dtype, direct);
   if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MUON_E_WORKSPACE;
@@ -107,7 +108,9 @@ muon_status muon_experts_workspace_bytes(int32_t pass, int64_t rows, int64_t exp
   if (!bytes) return MUON_E_ARG;
   if (pass < MUON_EXPERTS_FORWARD || pass > MUON_EXPERTS_INPUT_GRAD) return MUON_E_METHOD;
   if (!dtype_ok(dtype)) return MUON_E_DTYPE;
-  if (!side_ok(rows) || !side_ok(out) || !side_ok(in) || experts < 0 || experts > MAX_EXPERTS) return MUON_E_SHAPE;
+  // (a width is a leading dimension's least)
+  if (!side_ok(rows) || out < 0 || out > MAX_LD || in < 0 || in > MAX_LD || experts < 0 || experts > MAX_EXPERTS)
+    return MUON_E_SHAPE;
   // whichever way the operands are aligned
   *bytes = experts && out && in && rows
                ? std::max(experts_plan(pass, rows, experts, out, in, dtype, dtype == MUON_BF16).bytes,

@@ -28,7 +28,7 @@ namespace muon {
 
 constexpr int BIG_T = 256;
 constexpr int BIG_EXPERTS = 2048;  // experts of a large product, at most: their sums lie in LDS
-constexpr int BIG_UNITS = 2048;    // the same for pieces of experts
+constexpr int BIG_UNITS = 2048;    // the same for experts + rows / chunk
 
 // Inclusive prefix sums of the workgroup's 256 values; *total their sum.
 __device__ __forceinline__ int block_prefix(int v, int* wave_sums, int* total) {
@@ -134,8 +134,11 @@ template <int MODE> __global__ __launch_bounds__(256) void experts_list_kernel(c
       const int pre = block_prefix(k, wave_sums, &tot);
       const int prep = block_prefix(k > 1 ? k : 0, wave_sums, &totp);
       const int pres = block_prefix(k > 1, wave_sums, &tots);
-      if (units + tot > BIG_UNITS || split + tots > EXPERTS_SPLIT || parts + totp > 2 * (a.rows / a.chunk)) {
-        // more than the rows allow: the offsets go back
+      // More units than the rows allow: the offsets go back.  Within this there are no
+      // more partial ones than 2 (rows / chunk) and no more experts in parts than
+      // rows / chunk, as those have two units or more; lists and workspace have
+      // room for them.
+      if (units + tot > a.experts + a.rows / a.chunk || split + tots > EXPERTS_SPLIT) {
         if (tid == 0) {
           a.head->count[x] = 0;
           if (x == 0) a.head->splits = 0;

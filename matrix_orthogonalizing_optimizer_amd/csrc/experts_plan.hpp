@@ -23,7 +23,8 @@ struct ExpertsPlan {
   size_t bytes;
 };
 
-// direct: all operands are bf16 rows of whole 16-byte pieces.
+// direct: all operands are bf16 rows of whole 16-byte pieces.  out and in are 2^21
+// at most, so that no product here overflows.
 inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t out, int64_t in, int32_t dtype,
                                 bool direct) {
   const bool dw = pass == MUON_EXPERTS_WEIGHT_GRAD;
@@ -41,7 +42,7 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   // 768 x 768, 80 rows 10.3 and 11.2; odd widths: 8 of 1023 x 1025, 60 rows 14.9 and
   // 17.1, 100 rows 23 and 18).
   const bool dear = dtype == MUON_F32 || (direct && some * ((out + 31) / 32) < 512);
-  p.few = pass == MUON_EXPERTS_FORWARD && some <= 65535 && (rows <= (dear ? 24 : 12) * some || rows <= 64);
+  p.few = pass == MUON_EXPERTS_FORWARD && some <= 65535 && (out + 15) / 16 * some <= 1 << 22 && (rows <= (dear ? 24 : 12) * some || rows <= 64);
   if (p.few) {
     p.tiles = (out + 15) / 16 * some;
     return p;

@@ -124,3 +124,17 @@ def test_binding_refusals():
     for bad in ((dy[:, :5], w, off), (dy.bfloat16(), w, off), (dy, w, off)):
         with pytest.raises(ValueError):
             mo.muon_experts_input_grad(*bad)
+
+
+def test_widths_past_a_leading_dimension():
+    """2^21 is the most a row can be apart, so wider matrices are refused, by the
+    query too (whose counts of tiles would not fit 64 bits)."""
+    L = _lib()
+    b = ctypes.c_size_t()
+    for kind in range(3):
+        for wide in ((1 << 30, 1 << 16, 1 << 30, 1 << 30), (1 << 30, 1, (1 << 21) + 1, 8), (9, 1, 8, (1 << 21) + 1)):
+            for dtype in (0, 1):
+                assert L.muon_experts_workspace_bytes(kind, *wide, dtype, ctypes.byref(b)) == E_SHAPE
+        for dtype in (0, 1):
+            assert L.muon_experts_workspace_bytes(kind, 1 << 30, 1 << 16, 1 << 21, 1 << 21, dtype, ctypes.byref(b)) == 0
+    assert L.muon_experts_forward(*dict(F, out=(1 << 21) + 8, ldy=(1 << 21) + 8, stride=1 << 40).values()) == E_SHAPE

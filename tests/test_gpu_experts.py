@@ -321,3 +321,55 @@ def test_one_width_shorter_than_a_piece(shape, dtype):
     print("experts short rows", shape, dtype, flush=True)
     run_all(*shape, dtype, split_rows(shape[0], shape[1], 2, lead=1), 5, (1, 2, 3), (3, 2, 1), what=shape)
     run_all(*shape, dtype, split_rows(shape[0], shape[1], 2), 5, what=shape)
+
+
+def test_sums_over_nothing_need_no_workspace():
+    """No rows at all in the weight gradient (a rank that got no tokens), no inputs
+    in the forward product, no outputs in the other, at sizes of large products."""
+    print("experts sums over nothing", flush=True)
+    d = dev()
+    e, out, in_ = 40, 1408, 2048
+    off = torch.zeros(e + 1, dtype=torch.int32, device=d)
+    none = torch.empty(0, dtype=torch.uint8, device=d)
+    for dt in (BF, F32):
+        dw = torch.full((e, out, in_), 3.0, dtype=dt, device=d)
+        dy, x = torch.empty(0, out, dtype=dt, device=d), torch.empty(0, in_, dtype=dt, device=d)
+        mo.muon_experts_weight_grad(dy, x, off, dw=dw, accumulate=True)
+        assert (dw == 3).all()
+        mo.muon_experts_weight_grad(dy, x, off, dw=dw, workspace=none)
+        assert not dw.any()
+        rows = 9000
+        off2 = split_rows(rows, e, 1)
+        y = mo.muon_experts_forward(torch.empty(rows, 0, dtype=dt, device=d), torch.empty(e, out, 0, dtype=dt, device=d), off2)
+        dx = mo.muon_experts_input_grad(torch.empty(rows, 0, dtype=dt, device=d), torch.empty(e, 0, in_, dtype=dt, device=d), off2)
+        assert not y.any() and not dx.any()
+
+
+@pytest.mark.parametrize("back", [(0, 40000, 0, 30000), (0, 30000, 10000, 40000, 5000, 39000), (39000, 40000, 0, 40000),
+                                  (0, 20000, 15000, 40000)])
+def test_offsets_that_go_back_in_a_large_product(back):
+    """Groups that overlap, at sizes of the large products: whatever the results,
+    nothing outside dw and the workspace is written, and the next call is right."""
+    print("experts offsets back", back, flush=True)
+    d = dev()
+    rows, e, out, in_ = 40000, 30, 2560, 520
+    gen = torch.Generator(device=d).manual_seed(1)
+    whole = lambda *s: torch.randint(-3, 4, s, generator=gen, device=d).to(BF)
+    x, w, dy = whole(rows, in_), whole(e, out, in_), whole(rows, out)
+    n = [mo.muon_experts_workspace_bytes(k, rows, e, out, in_, mo.MUON_BF16) for k in range(3)]
+    ws = [torch.full((b + 4096,), 91, dtype=torch.uint8, device=d) for b in n]
+    guard = lambda r, c: torch.full((r + 2, c), 7.0, dtype=BF, device=d)
+    y, dx, dw = guard(rows, out), guard(rows, in_), guard(e * out, in_)
+    bad = torch.tensor(list(back) + [rows] * (e + 1 - len(back)), dtype=torch.int32, device=d)
+    good = split_rows(rows, e, 3)
+    for off in (bad, good):
+        mo.muon_experts_forward(x, w, off, y=y[1:-1], workspace=ws[0][:n[0]])
+        mo.muon_experts_weight_grad(dy, x, off, dw=dw[1:-1], workspace=ws[1][:n[1]])
+        mo.muon_experts_input_grad(dy, w, off, dx=dx[1:-1], workspace=ws[2][:n[2]])
+        torch.cuda.synchronize()
+        for b, t in zip(n, ws):
+            assert b > 0 and (t[b:] == 91).all(), b
+        for t in (y, dx, dw):
+            assert (t[0] == 7).all() and (t[-1] == 7).all()
+    for g, a, b in R.groups(good.tolist(), rows):
+        assert torch.equal(dw[1:-1].view(e, out, in_)[g], (dy[a:b].double().t().contiguous() @ x[a:b].double()).to(BF)), g
