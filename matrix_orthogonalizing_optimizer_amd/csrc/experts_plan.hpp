@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 
@@ -74,9 +75,27 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   // tiles of 128: two workgroups on a CU
   const int64_t bk = dtype == MUON_F32 ? 32 : 64, slots = 512;
   if (dw) {
-    // units as above
+    // Units as above, of 12 stages at least (us, against 8: 1000 rows of 2 experts of
+    // 1024 x 1024 14 and 18, 49152 of one of 64 x 64 20 and 21, 10000 of 4 of 300 x 300
+    // 23 and 22).  fp32 products fill the time of a CU: of 8 to 16, or of one to two
+    // times its share, the stages of a unit with which the busiest CU has the least
+    // to do (8, 12 and 16: 3001 rows of 7 of 513 x 767 53, 70 and 75; 2000 of 2 of
+    // 768 x 768 52, 43 and 49).
     const int64_t mine = ((out + 127) / 128) * ((N + 127) / 128);
-    p.chunk = bk * std::max<int64_t>(8, ((rows + bk - 1) / bk) * mine / slots);
+    int64_t unit = std::max<int64_t>(dtype == MUON_F32 ? 8 : 12, ((rows + bk - 1) / bk) * mine / slots);
+    if (dtype == MUON_F32) {
+      const int64_t from = unit, step = std::max<int64_t>(1, from / 16);
+      double least = 0.0;
+      for (int64_t s = from; s <= 2 * from; s += step) {
+        const double units = (double)rows / (double)(bk * s) + 0.5 * (double)experts;  // the last ones half full
+        const double work = std::ceil(units * (double)mine / 256.0) * (double)(s + 2);
+        if (s == from || work < least) {
+          least = work;
+          unit = s;
+        }
+      }
+    }
+    p.chunk = bk * unit;
     p.tiles = (experts + rows / p.chunk) * mine;
     p.joined = rows / p.chunk * mine;
     p.bytes = p.joined ? (size_t)(2 * p.joined) * 128 * 128 * sizeof(float) + WS_ALIGN : 0;
