@@ -10,6 +10,10 @@
 // rows go to registers directly: no wave shares a weight, and the rows come from
 // L2.  Only experts with rows get workgroups: the j-th of the grid's row takes
 // the j-th such expert.
+//
+// Measured, bf16: 6 rows of 64 experts of 1408 x 2048 8.1 us, 4.3 TB/s with the launch;
+// 384 rows of all 64 experts 71 to 81 us, 4.6 to 5.2 TB/s of weights (a large copy: 5.4
+// to 6.0); 900 rows 88: the rows, which every workgroup reads from L2, begin to count.
 #pragma once
 
 #include "experts.hpp"
