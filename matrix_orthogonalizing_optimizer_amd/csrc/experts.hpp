@@ -295,8 +295,9 @@ template <int NA, int NB, int IA, int IB, typename P> __device__ __forceinline__
 }
 
 // One tile, of which the first 64 MA rows and 128 NA columns are computed (the
-// others lie outside C): MA, NA are the 32 x 32 blocks of a wave along M and N.
-template <int MODE, int T, int MA, int NA, bool DIRECT, bool SHORT, typename TI, typename TO>
+// others lie outside C): MA, NA are the 32 x 32 blocks of a wave along M and N.  SKIP:
+// waves whose blocks lie outside C leave their products out.
+template <int MODE, int T, int MA, int NA, bool DIRECT, bool SHORT, bool SKIP, typename TI, typename TO>
 __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const ExpertTile& t, u32x4 (*ring)[2 * T * 8]) {
   constexpr int NW = 8;
   constexpr bool AKM = MODE == EX_DW;      // A lies K-major
@@ -317,7 +318,9 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   static_assert(RPC >= 1 && BK * CR == OPS, "K-major stage");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wid / WGN, wn = wid % WGN;
+  // SKIP: the lower half's waves turned by two, so that those inside a narrow C are on
+  // all four SIMDs
+  const int wm = wid / WGN, wn = SKIP ? (wid + wm * (WGN / 2)) % WGN : wid % WGN;
   const int half = lane >> 5, l32 = lane & 31;
   const int row0 = t.bi * T, col0 = t.bj * T;
   int ks0, ks1;
@@ -459,7 +462,11 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   auto wait_frag = [&](auto pc) {
     experts_wait_frag<MA, NA, AKM ? (ES == 2 ? 2 : 0) : 1, BKM ? (ES == 2 ? 2 : 0) : 1>(pc);
   };
-  auto mfma_pair = [&](int p, int slot) { Mfma<TI>::run(acc[p / NA][p % NA], fa[slot][p / NA], fb[slot][p % NA]); };
+  const bool inside = row0 + wm * (32 * MA) < M && col0 + wn * WN < a.N;
+  auto mfma_pair = [&](int p, int slot) {
+    if (SKIP && !inside) return;
+    Mfma<TI>::run(acc[p / NA][p % NA], fa[slot][p / NA], fb[slot][p % NA]);
+  };
 
   if (nst > 0) {
     // ---- prologue: stages 0 and 1 in LDS (through registers: stage 1 in those)
@@ -589,12 +596,23 @@ void experts_kernel(const ExpertsArgs a) {
     // one operand's rows are shorter than a 16-byte piece
     constexpr int PER = 16 / (int)sizeof(TI);
     if ((MODE != EX_Y && a.N < PER) || (MODE == EX_DW ? a.M : a.K) < PER) {
-      experts_compute<MODE, T, 2, 1, false, true, TI, TO>(a, t, ring);
+      experts_compute<MODE, T, 2, 1, false, true, false, TI, TO>(a, t, ring);
       return;
     }
   }
-  if (low) experts_compute<MODE, T, 1, 1, DIRECT, false, TI, TO>(a, t, ring);
-  else experts_compute<MODE, T, 2, 1, DIRECT, false, TI, TO>(a, t, ring);
+  if constexpr (sizeof(TI) == 4) {
+    // fp32, bound by its products: where blocks of waves lie outside C (us with and without:
+    // 541 rows of 128 experts of 586 x 3008, input gradient 245 and 318; forward 29597 rows
+    // of 3 of 59 x 9472 423 and 642; but 4000 of 64 of 1408 x 2048, few of them outside,
+    // 463 and 392 with the branch in every tile)
+    if ((MODE == EX_DW ? a.M : t.count) - t.bi * T <= 32 || a.N - t.bj * T <= 96) {
+      if (low) experts_compute<MODE, T, 1, 1, DIRECT, false, true, TI, TO>(a, t, ring);
+      else experts_compute<MODE, T, 2, 1, DIRECT, false, true, TI, TO>(a, t, ring);
+      return;
+    }
+  }
+  if (low) experts_compute<MODE, T, 1, 1, DIRECT, false, false, TI, TO>(a, t, ring);
+  else experts_compute<MODE, T, 2, 1, DIRECT, false, false, TI, TO>(a, t, ring);
 }
 
 // Adds the partial tiles of a tile in order.  8 columns per thread, T * T / 2048
