@@ -39,11 +39,12 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   // the chip up to 24, and up to 64 rows at all (us, against the tiles: 64 experts of
   // 1408 x 2048, 384 rows 74 and 87, 900 rows 88 and 84; 8 of 14336 x 4096, 96 rows
   // 204 and 206; 8 of 1024 x 1024, 200 rows 10.6 and 13.7, 500 rows 18.1 and 15.7;
-  // fp32, 8 of 4096 x 4096, 200 rows 173 and 186, 300 rows 272 and 182; one of
-  // 768 x 768, 80 rows 10.3 and 11.2; odd widths: 8 of 1023 x 1025, 60 rows 14.9 and
-  // 17.1, 100 rows 23 and 18).
+  // fp32, 8 of 4096 x 4096, 150 rows 146 and 151, 190 rows 153 and 151, 64 of 1408 x
+  // 2048, 1024 rows 193 and 208, 1500 rows 212 and 200; one of 768 x 768, 80 rows 10.3
+  // and 11.2; odd widths: 8 of 1023 x 1025, 60 rows 14.9 and 17.1, 100 rows 23 and 18).
   const bool dear = dtype == MUON_F32 || (direct && some * ((out + 31) / 32) < 512);
-  p.few = pass == MUON_EXPERTS_FORWARD && some <= 65535 && (out + 15) / 16 * some <= 1 << 22 && (rows <= (dear ? 24 : 12) * some || rows <= 64);
+  p.few = pass == MUON_EXPERTS_FORWARD && some <= 65535 && (out + 15) / 16 * some <= 1 << 22 &&
+          (rows <= (dear ? 24 : 12) * some || rows <= 64);
   if (p.few) {
     p.tiles = (out + 15) / 16 * some;
     return p;
