@@ -243,23 +243,28 @@ class Plan:
     def slots(self):
         """What muon_step checks of the buffers the table asks for: (position in
         muon_param_ptrs, parameter) of each, their dtypes, their elements, and
-        their positions in the array of all pointers; and the places that stay
-        empty.  The optional update_out is in none of them."""
+        their positions in the array of all pointers; the places that stay
+        empty; and (position, parameter, dtype) of the buffers of parameters
+        without elements, which may be missing.  The optional update_out is in
+        none of them."""
         if self._slots is None:
             import torch
-            used, dtypes, numels, places, unused = [], [], [], [], []
+            used, dtypes, numels, places, unused, empty = [], [], [], [], [], []
             for i, (kind, dt, rows, cols, _split, _sd) in enumerate(self.table):
                 own = torch.float32 if dt == MUON_F32 else torch.bfloat16
                 kept, n = (torch.uint8, muon_adamw8_state_bytes(rows * cols)) if kind == MUON_KIND_ADAMW8 else (
                     torch.float32, rows * cols)
                 moments = [2] if kind == MUON_KIND_MUON else [3, 4]
                 for k in [0, 1] + moments:
+                    if rows * cols == 0:
+                        empty.append((k, i, own if k < 2 else kept))
+                        continue
                     used.append((k, i))
                     dtypes.append(own if k < 2 else kept)
                     numels.append(rows * cols if k < 2 else n)
                     places.append(6 * i + k)
                 unused += [(k, i) for k in (2, 3, 4) if k not in moments]
-            self._slots = used, dtypes, numels, places, unused
+            self._slots = used, dtypes, numels, places, unused, empty
         return self._slots
 
     def close(self):
@@ -365,22 +370,29 @@ def _check_moment8(name, t, numel, device_index=None):
 def _step_pointers(plan, lists, workspace, stream):
     """The array of a step's pointers where every buffer is what the table says,
     checked list by list (74 vectors: 0.25 us a buffer); None where one is not,
-    or is a raw pointer: muon_step then looks at each and says what is wrong."""
+    or is a raw pointer: muon_step then looks at each and says what is wrong.
+    workspace: as muon_step takes it; what can end this early is looked at first."""
     import torch
-    used, dtypes, numels, places, unused = plan.slots()
+    t = torch.Tensor
+    used, dtypes, numels, places, unused, empty = plan.slots()
+    if workspace is not None and not isinstance(workspace, (t, tuple, int)):
+        return None
     for k, i in unused:
         if lists[k][i] is not None:
             return None
-    t = torch.Tensor
     try:
         buffers = [lists[k][i] for k, i in used]
         if not buffers or not buffers[0].is_cuda:
             return None
         di = _device_index(stream)
+        if isinstance(workspace, t) and workspace.get_device() != di:
+            return None
+        for k, i, dtype in empty:
+            b = lists[k][i]
+            if b is not None and (b.dtype != dtype or t.numel(b) or t.get_device(b) != di):
+                return None
         if (list(map(operator.attrgetter("dtype"), buffers)) != dtypes or list(map(t.numel, buffers)) != numels
                 or list(map(t.get_device, buffers)).count(di) != len(buffers) or not all(map(t.is_contiguous, buffers))):
-            return None
-        if workspace is not None and workspace.get_device() != di:
             return None
         words = [0] * (6 * len(plan.table))
         for at, address in zip(places, map(t.data_ptr, buffers)):
@@ -393,8 +405,9 @@ def _step_pointers(plan, lists, workspace, stream):
 def muon_step(plan: Plan, params, grads, moms, exp_avgs, exp_avg_sqs, hp: MuonHparams, workspace,
               stream=None, update_outs=None) -> None:
     """One optimizer step; lists follow the plan's table order (None where a
-    buffer does not apply).  workspace: a device tensor (or pointer) of at
-    least muon_plan_workspace_bytes(plan) bytes."""
+    buffer does not apply, or for any of a parameter without elements).
+    workspace: a device tensor of at least muon_plan_workspace_bytes(plan)
+    bytes, or (address, bytes)."""
     n = len(plan.table)
     for name, lst in (("params", params), ("grads", grads), ("moms", moms), ("exp_avgs", exp_avgs),
                       ("exp_avg_sqs", exp_avg_sqs), ("update_outs", update_outs)):
