@@ -56,7 +56,9 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   const int64_t per = ((out + 255) / 256) * ((N + 255) / 256);  // weight gradient: tiles of an expert
   // an expert with more rows than a CU sums over all is cut
   const int64_t share = (rows + 63) / 64 * per / 256;
-  p.chunk = 64 * std::max<int64_t>(8, share);
+  // (at most 2^29: the kernels add it to an expert's rows, up to 2^30, in 32 bits)
+  constexpr int64_t MAX_CHUNK = (int64_t)1 << 29;
+  p.chunk = std::min(MAX_CHUNK, 64 * std::max<int64_t>(8, share));
   // 256 x 256 tiles where there is about one for every CU.  us, against tiles of 128:
   // forward 4096 rows of 8 experts of 1408 x 2048, 120 tiles 43 and 34; weight
   // gradient 4096 rows of 8 of 512 x 1024, 64 tiles 34 and 25; from about 260 on
@@ -96,7 +98,7 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
         }
       }
     }
-    p.chunk = bk * unit;
+    p.chunk = std::min(MAX_CHUNK, bk * unit);
     p.tiles = (experts + rows / p.chunk) * mine;
     p.joined = rows / p.chunk * mine;
     p.bytes = p.joined ? (size_t)(2 * p.joined) * 128 * 128 * sizeof(float) + WS_ALIGN : 0;
