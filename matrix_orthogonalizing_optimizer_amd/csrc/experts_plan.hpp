@@ -24,6 +24,26 @@ struct ExpertsPlan {
   size_t bytes;
 };
 
+// The few-row kernel's shape: tiles of 16 rows that a workgroup takes at a time,
+// with two of them two groups of 16 channels; whole: K a multiple of a step.
+// Two tiles of rows and two groups of channels read the rows half as often, and
+// leave enough workgroups where the channels of all experts make 512 (us, one
+// of each against two: 64 experts of 1408 x 2048, 384 rows 82 and 76, 1024 rows
+// 131 and 103, before experts of at most 16 rows left the second tile out; but 64
+// rows, one an expert, 38 and 39, 16 rows of one expert of 768 x 768 6.0 and 7.5).
+// Where they do not, 4 tiles of rows from 8 rows an expert up (256 rows over 16
+// experts of 512 x 513: 25 and 14 us).
+struct ExpertsFewShape {
+  int row_tiles;
+  bool whole;
+};
+inline ExpertsFewShape experts_few_shape(int64_t rows, int64_t experts, int64_t out, int64_t in, int32_t dtype) {
+  const int64_t some = std::min(experts, rows);
+  const bool whole = in % (dtype == MUON_F32 ? 16 : 32) == 0;
+  if (rows > 2 * some && some * ((out + 31) / 32) >= 512) return {2, whole};
+  return {rows <= 8 * some ? 1 : 4, whole};
+}
+
 // direct: all operands are bf16 rows of whole 16-byte pieces.  out and in are 2^21
 // at most, so that no product here overflows.
 inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t out, int64_t in, int32_t dtype,

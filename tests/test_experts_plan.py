@@ -1,12 +1,15 @@
 """The planner of the products grouped by expert (csrc/experts_plan.hpp) in a
 host program built with g++: what it plans for any size that the entry points
-accept is sound, and fits the kernels' 32-bit arguments."""
+accept is sound and fits the kernels' 32-bit arguments, and the sizes of
+tests/test_gpu_experts_few.py still take the kernels they are there for."""
 import os
 import random
 import shutil
 import subprocess
 
 import pytest
+
+from tests import experts_cases as C
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "matrix_orthogonalizing_optimizer_amd", "csrc")
@@ -53,7 +56,7 @@ def test_plans_fit_the_kernels(ask):
     workspace has room for."""
     asked = list(sizes(20000, 1)) + LIMITS
     seen = {}
-    for q, (kernel, tile, splits, tiles, joined, chunk, cap, nbytes) in zip(asked, ask(asked)):
+    for q, (kernel, tile, splits, tiles, joined, chunk, cap, nbytes, _, _) in zip(asked, ask(asked)):
         which, rows, experts, out, in_, dtype, direct = q
         if max(tiles * splits, joined * (tile * tile // 2048)) > 1 << 22:
             continue  # refused
@@ -88,3 +91,28 @@ def test_plans_fit_the_kernels(ask):
         else:
             assert tile == 128, q
     assert len(seen) == 7, seen
+
+
+def test_few_row_cases_take_their_kernels(ask):
+    """Whole 16-byte pieces or not: the cases run both."""
+    for direct in (0, 1):
+        cases = [c for c in C.FEW if not direct or (c[4] == BF16 and c[3] % 8 == 0)]
+        for c, p in zip(cases, ask([(FORWARD, *c[:5], direct) for c in cases])):
+            assert p[0] == "few" and p[8:] == c[5], (c, direct, p)
+
+
+def test_every_few_row_kernel_has_a_case():
+    have = {(c[4],) + c[5] for c in C.FEW}
+    assert have == {(d, t, w) for d in (F32, BF16) for t in (1, 2, 4) for w in (0, 1)}
+    two = [c for c in C.FEW if c[5][0] == 2]
+    for dtype, piece in ((F32, 4), (BF16, 8)):
+        mine = [c for c in two if c[4] == dtype]
+        # the second group of channels whole, cut and outside; rows shorter than a piece
+        assert {(0 if c[2] % 32 == 0 else 1 if c[2] % 32 > 16 else 2) for c in mine} == {0, 1, 2}
+        assert any(c[3] < piece for c in mine)
+        # an expert with several rounds of two tiles, one with 17 to 32 rows, one with up to 16
+        for c in mine:
+            counts = C.counts(c)
+            assert sum(counts) == c[0] and len(counts) == c[1]
+        assert any(max(C.counts(c)) > 64 for c in mine)
+        assert any(any(17 <= n <= 32 for n in C.counts(c)) and any(0 < n <= 16 for n in C.counts(c)) for c in mine)
