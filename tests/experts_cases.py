@@ -53,3 +53,12 @@ def counts(case):
     for _ in range(rows - sum(some)):
         n[rng.choice(rest)] += 1
     return n
+
+# Products that take the large tiles: pass, rows, experts, out, in
+FORWARD, WEIGHT, INPUT = 0, 1, 2
+LARGE = [
+    (FORWARD, 9000, 12, 5125, 1288), (FORWARD, 20000, 30, 1157, 264), (FORWARD, 30000, 9, 513, 72),
+    (FORWARD, 9000, 12, 5128, 1288), (INPUT, 9000, 12, 5128, 1288), (WEIGHT, 9000, 12, 5128, 1288),
+    (FORWARD, 20000, 30, 1160, 2056), (INPUT, 20000, 30, 1160, 2056), (WEIGHT, 20000, 30, 1160, 2056),
+    (FORWARD, 5000, 3, 5128, 5144), (INPUT, 5000, 3, 5128, 5144), (WEIGHT, 5000, 3, 5128, 5144),
+]

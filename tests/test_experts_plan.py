@@ -116,3 +116,8 @@ def test_every_few_row_kernel_has_a_case():
             assert sum(counts) == c[0] and len(counts) == c[1]
         assert any(max(C.counts(c)) > 64 for c in mine)
         assert any(any(17 <= n <= 32 for n in C.counts(c)) and any(0 < n <= 16 for n in C.counts(c)) for c in mine)
+
+
+def test_large_cases_take_the_large_tiles(ask):
+    for c, p in zip(C.LARGE, ask([(*c, BF16, 1) for c in C.LARGE])):
+        assert p[0] == "big", (c, p)
