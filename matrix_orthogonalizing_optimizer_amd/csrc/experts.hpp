@@ -7,15 +7,16 @@
 //
 // The offsets lie on the device, so the host does not know how many rows an
 // expert has.  EX_Y and EX_DX launch as many workgroups as any offsets can
-// need (rows / T + experts tile rows); each finds its tile from a prefix sum
+// need (rows / 128 + experts tile rows); each finds its tile from a prefix sum
 // over the experts' tile rows (experts_tile), and those past the last tile
 // end at once.  EX_DW has a workgroup per tile and unit of at most `chunk` rows
 // of an expert (one unit for an expert without rows).  Offsets are clamped to 0 .. rows, so no value of theirs
 // leads outside the operands.
 //
-// A workgroup of 8 waves owns a T x T tile of C (T = 128: 64 x 32 outputs per wave,
-// two workgroups per CU) and walks K in stages of 128 bytes per row: 64 values of bf16, 32 of fp32.  Two stages live
-// in LDS.  v_mfma_f32_32x32x16_bf16, or v_mfma_f32_32x32x2_f32.
+// A workgroup of 8 waves owns a 128 x 128 tile of C (64 x 32 outputs per wave,
+// two workgroups per CU) and walks K in stages of 128 bytes per row: 64 values of
+// bf16, 32 of fp32.  Two stages live in LDS.  v_mfma_f32_32x32x16_bf16, or
+// v_mfma_f32_32x32x2_f32.
 //
 // An operand lies row-major (K contiguous: x and w of EX_Y, dy of EX_DX) or
 // K-major (w of EX_DX, both of EX_DW).  K-major bf16 fragments come out of LDS
@@ -44,6 +45,7 @@
 namespace muon {
 
 enum : int { EX_Y = 0, EX_DW = 1, EX_DX = 2 };
+constexpr int EXPERTS_T = 128;  // edge of a tile
 
 // First row of expert e and their number.
 struct ExpertRows {
@@ -98,10 +100,11 @@ __device__ __forceinline__ void experts_place(int w, int tilesM, int tilesN, int
 
 // The tile of workgroup b; false if there is none.  JOIN: the b-th tile that was
 // left in parts.
-//   forward, input gradient: tiles of T rows of the experts; all in `splits` parts
+//   forward, input gradient: tiles of 128 rows of the experts; all in `splits` parts
 //   weight gradient: units of at most `chunk` rows of an expert; experts of
 //   several units leave parts
-template <int MODE, int T, bool JOIN> __device__ __forceinline__ bool experts_tile(const ExpertsArgs& a, int b, ExpertTile& t) {
+template <int MODE, bool JOIN> __device__ __forceinline__ bool experts_tile(const ExpertsArgs& a, int b, ExpertTile& t) {
+  constexpr int T = EXPERTS_T;
   constexpr bool DW = MODE == EX_DW;
   const int lane = threadIdx.x & 63;
   const int tiles = DW ? a.tilesM * a.tilesN : a.tilesN;  // of a unit, or of a tile row
@@ -294,11 +297,13 @@ template <int NA, int NB, int IA, int IB, typename P> __device__ __forceinline__
   }
 }
 
-// One tile, of which the first 64 MA rows and 128 NA columns are computed (the
-// others lie outside C): MA, NA are the 32 x 32 blocks of a wave along M and N.  SKIP:
-// waves whose blocks lie outside C leave their products out.
-template <int MODE, int T, int MA, int NA, bool DIRECT, bool SHORT, bool SKIP, typename TI, typename TO>
-__device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const ExpertTile& t, u32x4 (*ring)[2 * T * 8]) {
+// One tile, of which the first 64 MA rows are computed (the others lie outside
+// C): MA is the number of 32 x 32 blocks of a wave along M.  SKIP: waves whose
+// blocks lie outside C leave their products out.
+template <int MODE, int MA, bool DIRECT, bool SHORT, bool SKIP, typename TI, typename TO>
+__device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const ExpertTile& t, u32x4 (*ring)[2 * EXPERTS_T * 8]) {
+  constexpr int T = EXPERTS_T;
+  constexpr int NA = 1;                    // 32 x 32 blocks of a wave along N
   constexpr int NW = 8;
   constexpr bool AKM = MODE == EX_DW;      // A lies K-major
   constexpr bool BKM = MODE != EX_Y;       // B lies K-major
@@ -375,7 +380,7 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   };
   auto copy_b = [&](int q, int v, int ks) {
     if constexpr (BKM) copy_k_major(B, a.ldb, a.N, tb, OPS, q, v, ks);
-    else if (128 * NA >= T || wid * (8 * NQ) < 128 * NA) copy_row_major(Brow, a.ldb, rows_b, OPS, q, v, ks);
+    else copy_row_major(Brow, a.ldb, rows_b, OPS, q, v, ks);
   };
 
   // ---- the same chunks through registers
@@ -582,12 +587,13 @@ __device__ __forceinline__ void experts_compute(const ExpertsArgs& a, const Expe
   });
 }
 
-template <int MODE, int T, bool DIRECT, typename TI, typename TO>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(T == 128 ? 4 : 2, T == 128 ? 4 : 2)))
+template <int MODE, bool DIRECT, typename TI, typename TO>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void experts_kernel(const ExpertsArgs a) {
+  constexpr int T = EXPERTS_T;
   __shared__ u32x4 ring[2][2 * T * 8];
   ExpertTile t;
-  if (!experts_tile<MODE, T, false>(a, blockIdx.x, t)) return;
+  if (!experts_tile<MODE, false>(a, blockIdx.x, t)) return;
   // a tile at C's edge of which half or less is inside computes that half: 64
   // experts of 1408 x 2048, 49152 rows lose a tenth of their work to edges
   // instead of a quarter
@@ -596,7 +602,7 @@ void experts_kernel(const ExpertsArgs a) {
     // one operand's rows are shorter than a 16-byte piece
     constexpr int PER = 16 / (int)sizeof(TI);
     if ((MODE != EX_Y && a.N < PER) || (MODE == EX_DW ? a.M : a.K) < PER) {
-      experts_compute<MODE, T, 2, 1, false, true, false, TI, TO>(a, t, ring);
+      experts_compute<MODE, 2, false, true, false, TI, TO>(a, t, ring);
       return;
     }
   }
@@ -606,21 +612,21 @@ void experts_kernel(const ExpertsArgs a) {
     // of 3 of 59 x 9472 423 and 642; but 4000 of 64 of 1408 x 2048, few of them outside,
     // 463 and 392 with the branch in every tile)
     if ((MODE == EX_DW ? a.M : t.count) - t.bi * T <= 32 || a.N - t.bj * T <= 96) {
-      if (low) experts_compute<MODE, T, 1, 1, DIRECT, false, true, TI, TO>(a, t, ring);
-      else experts_compute<MODE, T, 2, 1, DIRECT, false, true, TI, TO>(a, t, ring);
+      if (low) experts_compute<MODE, 1, DIRECT, false, true, TI, TO>(a, t, ring);
+      else experts_compute<MODE, 2, DIRECT, false, true, TI, TO>(a, t, ring);
       return;
     }
   }
-  if (low) experts_compute<MODE, T, 1, 1, DIRECT, false, false, TI, TO>(a, t, ring);
-  else experts_compute<MODE, T, 2, 1, DIRECT, false, false, TI, TO>(a, t, ring);
+  if (low) experts_compute<MODE, 1, DIRECT, false, false, TI, TO>(a, t, ring);
+  else experts_compute<MODE, 2, DIRECT, false, false, TI, TO>(a, t, ring);
 }
 
-// Adds the partial tiles of a tile in order.  8 columns per thread, T * T / 2048
+// Adds the partial tiles of a tile in order.  8 columns per thread, WGS
 // workgroups per tile.  Parts without stages were written as zeros.
-template <int MODE, int T, typename TO> __global__ __launch_bounds__(256) void experts_join_kernel(const ExpertsArgs a) {
-  constexpr int WGS = T * T / 2048;
+template <int MODE, typename TO> __global__ __launch_bounds__(256) void experts_join_kernel(const ExpertsArgs a) {
+  constexpr int T = EXPERTS_T, WGS = T * T / 2048;
   ExpertTile t;
-  if (!experts_tile<MODE, T, true>(a, (int)(blockIdx.x / WGS), t)) return;
+  if (!experts_tile<MODE, true>(a, (int)(blockIdx.x / WGS), t)) return;
   const int in = (int)(blockIdx.x % WGS) * 2048 + threadIdx.x * 8;  // first value within the tile
   const int r = t.bi * T + in / T, c = t.bj * T + in % T;
   if (r >= (MODE == EX_DW ? a.M : t.count) || c >= a.N) return;
