@@ -223,3 +223,28 @@ def test_graph_replays_and_two_streams():
     torch.cuda.synchronize()
     for i, (which, o) in enumerate(many):
         verify(which, o, f"stream {i}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("experts,out,in_", [(65535, 8, 16), (65536, 8, 16), (65536, 5, 9)])
+def test_as_many_experts_as_there_may_be(experts, out, in_, dtype):
+    """2^16 experts, most of them with a row or none, a few with many."""
+    print("experts at their limit", experts, out, in_, dtype, flush=True)
+    rows = 70001
+    gen = torch.Generator(device=dev()).manual_seed(9)
+    n = torch.ones(experts, dtype=torch.int64, device=dev())
+    n[torch.randint(0, experts, (30000,), generator=gen, device=dev())] = 0
+    n[experts // 2], n[experts - 1] = 20000, 300
+    off = torch.cat([n.new_zeros(1), n.cumsum(0)])
+    assert off[-1] < rows
+    mine = torch.repeat_interleave(torch.arange(experts, device=dev()), n)
+    live = mine.numel()
+    off = off.to(torch.int32)
+    x, w, dy = whole(gen, (rows, in_), dtype), whole(gen, (experts, out, in_), dtype), whole(gen, (rows, out), dtype)
+    y = mo.muon_experts_forward(x, w, off, y=torch.full((rows, out), 77.0, device=dev()))
+    assert torch.equal(y[:live], (w[mine].double() * x[:live].double().unsqueeze(1)).sum(2).float()) and (y[live:] == 77).all()
+    dx = mo.muon_experts_input_grad(dy, w, off, dx=torch.full((rows, in_), 77.0, device=dev()))
+    assert torch.equal(dx[:live], (w[mine].double() * dy[:live].double().unsqueeze(2)).sum(1).float()) and (dx[live:] == 77).all()
+    dw = mo.muon_experts_weight_grad(dy, x, off, dtype=F32)
+    each = dy[:live].double().unsqueeze(2) * x[:live].double().unsqueeze(1)
+    assert torch.equal(dw, torch.zeros(experts, out, in_, dtype=torch.float64, device=dev()).index_add_(0, mine, each).float())
