@@ -208,8 +208,8 @@ typedef struct {
  * Storage: the codes of ceil(numel / 256) whole blocks, then a 16-bit offset
  * per block, then up to the next multiple of 16 bytes.  All zero bytes are
  * zero moments (a new parameter's).  Codes behind the last element are left as
- * they are.  Buffers of one parameter follow each other without gaps at
- * 16-byte alignment.
+ * they are.  The size is a multiple of 16 bytes, so buffers that follow each
+ * other without gaps stay aligned.
  * adam_beta1 and adam_beta2 are in [0, 1) for such parameters.
  *
  * muon_adamw8_state_bytes: bytes of one moment (host only).

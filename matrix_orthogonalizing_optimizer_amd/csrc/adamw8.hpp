@@ -30,9 +30,10 @@
 // element against 22 with fp32 moments.  A wave owns blocks of 256 elements, 4
 // per lane: one load or store instruction per array and block, and the block's
 // largest value is a reduction over the wave's registers.  128256 x 4096 in bf16:
-// 892 us, 5.9 TB/s (3.2 GB read and 2.1 GB written by the counters, what it cannot
-// do without); 50257 x 768 and 74 vectors 66 us, 5.9 TB/s with what the caches keep of
-// the step before.
+// 902 us a call, 5.8 TB/s; traced over 23 calls in a row 897 to 1006 us, 944 on
+// average (3.2 GB read and 2.1 GB written by the counters, what it cannot do
+// without).  50257 x 768 and 74 vectors: 66 us, 5.9 TB/s with what the caches keep
+// of the step before.
 #pragma once
 
 #include "consts.hpp"
@@ -309,7 +310,9 @@ template <bool EXACT, bool STREAM> __global__ __launch_bounds__(256) void adamw8
 }
 
 // fp32 values -> codes (rounded as in a step of number `step`), and back.  A
-// wave per block.
+// wave per block, element by element, as they are for conversions now and then:
+// 128256 x 4096 values packed in 530 us (5.0 TB/s), unpacked in 955 (2.8 TB/s: a
+// lane's 4 values go out in 4 stores), where a large copy's rate would take 438.
 template <bool SECOND> __global__ __launch_bounds__(256) void adamw8_pack_kernel(const Adamw8PackArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t nblk = adamw8_blocks(a.numel);

@@ -30,11 +30,20 @@
 // weight gradient) go to workgroups of their own, which leave partial tiles in
 // the workspace; experts_join_kernel adds those in order.
 //
-// Measured (kernels alone): fp32 weight gradient, 8192 rows of 8 experts of 2048 x
-// 2048 548 us, 125 of the 154 TFLOP/s of a large fp32 product; 3001 rows of 7 of
-// 513 x 767 47 us and 8 to join, 50 TFLOP/s, bound by 480 workgroups of 14 us each on 256
-// CUs; bf16 input gradient at any address, 1531 rows of 13 of 701 x 301 14 us and 4 to
-// join, bound by the latency of its 11 stages and two launches.
+// Measured: fp32, 8192 rows of 8 experts of 2048 x 2048, weight gradient 555 us, 124
+// of the 154 TFLOP/s of a large fp32 product, forward 657, input gradient 676; weight
+// gradient of 3001 rows of 7 of 513 x 767 51 us a call (kernels traced one by one 46
+// and 8 to join), bound by 480 workgroups of unequal length, up to 14 us, dealt in
+// table order on 256 CUs, and by 31 MB of partial tiles; bf16 input gradient at any
+// address, 1531 rows of 13 of 701 x 301 17 us a call (14 and 4 to join): K's 11 stages
+// in two parts make 108 workgroups on 256 CUs, bound by the latency of their 6 stages
+// through registers and by two launches.  With one odd width large bf16 products
+// come here too: 49152 rows of 64 experts of 1407 x 2048, input gradient 489 us,
+// weight gradient 522 (302 and 342 with 1408 in the large tiles); of 1408 x 2047
+// forward 566, input gradient 484, weight gradient 529.
+// A workgroup scans the offsets of all experts for its tile, so that part grows with
+// the square of their number: weight gradient of 40000 rows of 2048 experts of 512 x
+// 512 2.1 ms, of 4096 7.4 ms, where the results' bytes alone would take 0.2 and 0.4.
 #pragma once
 
 #include "device_common.hpp"

@@ -22,14 +22,21 @@
 // instead of 310 us.)
 //
 // Measured at 49152 rows of 64 experts of 1408 x 2048, where a large library product's
-// 1.36 PFLOP/s would take 208 us: forward 314 us, input gradient 287, weight
-// gradient 331, with the matrix pipes busy 48, 54 and 42% at 1.9 to 2.05 GHz. In a
-// stage the reads and copies of LDS take as many cycles as the matrix
-// instructions (2048 of a CU's 128 bytes a cycle for operands that all lie K-major); the
-// experts' last tiles are half empty. 16384 rows of 8 experts of 14336 x 4096: 1560 to
-// 1640 us, 1.17 to 1.23 PFLOP/s, bound by power (busy 67 to 70%, the clock falls to 1.34 to
-// 1.74 GHz). Storing a tile by exchanges between lanes instead of through
-// LDS changed nothing (forward 314 and 317).
+// 1.36 PFLOP/s would take 208 us: forward 322 us a call, input gradient 302, weight
+// gradient 342, with the matrix pipes busy 44 to 48, 49 to 55 and 41 to 42% at 1.8 to
+// 2.06 GHz; traced over 23 calls in a row, without lists and sums, 363 (317 to 395),
+// 329 (286 to 358) and 353 us (337 to 367).  16384 rows of 8 experts of 14336 x 4096:
+// 1646 us a call, 1.17 PFLOP/s; 1713 traced (1608 to 1961), bound by power (busy 67 to
+// 70%, the clock falls to 1.34 to 1.74 GHz).  In a stage the reads and copies of LDS
+// take as many cycles as the matrix instructions (2048 of a CU's 128 bytes a cycle for
+// operands that all lie K-major) in both; what the first has more of is tiles' ends,
+// one in 32, 22 or 12 stages instead of 64, half-empty last tiles (8%) and the last
+// round of workgroups.  A weight gradient that is added to reads C in an epilogue
+// whose end the next tile waits for: 424 us (fp32 C 496, written 390).  Storing a tile by
+// exchanges between lanes instead of through LDS changed nothing (forward 314 and 317).
+// The list takes 5 us at 64 experts (weight gradient 8), 7 at 1024 and 11 at 2048; the
+// weight gradient's, which compares every unit with every other, 11 at 256 experts
+// and 113 at 1024.
 #pragma once
 
 #include "experts.hpp"

@@ -11,9 +11,13 @@
 // L2.  Only experts with rows get workgroups: the j-th of the grid's row takes
 // the j-th such expert.
 //
-// Measured, bf16: 6 rows of 64 experts of 1408 x 2048 8.1 us, 4.3 TB/s with the launch;
-// 384 rows of all 64 experts 71 to 81 us, 4.6 to 5.2 TB/s of weights (a large copy: 5.4
-// to 6.0); 900 rows 88: the rows, which every workgroup reads from L2, begin to count.
+// Measured, bf16: 6 rows of 64 experts of 1408 x 2048 9.0 to 10.2 us a call (the kernel
+// 8.0 on average, 7.6 at least: 64 KB of weights a workgroup, two trips to HBM in
+// series for each of its waves); 384 rows of all 64 experts 71 us a call, 5.2 TB/s of
+// weights (a large copy: 5.4 to 6.0; the kernel traced over 23 calls 77 to 117 us, 81 on
+// average); 900 rows 92: the rows, which every workgroup reads from L2, begin to count.
+// An expert's rows are one loop: 384 rows that all go to one of the 64 experts take 95
+// us instead of 73.
 #pragma once
 
 #include "experts.hpp"

@@ -62,6 +62,10 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   // fp32, 8 of 4096 x 4096, 150 rows 146 and 151, 190 rows 153 and 151, 64 of 1408 x
   // 2048, 1024 rows 193 and 208, 1500 rows 212 and 200; one of 768 x 768, 80 rows 10.3
   // and 11.2; odd widths: 8 of 1023 x 1025, 60 rows 14.9 and 17.1, 100 rows 23 and 18).
+  // These rows are spread over the experts; the counts lie on the device, so the rule
+  // cannot see them.  All of them on one expert of 64 of 1408 x 2048 (us, and the same
+  // rows spread): 384 rows 95 and 73; 768 rows 190 and 82, where the tiles take 23 for
+  // 769; fp32 1536 rows 723 and 220, the tiles 144 for 1537.
   const bool dear = dtype == MUON_F32 || (direct && some * ((out + 31) / 32) < 512);
   p.few = pass == MUON_EXPERTS_FORWARD && some <= 65535 && (out + 15) / 16 * some <= 1 << 22 &&
           (rows <= (dear ? 24 : 12) * some || rows <= 64);
@@ -84,7 +88,10 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
   // gradient 4096 rows of 8 of 512 x 1024, 64 tiles 34 and 25; from about 260 on
   // ahead: forward 16384 rows of 8 of 4096 x 4096 497 and 587, weight gradient 1024
   // rows of 2 of 4096 x 4096, 512 tiles 46 and 61, 4096 rows of 64 of 1408 x 2048 103
-  // and 176 (but the forward product of the latter 120 and 102).
+  // and 176 (but the forward product of the latter 120 and 102).  The lists hold 2048
+  // experts, in the weight gradient experts and units: past that come the tiles of 128,
+  // whose search for a tile is dear by then (40000 rows of 512 x 512: weight gradient at
+  // 1900 experts 612, at 2048 2110; forward at 2048 257, at 4096 1357).
   p.big = direct && tiles(256) >= 240 && experts + (dw ? rows / p.chunk : 0) <= 2048;
   if (p.big) {
     p.tile = 256;
