@@ -73,9 +73,9 @@ inline ExpertsPlan experts_plan(int pass, int64_t rows, int64_t experts, int64_t
     p.tiles = (out + 15) / 16 * some;
     return p;
   }
-  // tile rows that the offsets need at most, and those they need when every
-  // expert's last tile is half full
-  auto most = [&](int64_t t) { return dw ? experts * ((out + t - 1) / t) : rows / t + some; };
+  // forward, input gradient: tile rows that the offsets need at most; tiles when
+  // every expert's last tile row is half full
+  auto most = [&](int64_t t) { return rows / t + some; };
   auto tiles = [&](int64_t t) { return (dw ? experts * ((out + t - 1) / t) : rows / t + (some + 1) / 2) * ((N + t - 1) / t); };
   const int64_t per = ((out + 255) / 256) * ((N + 255) / 256);  // weight gradient: tiles of an expert
   // an expert with more rows than a CU sums over all is cut
